@@ -36,6 +36,7 @@ extern "C" {
 
 #define WFST_LP_F32 0      /* log_prob elements are binary32                          */
 #define WFST_LP_F16 1      /* log_prob elements are binary16, widened exactly to fp32 */
+#define WFST_LP_BF16 2     /* bfloat16: operands of the operators around the search only */
 
 /* out_meta[b * 3 + 2] bits (section 7 of the page): a non-zero value means the
  * lane's result may be degraded; such a lane also reports ok = 0. */
@@ -561,6 +562,133 @@ int wfst_decoder_profile(wfst_decoder_t d, int32_t enable);
  * the last decode was not profiled), WFST_EDEVICE.
  */
 int wfst_decoder_kernel_times(wfst_decoder_t d, double *out, int32_t n);
+
+/*
+ * Operators around the search: what makes log_prob from a model's last hidden
+ * states, and the draw of tokens from scores. They take no decoder. Each call is
+ * asynchronous: it is ordered on the caller's HIP stream (null: the null stream
+ * of the operands' device) and returns without waiting for it, so operands must
+ * stay valid until the stream has passed it. None allocates device memory or
+ * synchronises (but wfst_layer_create / _release), so they may be captured into
+ * a HIP graph, which then reads and writes the same buffers at every replay.
+ * They use no workspace: calls on different streams run at once. Element types
+ * are WFST_LP_F32, _F16 and _BF16; a result is rounded to its type once, to
+ * nearest even. Tensors are rows `stride` elements apart (stride >= the row's
+ * length, any alignment of whole elements) on one device, which need not be the
+ * current one; the calling thread's current device is left as it was.
+ *
+ * lengths (device int32 [rows / T], or null): row r = b * T + t holds data iff
+ * t < lengths[b]; the other rows are not read and their outputs left as they
+ * were. With null every row holds data and T is ignored.
+ */
+
+typedef struct wfst_layer_s *wfst_layer_t;
+
+/*
+ * An output layer with 4-bit weights and group scales, as device arrays:
+ *   y[m, n] = bias[n] + sum_g scales[n, g] * sum_{k in g} (q[n, k] - zeros[n, g]) * x[m, k]
+ *  in_features   K, in [1, 2^24].
+ *  out_features  N, in [1, 2^24].
+ *  group_size    input features of one group, a multiple of 32; the last group of
+ *                a row may be shorter; G = ceil(K / group_size) groups.
+ *  scale_dtype   element type of scales.
+ *  weights       uint8 [N, ceil(K / 2)]: q of feature 2i in the low half of byte
+ *                i, of feature 2i + 1 in the high half (ignored past K).
+ *  scales        [N, G] of scale_dtype.
+ *  zeros         uint8 [N, G], the low 4 bits count; null: 8 everywhere.
+ *  bias          float [N]; null: 0.
+ */
+typedef struct wfst_layer_desc {
+    int32_t in_features;
+    int32_t out_features;
+    int32_t group_size;
+    int32_t scale_dtype;
+    const void *weights;
+    const void *scales;
+    const void *zeros;
+    const void *bias;
+} wfst_layer_desc;
+
+/*
+ * Lay a layer's arrays out for the kernels, in memory of its own on `device`
+ * (N * K / 2 bytes, K and N rounded up to 128 and 16, and the scales, zeros and
+ * bias). Ordered on `stream`, which it synchronises: the source arrays may be
+ * freed when the call returns. Release with wfst_layer_release, which waits for
+ * the device; graphs that captured the layer must not be replayed after it.
+ * Errors: WFST_EINVAL, WFST_ENOMEM, WFST_EDEVICE.
+ */
+int wfst_layer_create(const wfst_layer_desc *d, int device, void *stream, wfst_layer_t *out);
+int wfst_layer_release(wfst_layer_t layer);   /* null is a no-op */
+
+/*
+ * out[r, :] = the layer's y for hidden state x[r, :], rows in [0, 2^20 - 16].
+ * q - zeros is exact, products and a group's sums are binary32 sums of products
+ * of exact values (a binary32 x enters as a sum of two binary16 values, off by at
+ * most 2^-24 of itself or 2^-38 of the largest finite |x| among its 128
+ * neighbours); infinities and NaN in x go where the formula takes them.
+ * out must not overlap x. Errors: WFST_EINVAL, WFST_EDEVICE.
+ */
+int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_t x_stride, int32_t rows,
+                      const int32_t *lengths, int32_t T, void *out, int32_t out_dtype, int64_t out_stride,
+                      void *stream);
+
+/*
+ * out[r, :] = log_softmax(scale * x[r, :] + bias): the search's log_prob rows
+ * from logits, with an acoustic scale and a bias per label (minus a log-prior, a
+ * blank penalty, -inf for a label that may not be emitted). V in [1, 2^24]; bias
+ * is a device float [V] or null. Statistics are binary32. A row whose entries
+ * are all -inf stays -inf; a row with a NaN or +inf becomes NaN. out may be x
+ * itself (same element type and stride), otherwise it must not overlap x.
+ * Errors: WFST_EINVAL, WFST_EDEVICE.
+ */
+int wfst_log_softmax(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, float scale,
+                     const float *bias, const int32_t *lengths, int32_t T, void *out, int32_t out_dtype,
+                     int64_t out_stride, void *stream);
+
+/*
+ * Settings of a draw, for every row or, where a device array is given, one value
+ * a row. Rules apply in this order, ties always to the lowest index:
+ *  temperature  T >= 0, finite. 0: the largest score (greedy; the other rules and
+ *               u have no say). In an array, a value that is not > 0 is 0.
+ *  top_k        keep the top_k largest; 0: all. In an array, <= 0 is 0.
+ *  top_p        in [0, 1]: of these keep the fewest largest whose mass
+ *               exp((x - max) / T) reaches top_p of theirs, at least one; 1: all.
+ *               In an array, a value that is not < 1 is 1, one below 0 is 0.
+ *  min_p        in [0, 1]: of these keep the ones with mass >= min_p (the largest
+ *               score has mass 1); 0: all. In an array, a value that is not > 0
+ *               is 0 and one above 1 is 1.
+ */
+typedef struct wfst_sample_config {
+    float temperature;
+    int32_t top_k;
+    float top_p;
+    float min_p;
+    const void *temperatures;
+    const void *top_ks;
+    const void *top_ps;
+    const void *min_ps;
+} wfst_sample_config;
+
+/*
+ * Draw one token of each row of scores (logits or log-probabilities).
+ *  u             device float [rows]: uniform random numbers in [0, 1), the
+ *                caller's; below 0 or NaN counts as 0, 1 and above as just below 1.
+ *  out_tokens    device int32 [rows]: the first kept label, in index order, whose
+ *                running mass exceeds u times the kept mass; -1 for an empty row.
+ *  out_log_probs device float [rows] or null: its log-probability among the kept
+ *                (0 when greedy, -inf for an empty row).
+ *  out_kept      device int32 [rows] or null: the number of labels kept.
+ * Labels with score -inf or NaN are never drawn nor kept; a row of nothing else
+ * is empty. +inf scores leave only each other, with equal masses. Masses are
+ * computed in binary64 and added as multiples of 2^-52 or of V * 2^-62 rounded up
+ * to a power of two, whichever is larger: results do not depend on any order of
+ * addition, and labels whose mass rounds to 0 are not drawn. V in [1, 2^24].
+ * Outputs must not overlap each other or the inputs.
+ * Errors: WFST_EINVAL, WFST_EDEVICE.
+ */
+int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, const float *u,
+                const wfst_sample_config *cfg, const int32_t *lengths, int32_t T, int32_t *out_tokens,
+                float *out_log_probs, int32_t *out_kept, void *stream);
 
 #ifdef __cplusplus
 }

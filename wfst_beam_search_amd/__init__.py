@@ -18,7 +18,7 @@ from types import SimpleNamespace
 import numpy as np
 
 __all__ = ["Graph", "Decoder", "DecodeResult", "WfstError", "library_path", "load_library", "decode_noalloc",
-           "EXPORTED_SYMBOLS", "LP_F32", "LP_F16"]
+           "EXPORTED_SYMBOLS", "LP_F32", "LP_F16", "OutputLayer", "log_softmax", "sample", "SampleResult"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libwfst_mi355x.so")
@@ -29,7 +29,8 @@ EXPORTED_SYMBOLS = ("wfst_last_error", "wfst_graph_upload", "wfst_graph_release"
                     "wfst_decoder_stats", "wfst_decoder_mem_stats", "wfst_decoder_step_stats", "wfst_decoder_profile",
                     "wfst_decoder_kernel_times", "wfst_create_stream", "wfst_advance_chunk",
                     "wfst_finalize_stream", "wfst_finalize_streams", "wfst_create_streams", "wfst_release_stream", "wfst_lattice_records",
-                    "wfst_blank_skip", "wfst_decode_noalloc")
+                    "wfst_blank_skip", "wfst_decode_noalloc", "wfst_layer_create", "wfst_layer_release",
+                    "wfst_layer_logits", "wfst_log_softmax", "wfst_sample")
 KERNELS = ("clear", "init", "lpmax", "max", "expand", "finalize", "eps_expand", "eps_resolve",
            "eps_apply", "backtrack", "stream_begin", "stream_end", "reclass", "lat_resolve", "lat_init",
            "lat_back", "gc_begin", "gc_mark", "gc_scan", "gc_compact", "gc_commit", "gc_roots", "gc_clear",
@@ -123,6 +124,12 @@ def load_library():
         lib.wfst_blank_skip.argtypes = [vp, vp, i32, i32, i32, vp, i32, ctypes.c_float, vp, vp, vp]
         lib.wfst_decode_noalloc.argtypes = [vp, ctypes.POINTER(_Config), vp, i32, i32, i32, vp, vp, vp, i32, vp,
                                             vp, i32, vp, vp, vp]
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        lib.wfst_layer_create.argtypes = [vp, ctypes.c_int, vp, ctypes.POINTER(vp)]
+        lib.wfst_layer_release.argtypes = [vp]
+        lib.wfst_layer_logits.argtypes = [vp, vp, i32, i64, i32, vp, i32, vp, i32, i64, vp]
+        lib.wfst_log_softmax.argtypes = [vp, i32, i64, i64, i32, f32, vp, vp, i32, vp, i32, i64, vp]
+        lib.wfst_sample.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, i32, vp, vp, vp, vp]
         for name in EXPORTED_SYMBOLS:
             if name != "wfst_last_error":
                 getattr(lib, name).restype = ctypes.c_int
@@ -324,6 +331,36 @@ class Decoder:
                                 _ptr(sc), _ptr(meta)))
         return self._result(out, wcap, acap)
 
+    def decode_hidden(self, layer, hidden, lengths, scale: float = 1.0, bias=None, stream=None,
+                      words_cap: int | None = None, arcs_cap: int | None = None) -> DecodeResult:
+        """Decode a model's last hidden states [B, T, K]: ``layer`` (an OutputLayer
+        with the graph's vocabulary) and log_softmax(scale * logits + bias) make the
+        log-posteriors of the ``lengths[b]`` frames of each lane, in the decoder's
+        dtype, and decode searches them."""
+        lp = self._log_probs(layer, hidden, lengths, scale, bias, stream)
+        return self.decode(lp, lengths, stream=self._raw(stream), words_cap=words_cap, arcs_cap=arcs_cap)
+
+    def advance_hidden(self, channels, layer, hidden, lengths, scale: float = 1.0, bias=None,
+                       want_partial: bool = False, stream=None, words_cap: int = 4096, arcs_cap: int = 4096):
+        """advance_chunk from hidden states [C, T, K], as decode_hidden makes their log-posteriors."""
+        lp = self._log_probs(layer, hidden, lengths, scale, bias, stream)
+        return self.advance_chunk(channels, lp, lengths, want_partial=want_partial, stream=self._raw(stream),
+                                  words_cap=words_cap, arcs_cap=arcs_cap)
+
+    def _log_probs(self, layer, hidden, lengths, scale, bias, stream):
+        if hidden.dim() != 3:
+            raise ValueError("hidden must be [B, T, K]")
+        if layer.out_features != self.graph.vocab:
+            raise ValueError("the layer's out_features differ from the graph's vocabulary")
+        lens = np.asarray(lengths, dtype=np.int32).reshape(-1)
+        if lens.size and (lens.min() < 0 or lens.max() > hidden.shape[1]):
+            raise ValueError("lengths must lie in [0, T]")
+        return layer.log_probs(hidden, dtype=self.lp_dtype, scale=scale, bias=bias, lengths=lens, stream=stream)
+
+    @staticmethod
+    def _raw(stream):
+        return getattr(stream, "cuda_stream", stream)
+
     # ---- streams (page section 8): one lane per stream, search state kept on the device
 
     def create_stream(self, stream=None) -> int:
@@ -458,3 +495,6 @@ class Decoder:
             self.close()
         except Exception:
             pass
+
+
+from .score import OutputLayer, SampleResult, log_softmax, sample  # noqa: E402  (needs the names above)

@@ -10,7 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwfst_mi355x.so")
 SOURCES = [os.path.join(HERE, "csrc", "wfst_kernels.hip"), os.path.join(HERE, "csrc", "wfst_noalloc.hip"),
-           os.path.join(HERE, "csrc", "wfst_api.cpp")]
+           os.path.join(HERE, "csrc", "wfst_api.cpp"), os.path.join(HERE, "csrc", "wfst_score.hip"),
+           os.path.join(HERE, "csrc", "wfst_score_api.cpp")]
 
 FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",

@@ -19,6 +19,7 @@
 
 #include "wfst.h"
 #include "wfst_internal.h"
+#include "wfst_score.h"
 
 using namespace wfst;
 
@@ -1746,3 +1747,16 @@ extern "C" int wfst_blank_skip(wfst_decoder_t d, const void *log_prob, int32_t B
     HIP_TRY(hipStreamSynchronize(s));
     return WFST_OK;
 }
+
+// ---- helpers shared with the operators around the search (wfst_score_api.cpp)
+
+namespace wfst {
+
+int api_fail(int code, const std::string &msg) { return fail(code, msg); }
+
+int api_check_buffer(const void *p, size_t bytes, int device, const char *what)
+{
+    return check_device_buffer(p, bytes, device, what);
+}
+
+}  // namespace wfst
