@@ -571,7 +571,7 @@ int wfst_decoder_kernel_times(wfst_decoder_t d, double *out, int32_t n);
  * stay valid until the stream has passed it. None allocates device memory or
  * synchronises (but wfst_layer_create / _release), so they may be captured into
  * a HIP graph, which then reads and writes the same buffers at every replay.
- * They use no workspace: calls on different streams run at once. Element types
+ * Calls on different streams run at once (a workspace serves one call at a time). Element types
  * are WFST_LP_F32, _F16 and _BF16; a result is rounded to its type once, to
  * nearest even. Tensors are rows `stride` elements apart (stride >= the row's
  * length, any alignment of whole elements) on one device, which need not be the
@@ -639,11 +639,14 @@ int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_
  * is a device float [V] or null. Statistics are binary32. A row whose entries
  * are all -inf stays -inf; a row with a NaN or +inf becomes NaN. out may be x
  * itself (same element type and stride), otherwise it must not overlap x.
+ * workspace: device memory of at least wfst_log_softmax_workspace's bytes (null
+ * when those are 0), in use until the stream has passed the call.
  * Errors: WFST_EINVAL, WFST_EDEVICE.
  */
 int wfst_log_softmax(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, float scale,
                      const float *bias, const int32_t *lengths, int32_t T, void *out, int32_t out_dtype,
-                     int64_t out_stride, void *stream);
+                     int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream);
+int wfst_log_softmax_workspace(int32_t x_dtype, int64_t rows, int32_t V, int32_t out_dtype, int64_t *bytes);
 
 /*
  * Settings of a draw, for every row or, where a device array is given, one value

@@ -316,10 +316,18 @@ def test_log_softmax_refuses():
         wb.log_softmax(t, scale=float("nan"))
     lib = wb.load_library()
     # a tensor that ends past its allocation
-    assert lib.wfst_log_softmax(t.data_ptr(), 0, 1 << 40, 4, 10, 1.0, None, None, 1, t.data_ptr(), 0, 1 << 40, None) == -1
+    assert lib.wfst_log_softmax(t.data_ptr(), 0, 1 << 40, 4, 10, 1.0, None, None, 1, t.data_ptr(), 0, 1 << 40,
+                                None, 0, None) == -1
     assert b"past its allocation" in lib.wfst_last_error()
     assert lib.wfst_log_softmax(np.zeros(40, np.float32).ctypes.data, 0, 10, 4, 10, 1.0, None, None, 1, t.data_ptr(),
-                                0, 10, None) == -1
+                                0, 10, None, 0, None) == -1
+    # a row in pieces needs its workspace
+    t = torch.randn(2, 9000, device="cuda")
+    n = np.zeros(1, np.int64)
+    assert lib.wfst_log_softmax_workspace(0, 2, 9000, 0, n.ctypes.data) == 0 and n[0] > 0
+    for w, size in ((None, 0), (t.data_ptr(), int(n[0])), (torch.empty(8, device="cuda").data_ptr(), 8)):
+        assert lib.wfst_log_softmax(t.data_ptr(), 0, 9000, 2, 9000, 1.0, None, None, 1, t.data_ptr(), 0, 9000, w, size,
+                                    None) == -1
 
 
 # ---------------------------------------------------------------- draw

@@ -71,7 +71,7 @@ def test_log_softmax_refuses(lib, kw, word):
     a = dict(x=4096, xt=0, xs=8, rows=2, V=8, scale=1.0, out=8192, ot=0, os=8)
     a.update(kw)
     rc = lib.wfst_log_softmax(a["x"], a["xt"], a["xs"], a["rows"], a["V"], a["scale"], None, None, 1, a["out"],
-                              a["ot"], a["os"], None)
+                              a["ot"], a["os"], None, 0, None)
     assert rc == EINVAL and word in lib.wfst_last_error().decode()
 
 
@@ -93,7 +93,7 @@ def test_sample_refuses(lib, kw, word):
 def test_no_rows_is_no_work(lib):
     cfg = score._SampleConfig(1.0, 0, 1.0, 0.0, None, None, None, None)
     assert lib.wfst_sample(None, 0, 8, 0, 8, None, ctypes.byref(cfg), None, 1, None, None, None, None) == 0
-    assert lib.wfst_log_softmax(None, 0, 8, 0, 8, 1.0, None, None, 1, None, 0, 8, None) == 0
+    assert lib.wfst_log_softmax(None, 0, 8, 0, 8, 1.0, None, None, 1, None, 0, 8, None, 0, None) == 0
 
 
 def test_binding_refuses_host_tensors():

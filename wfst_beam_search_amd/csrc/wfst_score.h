@@ -77,8 +77,11 @@ struct NormCall {
     int32_t x_dtype, out_dtype;
     float scale;
     RowSet set;
+    void *workspace;            // norm_workspace bytes
 };
 
+int norm_pieces(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype);
+size_t norm_workspace(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype);
 hipError_t launch_log_softmax(const NormCall &c, hipStream_t s);
 
 // ---- draw

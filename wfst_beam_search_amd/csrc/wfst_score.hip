@@ -272,72 +272,270 @@ hipError_t launch_layer(const Layer &l, const LayerCall &c, hipStream_t s)
 
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr unsigned kMaxRowGrid = 1u << 18;
 
-__device__ __forceinline__ float norm_z(float x, float scale, const float *bias, int v)
+// VEC consecutive elements at any element alignment, as one load or store.
+template <typename T, int VEC> struct __attribute__((packed, aligned(sizeof(T)))) Pack { T v[VEC]; };
+
+// Elements moved at once: 16 bytes of the wider of the two types.
+template <typename A, typename B> constexpr int pack_len() { return 16 / (sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B)); }
+
+// z of the VEC elements from v on (-inf past V).
+template <typename XT, int VEC>
+__device__ __forceinline__ void norm_load(const XT *x, const NormCall &c, int v, float (&z)[VEC])
 {
-    const float z = x * scale;
-    return bias ? z + bias[v] : z;
+    if (v + VEC <= c.V) {
+        const Pack<XT, VEC> p = *(const Pack<XT, VEC> *)(x + v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) z[j] = (float)p.v[j] * c.scale;
+        if (c.bias) {
+            const Pack<float, VEC> b = *(const Pack<float, VEC> *)(c.bias + v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) z[j] += b.v[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            z[j] = -INFINITY;
+            if (v + j < c.V) {
+                z[j] = (float)x[v + j] * c.scale;
+                if (c.bias) z[j] += c.bias[v + j];
+            }
+        }
+    }
+}
+
+template <typename OT, int VEC>
+__device__ __forceinline__ void norm_store(OT *o, int V, int v, const float (&y)[VEC])
+{
+    if (v + VEC <= V) {
+        Pack<OT, VEC> p;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) p.v[j] = (OT)y[j];
+        *(Pack<OT, VEC> *)(o + v) = p;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (v + j < V) o[v + j] = (OT)y[j];
+    }
+}
+
+__device__ __forceinline__ float exp_diff(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896341f); }
+
+// Statistics of a set of z: the largest, how many equal it, and the sum of
+// exp(z - largest) over the others. A NaN makes the largest +inf.
+struct NormStat { float m, ones, sum; };
+
+__device__ __forceinline__ NormStat norm_join(const NormStat &a, const NormStat &b)
+{
+    NormStat r;
+    r.m = fmaxf(a.m, b.m);
+    r.ones = (a.m == r.m ? a.ones : 0.0f) + (b.m == r.m ? b.ones : 0.0f);
+    r.sum = 0.0f;
+    if (r.m > -INFINITY && r.m < INFINITY) {
+        r.sum += a.m == r.m ? a.sum : (a.sum + a.ones) * exp_diff(a.m - r.m);
+        r.sum += b.m == r.m ? b.sum : (b.sum + b.ones) * exp_diff(b.m - r.m);
+    }
+    return r;
+}
+
+// The row's normaliser: out = (z - m) - lz.
+__device__ __forceinline__ float norm_log(const NormStat &s) { return log1pf((s.ones - 1.0f) + s.sum); }
+
+__device__ __forceinline__ float norm_out(float z, const NormStat &s, float lz)
+{
+    const float y = (z - s.m) - lz;
+    return s.m == -INFINITY ? -INFINITY : (s.m == INFINITY ? NAN : y);
+}
+
+// Reduction over the WAVES wavefronts that share a row; red holds 3 * WAVES floats.
+template <int WAVES>
+__device__ __forceinline__ float row_max(float m, float *red)
+{
+    m = wave_max_f(m);
+    if (WAVES == 1) return m;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) m = fmaxf(m, red[w]);
+    return m;
+}
+
+template <int WAVES>
+__device__ __forceinline__ void row_sums(NormStat &s, float *red)
+{
+    s.sum = wave_sum_t(s.sum);
+    s.ones = wave_sum_t(s.ones);
+    if (WAVES == 1) return;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) { red[WAVES + wave] = s.sum; red[2 * WAVES + wave] = s.ones; }
+    __syncthreads();
+    s.sum = s.ones = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) { s.sum += red[WAVES + w]; s.ones += red[2 * WAVES + w]; }
+}
+
+// z in registers (NV packs a thread) and the statistics of what the WAVES wavefronts hold together.
+template <typename XT, int VEC, int WAVES, int NV>
+__device__ __forceinline__ NormStat norm_stat(const XT *x, const NormCall &c, int v0, float (&z)[NV][VEC], float *red)
+{
+    float m = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        norm_load<XT, VEC>(x, c, v0 + i * (WAVES * kWaveSize * VEC), z[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            m = fmaxf(m, z[i][j]);
+            bad |= z[i][j] != z[i][j];
+        }
+    if (bad) m = INFINITY;
+    NormStat s;
+    s.m = row_max<WAVES>(m, red);
+    s.sum = s.ones = 0.0f;
+    if (s.m > -INFINITY && s.m < INFINITY) {          // (the same for all threads of the row)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float d = z[i][j] - s.m;
+                s.ones += d == 0.0f ? 1.0f : 0.0f;
+                s.sum += d == 0.0f ? 0.0f : exp_diff(d);
+            }
+    }
+    row_sums<WAVES>(s, red);
+    return s;
+}
+
+// A row in the registers of WAVES wavefronts: read once, written once. With
+// WAVES = 1 a workgroup holds four rows and no barrier.
+template <typename XT, typename OT, int WAVES, int NV>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * kWaveSize) void k_norm_row(NormCall c)
+{
+    constexpr int VEC = pack_len<XT, OT>();
+    constexpr int kRows = WAVES == 1 ? 4 : 1;
+    __shared__ float red[3 * WAVES];
+    const int tid = WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    for (int64_t r = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? threadIdx.x >> 6 : 0); r < c.rows; r += step) {
+        if (!row_active(c.set, r)) continue;
+        float z[NV][VEC];
+        const NormStat s = norm_stat<XT, VEC, WAVES, NV>((const XT *)c.x + r * c.x_stride, c, tid * VEC, z, red);
+        const float lz = norm_log(s);
+        OT *o = (OT *)c.out + r * c.out_stride;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = tid * VEC + i * (WAVES * kWaveSize * VEC);
+            float y[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[j] = norm_out(z[i][j], s, lz);
+            if (v < c.V) norm_store<OT, VEC>(o, c.V, v, y);
+        }
+        if (WAVES > 1) __syncthreads();
+    }
+}
+
+// Long or few rows, cut into pieces of 256 * VEC * kPieceNV elements: the first
+// launch writes each piece's statistics, the second joins a row's and writes.
+constexpr int kPieceWaves = 4;
+constexpr int kPieceNV = 4;
+
+template <typename XT, typename OT, bool WRITE>
+__global__ __launch_bounds__(kPieceWaves *kWaveSize) void k_norm_piece(NormCall c, int pieces)
+{
+    constexpr int VEC = pack_len<XT, OT>();
+    constexpr int kSpan = kPieceWaves * kWaveSize * VEC;
+    __shared__ float red[3 * kPieceWaves];
+    const int tid = threadIdx.x;
+    NormStat *stats = (NormStat *)c.workspace;
+    for (int64_t w = blockIdx.x; w < c.rows * pieces; w += gridDim.x) {
+        const int64_t r = w / pieces;
+        const int p = (int)(w - r * pieces);
+        if (!row_active(c.set, r)) continue;
+        const XT *x = (const XT *)c.x + r * c.x_stride;
+        const int v0 = p * kSpan * kPieceNV + tid * VEC;
+        float z[kPieceNV][VEC];
+        if (!WRITE) {
+            const NormStat s = norm_stat<XT, VEC, kPieceWaves, kPieceNV>(x, c, v0, z, red);
+            if (tid == 0) stats[w] = s;
+            __syncthreads();
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < kPieceNV; ++i) norm_load<XT, VEC>(x, c, v0 + i * kSpan, z[i]);
+        NormStat s = {-INFINITY, 0.0f, 0.0f};
+        for (int q = tid & 63; q < pieces; q += kWaveSize) s = norm_join(s, stats[r * pieces + q]);
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            const NormStat o = {__shfl_xor(s.m, d, 64), __shfl_xor(s.ones, d, 64), __shfl_xor(s.sum, d, 64)};
+            s = norm_join(s, o);
+        }
+        const float lz = norm_log(s);
+        OT *o = (OT *)c.out + r * c.out_stride;
+#pragma unroll
+        for (int i = 0; i < kPieceNV; ++i) {
+            const int v = v0 + i * kSpan;
+            float y[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[j] = norm_out(z[i][j], s, lz);
+            if (v < c.V) norm_store<OT, VEC>(o, c.V, v, y);
+        }
+    }
 }
 
 template <typename XT, typename OT>
-__global__ __launch_bounds__(kNormThreads) void k_log_softmax(NormCall c)
+hipError_t norm_launch(const NormCall &c, hipStream_t s)
 {
-    __shared__ float red[8];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
-        if (!row_active(c.set, r)) continue;
-        const XT *x = (const XT *)c.x + r * c.x_stride;
-        OT *o = (OT *)c.out + r * c.out_stride;
-        float m = -INFINITY;
-        bool bad = false;
-        for (int v = tid; v < c.V; v += kNormThreads) {
-            const float z = norm_z((float)x[v], c.scale, c.bias, v);
-            bad |= z != z;
-            m = fmaxf(m, z);
-        }
-        m = wave_max_f(m);
-        if (__any(bad)) m = INFINITY;
-        if (lane == 0) red[wave] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        float sum = 0.0f, ones = 0.0f;
-        for (int v = tid; v < c.V; v += kNormThreads) {
-            const float z = norm_z((float)x[v], c.scale, c.bias, v);
-            if (z == m) ones += 1.0f;
-            else sum += __expf(z - m);
-        }
-        sum = wave_sum_t(sum);
-        ones = wave_sum_t(ones);
-        __syncthreads();
-        if (lane == 0) { red[wave] = sum; red[4 + wave] = ones; }
-        __syncthreads();
-        sum = (red[0] + red[1]) + (red[2] + red[3]);
-        ones = (red[4] + red[5]) + (red[6] + red[7]);
-        const float lz = log1pf((ones - 1.0f) + sum);
-        for (int v = tid; v < c.V; v += kNormThreads) {
-            const float z = norm_z((float)x[v], c.scale, c.bias, v);
-            float y = (z - m) - lz;
-            if (m == -INFINITY) y = -INFINITY;
-            if (m == INFINITY) y = NAN;
-            o[v] = (OT)y;
-        }
-        __syncthreads();
+    constexpr int VEC = pack_len<XT, OT>();
+    constexpr int kLane = kWaveSize * VEC;      // elements of one pack a lane
+    const auto grid = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxRowGrid)); };
+    const int pieces = norm_pieces(c.rows, c.V, c.x_dtype, c.out_dtype);
+    if (pieces > 0) {
+        const dim3 g = grid(c.rows * pieces), b(kPieceWaves * kWaveSize);
+        hipLaunchKernelGGL((k_norm_piece<XT, OT, false>), g, b, 0, s, c, pieces);
+        hipLaunchKernelGGL((k_norm_piece<XT, OT, true>), g, b, 0, s, c, pieces);
+    } else if (c.V <= 2 * kLane) {
+        hipLaunchKernelGGL((k_norm_row<XT, OT, 1, 2>), grid((c.rows + 3) / 4), dim3(256), 0, s, c);
+    } else if (c.V <= 8 * kLane) {
+        hipLaunchKernelGGL((k_norm_row<XT, OT, 1, 8>), grid((c.rows + 3) / 4), dim3(256), 0, s, c);
+    } else if (c.V <= 4 * 8 * kLane) {
+        hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 8>), grid(c.rows), dim3(256), 0, s, c);
+    } else {
+        hipLaunchKernelGGL((k_norm_row<XT, OT, 16, 8>), grid(c.rows), dim3(1024), 0, s, c);
     }
+    return hipGetLastError();
 }
 
 template <typename XT>
 hipError_t norm_ot(const NormCall &c, hipStream_t s)
 {
-    const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid)), b(kNormThreads);
-    if (c.out_dtype == kF32) hipLaunchKernelGGL((k_log_softmax<XT, float>), g, b, 0, s, c);
-    else if (c.out_dtype == kF16) hipLaunchKernelGGL((k_log_softmax<XT, _Float16>), g, b, 0, s, c);
-    else hipLaunchKernelGGL((k_log_softmax<XT, __bf16>), g, b, 0, s, c);
-    return hipGetLastError();
+    if (c.out_dtype == kF32) return norm_launch<XT, float>(c, s);
+    if (c.out_dtype == kF16) return norm_launch<XT, _Float16>(c, s);
+    return norm_launch<XT, __bf16>(c, s);
 }
 
 }  // namespace
+
+// Pieces a row is cut into, 0 for rows that stay whole: rows longer than 16
+// wavefronts hold, and rows so few that whole ones would leave most of the 256
+// CUs idle while each takes more than one piece.
+int norm_pieces(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype)
+{
+    const int vec = 16 / (int)std::max(dtype_size(x_dtype), dtype_size(out_dtype));
+    const int span = kPieceWaves * kWaveSize * vec * kPieceNV;
+    const int whole = 16 * 8 * kWaveSize * vec;
+    const int pieces = (V + span - 1) / span;
+    return V > whole || (rows <= 128 && pieces > 1) ? pieces : 0;
+}
+
+size_t norm_workspace(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype)
+{
+    return (size_t)rows * (size_t)norm_pieces(rows, V, x_dtype, out_dtype) * sizeof(NormStat);
+}
 
 hipError_t launch_log_softmax(const NormCall &c, hipStream_t s)
 {

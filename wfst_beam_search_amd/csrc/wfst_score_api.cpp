@@ -250,11 +250,11 @@ extern "C" int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dt
 
 extern "C" int wfst_log_softmax(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, float scale,
                                 const float *bias, const int32_t *lengths, int32_t T, void *out, int32_t out_dtype,
-                                int64_t out_stride, void *stream)
+                                int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream)
 {
     return guarded([&]() -> int {
         if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return api_fail(WFST_EINVAL, "not an element type");
-        if (rows < 0) return api_fail(WFST_EINVAL, "rows must not be negative");
+        if (rows < 0 || rows > ((int64_t)1 << 40)) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^40]");
         if (V < 1 || V > (1 << 24)) return api_fail(WFST_EINVAL, "V must lie in [1, 2^24]");
         if (!std::isfinite(scale)) return api_fail(WFST_EINVAL, "scale must be finite");
         if (rows == 0) return WFST_OK;
@@ -283,8 +283,29 @@ extern "C" int wfst_log_softmax(const void *x, int32_t x_dtype, int64_t x_stride
             return api_fail(WFST_EINVAL, "out must be x itself (same type and stride) or not overlap it");
         if (bias && ranges_meet(bias, (int64_t)V * 4, out, ob))
             return api_fail(WFST_EINVAL, "out must not overlap bias");
-        const NormCall c{x, out, bias, x_stride, out_stride, rows, V, x_dtype, out_dtype, scale, {lengths, T}};
+        const size_t need = norm_workspace(rows, V, x_dtype, out_dtype);
+        if (need) {
+            if (!workspace || workspace_bytes < 0 || (size_t)workspace_bytes < need)
+                return api_fail(WFST_EINVAL, "workspace must hold " + std::to_string(need) + " bytes");
+            TRY(check_aligned(workspace, 4, "workspace"));
+            TRY(api_check_buffer(workspace, need, device, "workspace"));
+            if (ranges_meet(workspace, (int64_t)need, out, ob) || ranges_meet(workspace, (int64_t)need, x, xb))
+                return api_fail(WFST_EINVAL, "workspace must not overlap x or out");
+        }
+        const NormCall c{x, out, bias, x_stride, out_stride, rows, V, x_dtype, out_dtype, scale, {lengths, T}, workspace};
         HIP_TRY(launch_log_softmax(c, (hipStream_t)stream));
+        return WFST_OK;
+    });
+}
+
+extern "C" int wfst_log_softmax_workspace(int32_t x_dtype, int64_t rows, int32_t V, int32_t out_dtype, int64_t *bytes)
+{
+    return guarded([&]() -> int {
+        if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return api_fail(WFST_EINVAL, "not an element type");
+        if (rows < 0 || rows > ((int64_t)1 << 40)) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^40]");
+        if (V < 1 || V > (1 << 24)) return api_fail(WFST_EINVAL, "V must lie in [1, 2^24]");
+        if (!bytes) return api_fail(WFST_EINVAL, "a pointer is null");
+        *bytes = (int64_t)norm_workspace(rows, V, x_dtype, out_dtype);
         return WFST_OK;
     });
 }
@@ -296,7 +317,7 @@ extern "C" int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int
     return guarded([&]() -> int {
         if (!cfg) return api_fail(WFST_EINVAL, "config is null");
         if (!dtype_ok(x_dtype)) return api_fail(WFST_EINVAL, "not an element type");
-        if (rows < 0) return api_fail(WFST_EINVAL, "rows must not be negative");
+        if (rows < 0 || rows > ((int64_t)1 << 40)) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^40]");
         if (V < 1 || V > (1 << 24)) return api_fail(WFST_EINVAL, "V must lie in [1, 2^24]");
         if (!cfg->temperatures && !(cfg->temperature >= 0.0f && std::isfinite(cfg->temperature)))
             return api_fail(WFST_EINVAL, "temperature must be finite and not negative");

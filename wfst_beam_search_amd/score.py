@@ -154,6 +154,15 @@ def _out(out, shape, dtype, device, other):
     return out
 
 
+def _workspace(nbytes, device, other):
+    import torch
+    if nbytes <= 0:
+        return None
+    work = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _keep(other, work)
+    return work
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -270,8 +279,12 @@ def log_softmax(x, dtype: str | None = None, scale: float = 1.0, bias=None, leng
     lengths, T = _lengths(lengths, x.shape[:-1], device, other)
     out = _out(out, x.shape, want, device, other)
     _, ostep = _rows(out, "out")
+    ocode = _types()[0][want]
+    need = ctypes.c_int64(0)
+    _check(lib.wfst_log_softmax_workspace(code, rows, V, ocode, ctypes.byref(need)))
+    work = _workspace(need.value, device, other)
     _check(lib.wfst_log_softmax(x.data_ptr(), code, step, rows, V, float(scale), _p(bias), _p(lengths), T,
-                                out.data_ptr(), _types()[0][want], ostep, raw))
+                                out.data_ptr(), ocode, ostep, _p(work), need.value, raw))
     return out
 
 
