@@ -24,11 +24,35 @@ __device__ __forceinline__ bool row_active(const RowSet &s, int64_t r)
     return (int32_t)(r - b * s.T) < s.lengths[b];
 }
 
+// Reductions over a wavefront by data-parallel moves (all 64 lanes active): four
+// steps inside rows of 16 lanes, two across rows, the result read from lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f(float id, float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(id), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+
 __device__ __forceinline__ float wave_max_f(float v)
 {
-#pragma unroll
-    for (int d = kWaveSize / 2; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, kWaveSize));
-    return v;
+    const float id = -INFINITY;
+    v = fmaxf(v, dpp_f<0x111, 0xf>(id, v));
+    v = fmaxf(v, dpp_f<0x112, 0xf>(id, v));
+    v = fmaxf(v, dpp_f<0x114, 0xf>(id, v));
+    v = fmaxf(v, dpp_f<0x118, 0xf>(id, v));
+    v = fmaxf(v, dpp_f<0x142, 0xa>(id, v));
+    v = fmaxf(v, dpp_f<0x143, 0xc>(id, v));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ float wave_sum_f(float v)
+{
+    v += dpp_f<0x111, 0xf>(0.0f, v);
+    v += dpp_f<0x112, 0xf>(0.0f, v);
+    v += dpp_f<0x114, 0xf>(0.0f, v);
+    v += dpp_f<0x118, 0xf>(0.0f, v);
+    v += dpp_f<0x142, 0xa>(0.0f, v);
+    v += dpp_f<0x143, 0xc>(0.0f, v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 template <typename T>
@@ -323,7 +347,8 @@ __device__ __forceinline__ void norm_store(OT *o, int V, int v, const float (&y)
 __device__ __forceinline__ float exp_diff(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896341f); }
 
 // Statistics of a set of z: the largest, how many equal it, and the sum of
-// exp(z - largest) over the others. A NaN makes the largest +inf.
+// exp(z - largest) over the others. A NaN or +inf among the z makes the sum NaN
+// (by itself, through z - largest), or the largest +inf where all else is -inf.
 struct NormStat { float m, ones, sum; };
 
 __device__ __forceinline__ NormStat norm_join(const NormStat &a, const NormStat &b)
@@ -332,108 +357,102 @@ __device__ __forceinline__ NormStat norm_join(const NormStat &a, const NormStat 
     r.m = fmaxf(a.m, b.m);
     r.ones = (a.m == r.m ? a.ones : 0.0f) + (b.m == r.m ? b.ones : 0.0f);
     r.sum = 0.0f;
-    if (r.m > -INFINITY && r.m < INFINITY) {
+    if (r.m == INFINITY) {
+        r.sum = NAN;
+    } else if (r.m > -INFINITY) {
         r.sum += a.m == r.m ? a.sum : (a.sum + a.ones) * exp_diff(a.m - r.m);
         r.sum += b.m == r.m ? b.sum : (b.sum + b.ones) * exp_diff(b.m - r.m);
     }
     return r;
 }
 
-// The row's normaliser: out = (z - m) - lz.
-__device__ __forceinline__ float norm_log(const NormStat &s) { return log1pf((s.ones - 1.0f) + s.sum); }
+// out = (z - m) - lz of a row. A row of -inf alone is left as it is.
+struct NormRow { float m, lz; };
 
-__device__ __forceinline__ float norm_out(float z, const NormStat &s, float lz)
+__device__ __forceinline__ NormRow norm_row(const NormStat &s)
 {
-    const float y = (z - s.m) - lz;
-    return s.m == -INFINITY ? -INFINITY : (s.m == INFINITY ? NAN : y);
+    NormRow r = {s.m, log1pf((s.ones - 1.0f) + s.sum)};
+    if (s.m == -INFINITY) r = {0.0f, 0.0f};
+    if (s.m == INFINITY) r = {0.0f, NAN};
+    return r;
 }
 
-// Reduction over the WAVES wavefronts that share a row; red holds 3 * WAVES floats.
-template <int WAVES>
-__device__ __forceinline__ float row_max(float m, float *red)
+// Statistics of a row that WAVES wavefronts hold, NV packs a thread; red holds
+// 3 * WAVES floats.
+template <int VEC, int WAVES, int NV>
+__device__ __forceinline__ NormStat norm_stats(const float (&z)[NV][VEC], float *red)
 {
-    m = wave_max_f(m);
-    if (WAVES == 1) return m;
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = red[0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) m = fmaxf(m, red[w]);
-    return m;
-}
-
-template <int WAVES>
-__device__ __forceinline__ void row_sums(NormStat &s, float *red)
-{
-    s.sum = wave_sum_t(s.sum);
-    s.ones = wave_sum_t(s.ones);
-    if (WAVES == 1) return;
     const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) { red[WAVES + wave] = s.sum; red[2 * WAVES + wave] = s.ones; }
-    __syncthreads();
-    s.sum = s.ones = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) { s.sum += red[WAVES + w]; s.ones += red[2 * WAVES + w]; }
-}
-
-// z in registers (NV packs a thread) and the statistics of what the WAVES wavefronts hold together.
-template <typename XT, int VEC, int WAVES, int NV>
-__device__ __forceinline__ NormStat norm_stat(const XT *x, const NormCall &c, int v0, float (&z)[NV][VEC], float *red)
-{
-    float m = -INFINITY;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        norm_load<XT, VEC>(x, c, v0 + i * (WAVES * kWaveSize * VEC), z[i]);
-    }
+    const bool first = (threadIdx.x & 63) == 0;
+    NormStat s = {-INFINITY, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            m = fmaxf(m, z[i][j]);
-            bad |= z[i][j] != z[i][j];
-        }
-    if (bad) m = INFINITY;
-    NormStat s;
-    s.m = row_max<WAVES>(m, red);
-    s.sum = s.ones = 0.0f;
-    if (s.m > -INFINITY && s.m < INFINITY) {          // (the same for all threads of the row)
+        for (int j = 0; j < VEC; ++j) s.m = fmaxf(s.m, z[i][j]);
+    s.m = wave_max_f(s.m);
+    if (WAVES > 1) {
+        if (first) red[wave] = s.m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) s.m = fmaxf(s.m, red[w]);
+    }
+    if (s.m > -INFINITY) {                            // (the same for all threads of the row)
+        uint32_t ones = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float d = z[i][j] - s.m;
-                s.ones += d == 0.0f ? 1.0f : 0.0f;
-                s.sum += d == 0.0f ? 0.0f : exp_diff(d);
+                const float d = z[i][j] - s.m, e = exp_diff(d);
+                const bool top = d == 0.0f;
+                ones += __popcll(__ballot(top));      // (counted on the scalar unit)
+                s.sum += top ? 0.0f : e;
             }
+        s.ones = (float)ones;
+    } else {
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) nan |= z[i][j] != z[i][j];
+        s.sum = nan ? 1.0f : 0.0f;
     }
-    row_sums<WAVES>(s, red);
+    s.sum = wave_sum_f(s.sum);
+    if (WAVES > 1) {
+        if (first) { red[WAVES + wave] = s.sum; red[2 * WAVES + wave] = s.ones; }
+        __syncthreads();
+        s.sum = s.ones = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) { s.sum += red[WAVES + w]; s.ones += red[2 * WAVES + w]; }
+    }
+    if (s.m == -INFINITY && s.sum > 0.0f) s.m = INFINITY;
     return s;
 }
 
-// A row in the registers of WAVES wavefronts: read once, written once. With
-// WAVES = 1 a workgroup holds four rows and no barrier.
+// A row in the registers of WAVES wavefronts: read once, written once. A workgroup
+// of one-wavefront rows holds four of them and no barrier.
 template <typename XT, typename OT, int WAVES, int NV>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * kWaveSize) void k_norm_row(NormCall c)
 {
     constexpr int VEC = pack_len<XT, OT>();
+    constexpr int kSpan = WAVES * kWaveSize * VEC;
     constexpr int kRows = WAVES == 1 ? 4 : 1;
     __shared__ float red[3 * WAVES];
-    const int tid = WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x;
+    const int v0 = (WAVES == 1 ? (threadIdx.x & 63) : threadIdx.x) * VEC;
     const int64_t step = (int64_t)gridDim.x * kRows;
     for (int64_t r = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? threadIdx.x >> 6 : 0); r < c.rows; r += step) {
         if (!row_active(c.set, r)) continue;
+        const XT *x = (const XT *)c.x + r * c.x_stride;
         float z[NV][VEC];
-        const NormStat s = norm_stat<XT, VEC, WAVES, NV>((const XT *)c.x + r * c.x_stride, c, tid * VEC, z, red);
-        const float lz = norm_log(s);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) norm_load<XT, VEC>(x, c, v0 + i * kSpan, z[i]);
+        const NormRow n = norm_row(norm_stats<VEC, WAVES, NV>(z, red));
         OT *o = (OT *)c.out + r * c.out_stride;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = tid * VEC + i * (WAVES * kWaveSize * VEC);
             float y[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) y[j] = norm_out(z[i][j], s, lz);
-            if (v < c.V) norm_store<OT, VEC>(o, c.V, v, y);
+            for (int j = 0; j < VEC; ++j) y[j] = (z[i][j] - n.m) - n.lz;
+            if (v0 + i * kSpan < c.V) norm_store<OT, VEC>(o, c.V, v0 + i * kSpan, y);
         }
         if (WAVES > 1) __syncthreads();
     }
@@ -459,14 +478,14 @@ __global__ __launch_bounds__(kPieceWaves *kWaveSize) void k_norm_piece(NormCall 
         const XT *x = (const XT *)c.x + r * c.x_stride;
         const int v0 = p * kSpan * kPieceNV + tid * VEC;
         float z[kPieceNV][VEC];
+#pragma unroll
+        for (int i = 0; i < kPieceNV; ++i) norm_load<XT, VEC>(x, c, v0 + i * kSpan, z[i]);
         if (!WRITE) {
-            const NormStat s = norm_stat<XT, VEC, kPieceWaves, kPieceNV>(x, c, v0, z, red);
+            const NormStat s = norm_stats<VEC, kPieceWaves, kPieceNV>(z, red);
             if (tid == 0) stats[w] = s;
             __syncthreads();
             continue;
         }
-#pragma unroll
-        for (int i = 0; i < kPieceNV; ++i) norm_load<XT, VEC>(x, c, v0 + i * kSpan, z[i]);
         NormStat s = {-INFINITY, 0.0f, 0.0f};
         for (int q = tid & 63; q < pieces; q += kWaveSize) s = norm_join(s, stats[r * pieces + q]);
 #pragma unroll
@@ -474,16 +493,37 @@ __global__ __launch_bounds__(kPieceWaves *kWaveSize) void k_norm_piece(NormCall 
             const NormStat o = {__shfl_xor(s.m, d, 64), __shfl_xor(s.ones, d, 64), __shfl_xor(s.sum, d, 64)};
             s = norm_join(s, o);
         }
-        const float lz = norm_log(s);
+        const NormRow n = norm_row(s);
         OT *o = (OT *)c.out + r * c.out_stride;
 #pragma unroll
         for (int i = 0; i < kPieceNV; ++i) {
             const int v = v0 + i * kSpan;
             float y[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) y[j] = norm_out(z[i][j], s, lz);
+            for (int j = 0; j < VEC; ++j) y[j] = (z[i][j] - n.m) - n.lz;
             if (v < c.V) norm_store<OT, VEC>(o, c.V, v, y);
         }
+    }
+}
+
+// A row on 4 or 16 wavefronts, with just the packs it needs (a pack past the row
+// costs its branch and registers: 5000 labels on 8 packs a thread instead of 5
+// took 114 us instead of 92).
+template <typename XT, typename OT>
+void norm_wide(const NormCall &c, hipStream_t s)
+{
+    constexpr int kPack4 = 4 * kWaveSize * pack_len<XT, OT>();
+    const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid));
+    switch ((c.V + kPack4 - 1) / kPack4) {
+    case 1: case 2: case 3: hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 3>), g, dim3(256), 0, s, c); break;
+    case 4: hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 4>), g, dim3(256), 0, s, c); break;
+    case 5: hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 5>), g, dim3(256), 0, s, c); break;
+    case 6: hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 6>), g, dim3(256), 0, s, c); break;
+    case 7: case 8: hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 8>), g, dim3(256), 0, s, c); break;
+    case 9: case 10: case 11: case 12: hipLaunchKernelGGL((k_norm_row<XT, OT, 16, 3>), g, dim3(1024), 0, s, c); break;
+    case 13: case 14: case 15: case 16: hipLaunchKernelGGL((k_norm_row<XT, OT, 16, 4>), g, dim3(1024), 0, s, c); break;
+    case 17: case 18: case 19: case 20: hipLaunchKernelGGL((k_norm_row<XT, OT, 16, 5>), g, dim3(1024), 0, s, c); break;
+    default: hipLaunchKernelGGL((k_norm_row<XT, OT, 16, 8>), g, dim3(1024), 0, s, c); break;
     }
 }
 
@@ -500,12 +540,12 @@ hipError_t norm_launch(const NormCall &c, hipStream_t s)
         hipLaunchKernelGGL((k_norm_piece<XT, OT, true>), g, b, 0, s, c, pieces);
     } else if (c.V <= 2 * kLane) {
         hipLaunchKernelGGL((k_norm_row<XT, OT, 1, 2>), grid((c.rows + 3) / 4), dim3(256), 0, s, c);
+    } else if (c.V <= 4 * kLane) {
+        hipLaunchKernelGGL((k_norm_row<XT, OT, 1, 4>), grid((c.rows + 3) / 4), dim3(256), 0, s, c);
     } else if (c.V <= 8 * kLane) {
         hipLaunchKernelGGL((k_norm_row<XT, OT, 1, 8>), grid((c.rows + 3) / 4), dim3(256), 0, s, c);
-    } else if (c.V <= 4 * 8 * kLane) {
-        hipLaunchKernelGGL((k_norm_row<XT, OT, 4, 8>), grid(c.rows), dim3(256), 0, s, c);
     } else {
-        hipLaunchKernelGGL((k_norm_row<XT, OT, 16, 8>), grid(c.rows), dim3(1024), 0, s, c);
+        norm_wide<XT, OT>(c, s);
     }
     return hipGetLastError();
 }

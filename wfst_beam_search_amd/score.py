@@ -17,6 +17,7 @@ they stay as they were (in a new tensor they are unspecified).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import numpy as np
@@ -102,11 +103,11 @@ def _rows(t, what):
 def _stream(stream, device):
     """(raw handle, the stream when it is not the current one)."""
     import torch
-    cur = torch.cuda.current_stream(device)
+    cur = torch._C._cuda_getCurrentRawStream(device.index)     # (current_stream() builds an object: 2 us)
     if stream is None:
-        return cur.cuda_stream, None
+        return cur, None
     raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if raw == cur.cuda_stream:
+    if raw == cur:
         return raw, None
     other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, device=device)
     return raw, other
@@ -259,6 +260,13 @@ class OutputLayer:
             pass
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(code, rows, V, ocode):
+    need = ctypes.c_int64(0)
+    _check(load_library().wfst_log_softmax_workspace(code, rows, V, ocode, ctypes.byref(need)))
+    return need.value
+
+
 def log_softmax(x, dtype: str | None = None, scale: float = 1.0, bias=None, lengths=None, out=None, stream=None):
     """log_softmax(scale * x + bias) over the last dimension of ``x``, in ``dtype``
     ("f32", "f16", "bf16"; default: x's own), ``bias`` float32 [V] or None. ``out``
@@ -280,11 +288,10 @@ def log_softmax(x, dtype: str | None = None, scale: float = 1.0, bias=None, leng
     out = _out(out, x.shape, want, device, other)
     _, ostep = _rows(out, "out")
     ocode = _types()[0][want]
-    need = ctypes.c_int64(0)
-    _check(lib.wfst_log_softmax_workspace(code, rows, V, ocode, ctypes.byref(need)))
-    work = _workspace(need.value, device, other)
+    need = _norm_bytes(code, rows, V, ocode)
+    work = _workspace(need, device, other)
     _check(lib.wfst_log_softmax(x.data_ptr(), code, step, rows, V, float(scale), _p(bias), _p(lengths), T,
-                                out.data_ptr(), ocode, ostep, _p(work), need.value, raw))
+                                out.data_ptr(), ocode, ostep, _p(work), need, raw))
     return out
 
 
