@@ -5,16 +5,19 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwfst_mi355x.so")
 SOURCES = [os.path.join(HERE, "csrc", "wfst_kernels.hip"), os.path.join(HERE, "csrc", "wfst_noalloc.hip"),
-           os.path.join(HERE, "csrc", "wfst_api.cpp"), os.path.join(HERE, "csrc", "wfst_score.hip"),
+           os.path.join(HERE, "csrc", "wfst_api.cpp"), os.path.join(HERE, "csrc", "wfst_layer.hip"),
+           os.path.join(HERE, "csrc", "wfst_norm.hip"), os.path.join(HERE, "csrc", "wfst_sample.hip"),
            os.path.join(HERE, "csrc", "wfst_score_api.cpp")]
 
 FLAGS = [
-    "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-shared",
+    "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
     # every fp32 operation is rounded on its own: no contraction into FMA
     "-ffp-contract=off",
     # no packed fp32 instructions
@@ -32,15 +35,25 @@ PROBE_LIB = os.path.join(HERE, "libwfst_probe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "wfst_probe.hip")]
 
 
-def _compile(out: str, sources, verbose: bool) -> None:
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = out + f".tmp{os.getpid()}"
-    cmd = [hipcc, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
-           "-o", tmp, *sources]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
-    os.replace(tmp, out)
+
+
+def _compile(out: str, sources, verbose: bool) -> None:
+    """Each source to an object of its own, several at once, then one shared library."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    jobs = max(1, min(4, int(os.environ.get("MAX_JOBS", "4"))))
+    with tempfile.TemporaryDirectory(prefix="wfst_build_") as tmpdir:
+        objs = [os.path.join(tmpdir, f"{i}.o") for i in range(len(sources))]
+        with ThreadPoolExecutor(jobs) as pool:
+            list(pool.map(lambda so: _run([hipcc, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I",
+                                           os.path.join(HERE, "csrc"), "-c", "-o", so[1], so[0]], verbose),
+                          zip(sources, objs)))
+        tmp = out + f".tmp{os.getpid()}"
+        _run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objs], verbose)
+        os.replace(tmp, out)
 
 
 def build(verbose: bool = False) -> str:

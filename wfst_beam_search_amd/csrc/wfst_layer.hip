@@ -1,0 +1,404 @@
+// gfx950 (CDNA4) kernels of the output layer with 4-bit weights: hidden states to logits.
+#include "wfst_score_device.h"
+
+namespace wfst {
+
+namespace {
+
+// y[m, n] = bias[n] + sum_g s[n, g] * sum_{k in g} (q[n, k] - z[n, g]) x[m, k]
+//
+// Each wavefront owns 16 output features and up to 16 rows of x and runs
+// v_mfma_f32_16x16x32_f16 with x as the left operand and the weights as the
+// right one, so the lane that unpacks feature n's weights also receives n's
+// sums and needs n's scale and zero alone. A weight is unpacked exactly: a mask
+// puts two 4-bit values into the mantissas of two halves 1024 + q (or 1024 +
+// 16 q), and one packed subtraction (or multiply-add by 1/16) of the zero point
+// leaves q - z, an integer in [-15, 15]. Sums inside a group are the matrix
+// unit's binary32 sums of exact products; a group's sum is multiplied by its
+// scale in binary32 and added to the row's sum.
+//
+// x enters the matrix unit as binary16. bfloat16 and binary32 rows are scaled
+// by a power of two per 128 features so that the block's largest finite value
+// lies in [2^14, 2^15): a bfloat16 value then fits binary16 exactly or, 2^29
+// below the block's largest, loses less than 2^-39 of that; a binary32 value is
+// cut into a sum of two binary16 values (off by at most 2^-24 of itself, or
+// 2^-39 of the block's largest).
+
+constexpr int kLayerWaves = 4;
+constexpr int kLayerThreads = kLayerWaves * kWaveSize;
+constexpr int kRowsM = 16;                     // rows of x one matrix instruction takes
+
+// The exponent e for which |x| <= mx lies below 2^15 when scaled by 2^-e.
+__device__ __forceinline__ int block_exponent(float mx)
+{
+    if (!(mx > 0.0f)) return 0;
+    int e;
+    (void)frexpf(mx, &e);                      // mx = f * 2^e, f in [0.5, 1)
+    e -= 15;
+    return e < -120 ? -120 : e;                // 2^e and its inverse stay normal
+}
+
+template <typename XT> constexpr int kParts = sizeof(XT) == 4 ? 2 : 1;
+template <typename XT> constexpr bool kScaled = !__is_same(XT, _Float16);
+
+// x[k .. k+7] of a row of K features (0 past them, and for a row that is not there).
+template <typename XT>
+__device__ __forceinline__ void load_x(const XT *row, bool there, int k, int K, float (&v)[8])
+{
+    if (there && k + 8 <= K) {
+        const Pack<XT, 8> p = *(const Pack<XT, 8> *)(row + k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (float)p.v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = there && k + j < K ? (float)row[k + j] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ float finite_max(const float (&v)[8], float mx)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = fabsf(v[j]);
+        mx = fmaxf(mx, a < INFINITY ? a : 0.0f);
+    }
+    return mx;
+}
+
+// The binary16 operand (and for binary32 its remainder) of eight values, scaled by `inv`, a power of two.
+template <typename XT>
+__device__ __forceinline__ void to_half(const float (&v)[8], float inv, half8_t &hi, half8_t &lo)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float s = kScaled<XT> ? v[j] * inv : v[j];
+        hi[j] = (_Float16)s;
+        if (kParts<XT> == 2) {
+            const float d = s - (float)hi[j];
+            lo[j] = (_Float16)(fabsf(s) < INFINITY ? d : 0.0f);      // (an infinity or NaN is in hi alone)
+        }
+    }
+}
+
+// Scales and zero points of one lane's output feature in one tile.
+template <int WS, int GPT> struct TileScale {
+    uint32_t s[WS * GPT < 4 ? 1 : WS * GPT / 4];
+    uint32_t z;
+};
+
+template <int WS, int GPT>
+__device__ __forceinline__ TileScale<WS, GPT> load_tile_scale(const Layer &l, size_t i)
+{
+    TileScale<WS, GPT> t;
+    if constexpr (WS * GPT == 2) {
+        t.s[0] = ((const uint16_t *)l.scales)[i];
+    } else {
+        const uint32_t *p = (const uint32_t *)l.scales + i * (WS * GPT / 4);
+#pragma unroll
+        for (int j = 0; j < WS * GPT / 4; ++j) t.s[j] = p[j];
+    }
+    t.z = 0x08080808u;
+    if (l.zeros) {
+        if constexpr (GPT == 1) t.z = l.zeros[i];
+        else if constexpr (GPT == 2) t.z = ((const uint16_t *)l.zeros)[i];
+        else t.z = ((const uint32_t *)l.zeros)[i];
+    }
+    return t;
+}
+
+template <int WS, int GPT>
+__device__ __forceinline__ float scale_of(const TileScale<WS, GPT> &t, int g, bool bf16)
+{
+    if constexpr (WS == 4) return __uint_as_float(t.s[g]);
+    const uint32_t h = (t.s[g / 2] >> (16 * (g & 1))) & 0xFFFFu;
+    union { uint16_t u; _Float16 h; } c;
+    c.u = (uint16_t)h;
+    return bf16 ? __uint_as_float(h << 16) : (float)c.h;
+}
+
+// The eight weights q - z of one word, exact in binary16.
+struct ZeroPair { half2_t whole, sixteenth; };
+
+__device__ __forceinline__ ZeroPair zero_pair(uint32_t z)
+{
+    const _Float16 h = (_Float16)(float)z;
+    const _Float16 a = (_Float16)-1024.0f - h, b = (_Float16)-64.0f - h;
+    return {{a, a}, {b, b}};
+}
+
+__device__ __forceinline__ half8_t unpack_word(uint32_t w, uint32_t magic, const ZeroPair &z)
+{
+    union { uint32_t u[4]; half2_t h[4]; half8_t v; } q;
+    const half2_t r16 = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const uint32_t w8 = w >> 8;
+    q.u[0] = (w & 0x000F000Fu) | magic;
+    q.u[1] = (w & 0x00F000F0u) | magic;
+    q.u[2] = (w8 & 0x000F000Fu) | magic;
+    q.u[3] = (w8 & 0x00F000F0u) | magic;
+    q.h[0] += z.whole;
+    q.h[2] += z.whole;
+    q.h[1] = __builtin_elementwise_fma(q.h[1], r16, z.sixteenth);
+    q.h[3] = __builtin_elementwise_fma(q.h[3], r16, z.sixteenth);
+    return q.v;
+}
+
+// 1024 in both halves, in a vector register that the compiler does not fold: a
+// mask and this then combine in one instruction.
+__device__ __forceinline__ uint32_t magic_1024()
+{
+    uint32_t m;
+    asm("v_mov_b32 %0, 0x64006400" : "=v"(m));
+    return m;
+}
+
+__device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, float y)
+{
+    const int64_t i = m * c.out_stride + n;
+    if (c.out_dtype == kF32) ((float *)c.out)[i] = y;
+    else if (c.out_dtype == kF16) ((_Float16 *)c.out)[i] = (_Float16)y;
+    else ((__bf16 *)c.out)[i] = (__bf16)y;
+}
+
+// Up to 16 rows of x at a time (blockIdx.y: which 16), which the workgroup itself turns into
+// binary16 in LDS, kc blocks of 128 features per slice at a time, laid out as the
+// matrix instruction reads it: [32 features][8 features][row][8]. Only RP rows
+// (the power of two that holds them) are kept; lanes of rows past them repeat
+// the last one and their sums are dropped. KS = 1: a wavefront owns 16 output
+// features and walks all of K. KS = 4: the four wavefronts of a workgroup own
+// the same 16 features and a quarter of K each, joined in LDS at the end.
+// Weights stream D tiles ahead of their use.
+template <typename XT, int WS, int GPT, int KS>
+__global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall c, int RP, int kc)
+{
+    constexpr int P = kParts<XT>;
+    constexpr int D = KS == 1 ? 4 : 2;
+    extern __shared__ __align__(16) char smem[];
+    half8_t *xs = (half8_t *)smem;                                      // [P][KS * kc * 16][RP]
+    const int part = KS * kc * 16 * RP;
+    float *xf = (float *)(xs + P * part);                               // [KS * kc][RP]
+    float4_t *joint = (float4_t *)(smem);                               // (KS = 4, after the last use of xs)
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int m0 = blockIdx.y * kRowsM, M = min(kRowsM, c.M - m0);
+    const int nt = min((int)(KS == 1 ? blockIdx.x * kLayerWaves + wave : blockIdx.x), l.nt - 1);
+    const bool live = KS > 1 || blockIdx.x * kLayerWaves + wave < l.nt;
+    const int col = lane & 15, quad = lane >> 4;
+    const int slice = KS == 1 ? 0 : wave;
+    const int b0 = (int)((int64_t)l.kb * slice / KS), nb = (int)((int64_t)l.kb * (slice + 1) / KS) - b0;
+    const bool bf16s = l.scale_dtype == kBF16;
+    const uint32_t magic = magic_1024();
+    const XT *x = (const XT *)c.x + (int64_t)m0 * c.x_stride;
+    const size_t tile0 = (size_t)nt * l.kb + b0;
+
+    uint4 wq[D];
+    TileScale<WS, GPT> sq[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+        const size_t t = tile0 + min(i, max(nb - 1, 0));
+        wq[i] = l.w[min(t, (size_t)l.nt * l.kb - 1) * kWaveSize + lane];
+        sq[i] = load_tile_scale<WS, GPT>(l, min(t, (size_t)l.nt * l.kb - 1) * kTileN + col);
+    }
+
+    // staging: 16 * RP threads (at most 64) take a block of 128 features, each up to four runs of 8
+    const int per = min(64, 16 * RP), bpw = 64 / per;
+    const int l2 = lane % per, sr = l2 % RP, s0 = l2 / RP, sstep = per / RP, spl = 16 / sstep;
+    const bool there = sr < M && row_active(c.rows, m0 + sr);
+    const int longest = (l.kb + KS - 1) / KS;
+    float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int arow = min(col, RP - 1), frow = min(quad * 4, RP - 1);
+
+    for (int c0 = 0; c0 < longest; c0 += kc) {
+        if (c0) __syncthreads();
+        for (int u = wave * bpw + lane / per; u < KS * kc; u += kLayerWaves * bpw) {
+            const int sl = u / kc, b = c0 + u % kc;
+            const int sb0 = (int)((int64_t)l.kb * sl / KS), sbn = (int)((int64_t)l.kb * (sl + 1) / KS) - sb0;
+            const bool in = b < sbn;
+            float v[4][8];
+            float mx = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < spl) {
+                    load_x<XT>(x + (int64_t)sr * c.x_stride, there && in, (sb0 + b) * kTileK + (s0 + i * sstep) * 8, l.K, v[i]);
+                    if (kScaled<XT>) mx = finite_max(v[i], mx);
+                }
+            }
+            float inv = 1.0f;
+            if (kScaled<XT>) {
+                for (int d = RP; d < per; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
+                const int e = block_exponent(mx);
+                inv = ldexpf(1.0f, -e);
+                if (s0 == 0) xf[u * RP + sr] = ldexpf(1.0f, e);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < spl) {
+                    half8_t hi, lo;
+                    to_half<XT>(v[i], inv, hi, lo);
+                    const int at = (u * 16 + s0 + i * sstep) * RP + sr;
+                    xs[at] = hi;
+                    if (P == 2) xs[part + at] = lo;
+                }
+            }
+        }
+        __syncthreads();
+        const int end = min(nb, c0 + kc);
+        for (int t = c0; t < end; t += D) {
+#pragma unroll
+            for (int i = 0; i < D; ++i) {
+                if (t + i >= end) break;
+                const uint4 w4 = wq[i];
+                const TileScale<WS, GPT> ts = sq[i];
+                const size_t nx = tile0 + min(t + i + D, nb - 1);
+                wq[i] = l.w[nx * kWaveSize + lane];
+                sq[i] = load_tile_scale<WS, GPT>(l, nx * kTileN + col);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                const int u = slice * kc + t + i - c0;
+                float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                if (kScaled<XT>) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) f[q] = xf[u * RP + min(frow + q, RP - 1)];
+                }
+                float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                ZeroPair z = zero_pair(ts.z & 255u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j && j % (4 / GPT) == 0) z = zero_pair((ts.z >> (8 * (j * GPT / 4))) & 255u);
+                    const half8_t q = unpack_word(w[j], magic, z);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[p * part + (u * 16 + j * 4 + quad) * RP + arow], q,
+                                                                     sum, 0, 0, 0);
+                    if ((j + 1) % (4 / GPT) == 0) {
+                        const float s = scale_of<WS, GPT>(ts, j * GPT / 4, bf16s);
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            acc[q4] = fmaf(sum[q4], kScaled<XT> ? s * f[q4] : s, acc[q4]);
+                            sum[q4] = 0.0f;
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (KS > 1) {
+        __syncthreads();
+        if (wave) joint[(wave - 1) * kWaveSize + lane] = acc;
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int s = 0; s < KS - 1; ++s) acc += joint[s * kWaveSize + lane];
+    }
+    const int n = nt * kTileN + col;
+    if (!live || n >= l.N) return;
+    const float bias = l.bias ? l.bias[n] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = quad * 4 + i;
+        if (m < M && row_active(c.rows, m0 + m)) store_y(c, m0 + m, n, acc[i] + bias);
+    }
+}
+
+// The caller's weights, scales and zeros into the layer's tiles; features past
+// K hold q = 0 (their x is 0), features past N and groups past K scale 0.
+template <typename ST>
+__global__ __launch_bounds__(256) void k_layer_pack(Layer l, LayerSource src, uint4 *w, ST *scales, uint8_t *zeros,
+                                                     float *bias)
+{
+    const size_t nthreads = (size_t)gridDim.x * blockDim.x;
+    const size_t t0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const size_t rowb = ((size_t)l.K + 1) / 2;
+    for (size_t i = t0; i < (size_t)l.nt * l.kb * kWaveSize; i += nthreads) {
+        const int lane = (int)(i & 63);
+        const size_t tile = i >> 6;
+        const int kb = (int)(tile % l.kb);
+        const size_t n = (tile / l.kb) * kTileN + (lane & 15);
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k0 = kb * kTileK + j * 32 + (lane >> 4) * 8;
+            uint32_t v = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int k = k0 + 2 * p;
+                uint32_t byte = 0;
+                if (n < (size_t)l.N && k < l.K) byte = src.w[n * rowb + k / 2];
+                if (k + 1 >= l.K) byte &= 15u;
+                v |= (byte & 15u) << (4 * p) | (byte >> 4) << (16 + 4 * p);
+            }
+            o[j] = v;
+        }
+        w[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    const size_t ngroups = (l.K + (size_t)l.group - 1) / l.group;
+    for (size_t i = t0; i < (size_t)l.nt * l.kb * kTileN * l.gpt; i += nthreads) {
+        const int sub = (int)(i % l.gpt);
+        const size_t tile = i / l.gpt / kTileN;
+        const size_t n = tile / l.kb * kTileN + i / l.gpt % kTileN;
+        const size_t k = tile % l.kb * kTileK + sub * (kTileK / l.gpt);
+        const size_t g = k / l.group;
+        const bool in = n < (size_t)l.N && g < ngroups;
+        scales[i] = in ? ((const ST *)src.scales)[n * ngroups + g] : (ST)0.0f;
+        if (zeros) zeros[i] = in ? (src.zeros[n * ngroups + g] & 15u) : 8;
+    }
+    if (bias)
+        for (size_t i = t0; i < (size_t)l.N; i += nthreads) bias[i] = src.bias[i];
+}
+
+template <typename XT, int WS, int GPT>
+hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
+{
+    int RP = 1;
+    while (RP < std::min(c.M, kRowsM)) RP *= 2;
+    const bool split = l.nt < 2048;
+    const int KS = split ? 4 : 1, D = split ? 2 : 4;
+    // blocks of 128 features staged at a time: all, or what 40 KiB hold
+    const int longest = (l.kb + KS - 1) / KS;
+    const size_t per = (size_t)KS * RP * (256 * kParts<XT> + 4);
+    int kc = std::min<int>(longest, std::max<int>(D, (int)(40960 / per) / D * D));
+    const size_t lds = std::max<size_t>(per * kc, split ? 3 * 64 * sizeof(float4_t) : 0);
+    const dim3 b(kLayerThreads);
+    const unsigned gy = (c.M + kRowsM - 1) / kRowsM;
+    if (split)
+        hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, 4>), dim3(l.nt, gy), b, lds, s, l, c, RP, kc);
+    else
+        hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, 1>), dim3((l.nt + kLayerWaves - 1) / kLayerWaves, gy), b, lds, s, l,
+                           c, RP, kc);
+    return hipGetLastError();
+}
+
+template <typename XT>
+hipError_t layer_xt(const Layer &l, const LayerCall &c, hipStream_t s)
+{
+    if (l.scale_dtype == kF32) {
+        if (l.gpt == 1) return layer_few<XT, 4, 1>(l, c, s);
+        if (l.gpt == 2) return layer_few<XT, 4, 2>(l, c, s);
+        return layer_few<XT, 4, 4>(l, c, s);
+    }
+    if (l.gpt == 1) return layer_few<XT, 2, 1>(l, c, s);
+    if (l.gpt == 2) return layer_few<XT, 2, 2>(l, c, s);
+    return layer_few<XT, 2, 4>(l, c, s);
+}
+
+}  // namespace
+
+hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, void *scales, uint8_t *zeros,
+                             float *bias, hipStream_t s)
+{
+    const size_t items = (size_t)l.nt * l.kb * kWaveSize;
+    const dim3 g((unsigned)std::min<size_t>((items + 255) / 256, 8192)), b(256);
+    if (l.scale_dtype == kF32)
+        hipLaunchKernelGGL(k_layer_pack<float>, g, b, 0, s, l, src, w, (float *)scales, zeros, bias);
+    else if (l.scale_dtype == kF16)
+        hipLaunchKernelGGL(k_layer_pack<_Float16>, g, b, 0, s, l, src, w, (_Float16 *)scales, zeros, bias);
+    else
+        hipLaunchKernelGGL(k_layer_pack<__bf16>, g, b, 0, s, l, src, w, (__bf16 *)scales, zeros, bias);
+    return hipGetLastError();
+}
+
+hipError_t launch_layer(const Layer &l, const LayerCall &c, hipStream_t s)
+{
+    if (c.x_dtype == kF32) return layer_xt<float>(l, c, s);
+    if (c.x_dtype == kF16) return layer_xt<_Float16>(l, c, s);
+    return layer_xt<__bf16>(l, c, s);
+}
+
+}  // namespace wfst

@@ -36,20 +36,23 @@ constexpr int kTileK = 128;     // input features of one weight tile
 // for each of 64 lanes; lane l holds output feature l % 16, and its word j the
 // features k = 32 j + 8 (l / 16) .. + 7 of the tile, feature 2p in bits 4p .. 4p+3
 // and feature 2p + 1 in bits 16+4p .. 16+4p+3 (the order in which a shift and a
-// mask yield the two halves of one register). Scales and zeros are [n / 16][group][n % 16].
+// mask yield the two halves of one register). Scales and zeros come gpt to a tile
+// and feature, [n / 16][k / 128][n % 16][gpt]: 1 where groups are multiples of
+// 128 features (a scale is repeated in each of its group's tiles), 2 for groups
+// of 64, 4 (every 32 features) for all others.
 struct Layer {
     const uint4 *w;
-    const void *scales;
+    const void *scales;         // binary32, or 16 bits as the caller gave them
     const uint8_t *zeros;       // null: 8
     const float *bias;          // null: 0
-    int32_t K, N, group, ngroups, kb, nt;
+    int32_t K, N, group, gpt, kb, nt;
     int32_t scale_dtype;
 };
 
 struct LayerSource {
     const uint8_t *w;           // [N, ceil(K / 2)], feature 2i in the low half of byte i
-    const void *scales;         // [N, ngroups]
-    const uint8_t *zeros;       // [N, ngroups] or null
+    const void *scales;         // [N, ceil(K / group)]
+    const uint8_t *zeros;       // the same shape, or null
     const float *bias;          // [N] or null
 };
 

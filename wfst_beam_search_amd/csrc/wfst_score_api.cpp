@@ -165,13 +165,13 @@ extern "C" int wfst_layer_create(const wfst_layer_desc *d, int device, void *str
         l.K = (int32_t)K;
         l.N = (int32_t)N;
         l.group = d->group_size;
-        l.ngroups = (int32_t)ng;
+        l.gpt = l.group % 128 == 0 ? 1 : (l.group == 64 ? 2 : 4);
         l.kb = (int32_t)((K + kTileK - 1) / kTileK);
         l.nt = (int32_t)((N + kTileN - 1) / kTileN);
         l.scale_dtype = d->scale_dtype;
         const auto up = [](size_t b) { return (b + 255) / 256 * 256; };
         const size_t wb = (size_t)l.nt * l.kb * 1024;
-        const size_t entries = (size_t)l.nt * l.ngroups * kTileN;
+        const size_t entries = (size_t)l.nt * l.kb * kTileN * l.gpt;
         const size_t sb = up(entries * ss), zb = d->zeros ? up(entries) : 0, bb = d->bias ? up((size_t)N * 4) : 0;
         wfst_layer_s *h = new wfst_layer_s;
         hipError_t e = hipMalloc(&h->block, wb + sb + zb + bb);
