@@ -626,11 +626,14 @@ int wfst_layer_release(wfst_layer_t layer);   /* null is a no-op */
  * of exact values (a binary32 x enters as a sum of two binary16 values, off by at
  * most 2^-24 of itself or 2^-38 of the largest finite |x| among its 128
  * neighbours); infinities and NaN in x go where the formula takes them.
- * out must not overlap x. Errors: WFST_EINVAL, WFST_EDEVICE.
+ * out must not overlap x. workspace: device memory, 16-byte aligned, of at least
+ * wfst_layer_workspace's bytes (null when those are 0), in use until the stream
+ * has passed the call. Errors: WFST_EINVAL, WFST_EDEVICE.
  */
 int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_t x_stride, int32_t rows,
                       const int32_t *lengths, int32_t T, void *out, int32_t out_dtype, int64_t out_stride,
-                      void *stream);
+                      void *workspace, int64_t workspace_bytes, void *stream);
+int wfst_layer_workspace(wfst_layer_t layer, int32_t x_dtype, int32_t rows, int64_t *bytes);
 
 /*
  * out[r, :] = log_softmax(scale * x[r, :] + bias): the search's log_prob rows
@@ -639,7 +642,7 @@ int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_
  * is a device float [V] or null. Statistics are binary32. A row whose entries
  * are all -inf stays -inf; a row with a NaN or +inf becomes NaN. out may be x
  * itself (same element type and stride), otherwise it must not overlap x.
- * workspace: device memory of at least wfst_log_softmax_workspace's bytes (null
+ * workspace: device memory, 16-byte aligned, of at least wfst_log_softmax_workspace's bytes (null
  * when those are 0), in use until the stream has passed the call.
  * Errors: WFST_EINVAL, WFST_EDEVICE.
  */

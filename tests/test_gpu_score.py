@@ -81,6 +81,13 @@ def _layer_check(y, x, arrays, out):
     (2, 8200, 70, 64, "f16", "f16", "f32", True, True),
     (5, 20000, 33, 128, "f32", "f16", "f32", True, False),
     (300, 257, 515, 32, "bf16", "f16", "f16", True, True),
+    # enough workgroups of many rows
+    (17, 300, 16500, 64, "bf16", "f16", "f32", True, True),
+    (32, 130, 16400, 32, "f16", "f32", "f32", False, False),
+    (64, 390, 17001, 32, "f32", "f32", "f16", True, True),
+    (65, 1, 8200, 128, "f32", "f16", "f32", True, False),
+    (1000, 257, 1100, 96, "f16", "bf16", "bf16", True, False),
+    (777, 512, 1300, 128, "bf16", "bf16", "f32", False, True),
 ])
 def test_layer(M, K, N, group, x, scale, out, zeros, bias):
     _say("layer", M, K, N, group, x, scale, out)
@@ -135,9 +142,10 @@ def test_layer_extreme_values(x, values):
 
 def test_layer_infinities_and_nan_stay_in_their_rows():
     K, N = 300, 50
-    for x in ("f32", "f16", "bf16"):
+    for x, M in (("f32", 5), ("f16", 5), ("bf16", 5), ("f32", 2100), ("bf16", 2100)):
+        N = 50 if M == 5 else 600
         layer, arrays = _layer_arrays(11, K, N, 64, zeros=True, bias=True)
-        h = torch.randn(5, K).to(DT[x])
+        h = torch.randn(M, K).to(DT[x])
         clean = layer.logits(h.cuda())
         h[1, 17], h[3, 299], h[4, 0] = float("inf"), float("nan"), float("-inf")
         y = layer.logits(h.cuda()).cpu()
@@ -148,6 +156,20 @@ def test_layer_infinities_and_nan_stay_in_their_rows():
             assert np.array_equal(np.isnan(_np(y[r])), d == 0)
             assert (_np(y[r])[d != 0] == sign * np.sign(d[d != 0]) * np.inf).all()
         assert torch.isnan(y[3]).all()
+
+
+def test_layer_many_rows_lengths():
+    """A padded batch on the many-row path: rows behind the last frame stay as they were."""
+    K, N, B, T = 200, 1030, 9, 130
+    for x in ("f32", "bf16"):
+        layer, arrays = _layer_arrays(6, K, N, 32, bias=True, zeros=True)
+        h = torch.randn(B, T, K + 5, device="cuda").to(DT[x])[:, :, 5:]
+        L = torch.tensor([130, 0, 1, 64, 65, 129, 17, 100, 3], dtype=torch.int32, device="cuda")
+        out = torch.full((B, T, N), 5.0, device="cuda")
+        layer.logits(h, lengths=L, out=out)
+        act = torch.arange(T, device="cuda")[None] < L[:, None]
+        assert (out[~act] == 5).all()
+        _layer_check(out[act], h[act], arrays, "f32")
 
 
 def test_layer_far_rows():
@@ -171,6 +193,11 @@ def test_layer_repeats_bit_for_bit():
         assert torch.equal(a, layer.logits(h))
     # a row's result does not depend on the rows beside it
     assert torch.equal(layer.logits(h[7:8]), a[7:8])
+    layer, _ = _layer_arrays(16, 300, 17000, 32)
+    h = torch.randn(70, 300, device="cuda")
+    a = layer.logits(h)
+    for _ in range(3):
+        assert torch.equal(a, layer.logits(h))
 
 
 def test_layer_refuses():

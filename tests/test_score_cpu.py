@@ -58,7 +58,8 @@ def test_layer_create_refuses(lib, bad, word):
 
 def test_layer_calls_refuse_null(lib):
     assert lib.wfst_layer_create(None, 0, None, ctypes.byref(ctypes.c_void_p())) == EINVAL
-    assert lib.wfst_layer_logits(None, 4096, 0, 8, 1, None, 1, 4096, 0, 8, None) == EINVAL
+    assert lib.wfst_layer_logits(None, 4096, 0, 8, 1, None, 1, 4096, 0, 8, None, 0, None) == EINVAL
+    assert lib.wfst_layer_workspace(None, 0, 1, ctypes.byref(ctypes.c_int64())) == EINVAL
     assert lib.wfst_layer_release(None) == 0
 
 

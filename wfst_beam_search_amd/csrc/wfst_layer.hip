@@ -297,6 +297,205 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
     }
 }
 
+// Many rows: x is first turned into matrix operands, once, in the workspace:
+// per 16 rows and 128 features, [P][32 features][lane][8 halves] and the 16
+// scale factors. One wavefront makes one such block.
+constexpr size_t kBlockHalves = 4 * 64 * 8;            // halves of one part of a block
+
+template <typename XT>
+__global__ __launch_bounds__(256) void k_layer_operands(Layer l, LayerCall c, half8_t *xa, float *xf)
+{
+    constexpr int P = kParts<XT>;
+    const int lane = threadIdx.x & 63;
+    const int row = lane & 15, quad = lane >> 4;
+    const int64_t nblk = (int64_t)((c.M + kRowsM - 1) / kRowsM) * l.kb;
+    const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (u >= nblk) return;
+    const int64_t mt = u / l.kb;
+    const int b = (int)(u - mt * l.kb);
+    const int64_t m = mt * kRowsM + row;
+    const bool there = m < c.M && row_active(c.rows, m);
+    const XT *x = (const XT *)c.x + (there ? m : 0) * c.x_stride;
+    float v[4][8], mx = 0.0f, inv = 1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        load_x<XT>(x, there, b * kTileK + j * 32 + quad * 8, l.K, v[j]);
+        if (kScaled<XT>) mx = finite_max(v[j], mx);
+    }
+    if (kScaled<XT>) {
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        const int e = block_exponent(mx);
+        inv = ldexpf(1.0f, -e);
+        if (quad == 0) xf[u * kRowsM + row] = ldexpf(1.0f, e);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        half8_t hi, lo;
+        to_half<XT>(v[j], inv, hi, lo);
+        xa[(u * P * 4 + j) * 64 + lane] = hi;
+        if (P == 2) xa[(u * P * 4 + 4 + j) * 64 + lane] = lo;
+    }
+}
+
+// The product for many rows: a workgroup of 8 wavefronts makes 16 MT rows by 128
+// output features. Each wavefront owns 32 features; the two halves of the
+// workgroup take alternate blocks of 128 input features (joined in LDS at the
+// end), so that each wavefront's matrix instructions share every operand of x
+// read from LDS between two weight tiles. Operands of the next step are loaded
+// into registers during a step and stored into the other LDS buffer after it.
+template <typename XT, int WS, int GPT, int MT>
+__global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf)
+{
+    constexpr int P = kParts<XT>;
+    constexpr int NT = 2;
+    constexpr int kBlk = P * 4 * 64;                    // half8 of one block (16 rows, 128 features)
+    constexpr int kStep = 2 * MT * kBlk;                // half8 of one step
+    constexpr int kCopies = kStep / 512;
+    extern __shared__ __align__(16) char smem[];
+    half8_t *buf = (half8_t *)smem;                     // [2][2 halves][MT][P][4][64]
+    float *fac = (float *)(buf + 2 * kStep);            // [2][2][MT][16]
+    float4_t *joint = (float4_t *)smem;                 // [4][MT * NT][64], after the last step
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int col = lane & 15, quad = lane >> 4;
+    const int half = wave >> 2;
+    const int nt0 = blockIdx.x * 8 + (wave & 3) * NT;
+    const int mblk = blockIdx.y;
+    const int mtiles = (c.M + kRowsM - 1) / kRowsM;
+    const bool bf16s = l.scale_dtype == kBF16;
+    const uint32_t magic = magic_1024();
+    const int steps = (l.kb + 1) / 2;
+
+    // block (half h, row tile mt) of a step: clamped to one that exists
+    const auto block = [&](int step, int h, int mt) {
+        const int64_t t = min(mblk * MT + mt, mtiles - 1);
+        return t * l.kb + min(step * 2 + h, l.kb - 1);
+    };
+    half8_t reg[kCopies];
+    float freg = 1.0f;
+    const auto fetch = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int u = (i * 512 + tid) / kBlk;       // (the same for a wavefront)
+            reg[i] = xa[block(step, u / MT, u % MT) * kBlk + (i * 512 + tid) % kBlk];
+        }
+        if (kScaled<XT> && tid < 2 * MT * 16) freg = xf[block(step, tid / 16 / MT, tid / 16 % MT) * kRowsM + tid % 16];
+    };
+    const auto put = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) buf[slot * kStep + i * 512 + tid] = reg[i];
+        if (kScaled<XT> && tid < 2 * MT * 16) fac[slot * 2 * MT * 16 + tid] = freg;
+    };
+    uint4 wq[NT];
+    TileScale<WS, GPT> sq[NT];
+    const auto weights = [&](int step) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const size_t t = (size_t)min(nt0 + n, l.nt - 1) * l.kb + min(step * 2 + half, l.kb - 1);
+            wq[n] = l.w[t * kWaveSize + lane];
+            sq[n] = load_tile_scale<WS, GPT>(l, t * kTileN + col);
+        }
+    };
+
+    float4_t acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    weights(0);
+    fetch(0);
+    put(0);
+    __syncthreads();
+    for (int step = 0; step < steps; ++step) {
+        const int slot = step & 1;
+        uint4 w4[NT];
+        TileScale<WS, GPT> ts[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) { w4[n] = wq[n]; ts[n] = sq[n]; }
+        if (step + 1 < steps) {
+            weights(step + 1);
+            fetch(step + 1);
+        }
+        if (step * 2 + half < l.kb) {
+            const half8_t *a0 = buf + slot * kStep + half * MT * kBlk + lane;
+            float4_t tile[MT][NT], sum[MT][NT];
+            ZeroPair z[NT];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool first = j % (4 / GPT) == 0, last = (j + 1) % (4 / GPT) == 0;
+                half8_t q[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (first) z[n] = zero_pair((ts[n].z >> (8 * (j * GPT / 4))) & 255u);
+                    const uint32_t w = j == 0 ? w4[n].x : j == 1 ? w4[n].y : j == 2 ? w4[n].z : w4[n].w;
+                    q[n] = unpack_word(w, magic, z[n]);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const half8_t a = a0[m * kBlk + (p * 4 + j) * 64];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if (first && p == 0) sum[m][n] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+                            sum[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[n], sum[m][n], 0, 0, 0);
+                        }
+                    }
+                }
+                if (last) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float s = scale_of<WS, GPT>(ts[n], j * GPT / 4, bf16s);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (!kScaled<XT>) acc[m][n][i] = fmaf(sum[m][n][i], s, acc[m][n][i]);
+                                else if (j < 4 / GPT) tile[m][n][i] = sum[m][n][i] * s;
+                                else tile[m][n][i] = fmaf(sum[m][n][i], s, tile[m][n][i]);
+                            }
+                    }
+                }
+            }
+            if (kScaled<XT>) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const float4_t f = *(const float4_t *)(fac + ((slot * 2 + half) * MT + m) * 16 + quad * 4);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][n][i] = fmaf(tile[m][n][i], f[i], acc[m][n][i]);
+                }
+            }
+        }
+        if (step + 1 < steps) put(slot ^ 1);
+        __syncthreads();
+    }
+    if (half) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) joint[((wave & 3) * MT * NT + m * NT + n) * 64 + lane] = acc[m][n];
+    }
+    __syncthreads();
+    if (half) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int f = (nt0 + n) * kTileN + col;
+        if (nt0 + n >= l.nt || f >= l.N) continue;
+        const float bias = l.bias ? l.bias[f] : 0.0f;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float4_t y = acc[m][n] + joint[((wave & 3) * MT * NT + m * NT + n) * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = ((int64_t)mblk * MT + m) * kRowsM + quad * 4 + i;
+                if (r < c.M && row_active(c.rows, r)) store_y(c, r, f, y[i] + bias);
+            }
+        }
+    }
+}
+
 // The caller's weights, scales and zeros into the layer's tiles; features past
 // K hold q = 0 (their x is 0), features past N and groups past K scale 0.
 template <typename ST>
@@ -365,17 +564,55 @@ hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
     return hipGetLastError();
 }
 
+// Row tiles of 16 a workgroup of k_layer_many takes (2 or 4); 0: the rows are few,
+// or the workgroups would be too few to fill the card, and k_layer_few serves.
+int many_tiles(const Layer &l, int32_t rows)
+{
+    if (rows <= kRowsM) return 0;
+    const int mt = rows <= 2 * kRowsM ? 2 : 4;
+    const int64_t groups = (int64_t)((l.nt + 7) / 8) * ((rows + mt * kRowsM - 1) / (mt * kRowsM));
+    return groups >= 128 ? mt : 0;
+}
+
+size_t operand_bytes(const Layer &l, int32_t rows, int32_t x_dtype)
+{
+    const size_t blocks = (size_t)((rows + kRowsM - 1) / kRowsM) * l.kb;
+    return blocks * kBlockHalves * 2 * (x_dtype == kF32 ? 2 : 1);
+}
+
+template <typename XT, int WS, int GPT, int MT>
+hipError_t layer_many(const Layer &l, const LayerCall &c, hipStream_t s)
+{
+    const int64_t blocks = (int64_t)((c.M + kRowsM - 1) / kRowsM) * l.kb;
+    half8_t *xa = (half8_t *)c.workspace;
+    float *xf = (float *)((char *)c.workspace + operand_bytes(l, c.M, c.x_dtype));
+    hipLaunchKernelGGL(k_layer_operands<XT>, dim3((unsigned)((blocks + 3) / 4)), dim3(256), 0, s, l, c, xa, xf);
+    const size_t lds = 2 * 2 * MT * (kParts<XT> * kBlockHalves * 2 + 64);
+    const dim3 g((l.nt + 7) / 8, (c.M + MT * kRowsM - 1) / (MT * kRowsM));
+    hipLaunchKernelGGL((k_layer_many<XT, WS, GPT, MT>), g, dim3(512), lds, s, l, c, (const half8_t *)xa, (const float *)xf);
+    return hipGetLastError();
+}
+
+template <typename XT, int WS, int GPT>
+hipError_t layer_rows(const Layer &l, const LayerCall &c, hipStream_t s)
+{
+    const int mt = many_tiles(l, c.M);
+    if (mt == 4) return layer_many<XT, WS, GPT, 4>(l, c, s);
+    if (mt == 2) return layer_many<XT, WS, GPT, 2>(l, c, s);
+    return layer_few<XT, WS, GPT>(l, c, s);
+}
+
 template <typename XT>
 hipError_t layer_xt(const Layer &l, const LayerCall &c, hipStream_t s)
 {
     if (l.scale_dtype == kF32) {
-        if (l.gpt == 1) return layer_few<XT, 4, 1>(l, c, s);
-        if (l.gpt == 2) return layer_few<XT, 4, 2>(l, c, s);
-        return layer_few<XT, 4, 4>(l, c, s);
+        if (l.gpt == 1) return layer_rows<XT, 4, 1>(l, c, s);
+        if (l.gpt == 2) return layer_rows<XT, 4, 2>(l, c, s);
+        return layer_rows<XT, 4, 4>(l, c, s);
     }
-    if (l.gpt == 1) return layer_few<XT, 2, 1>(l, c, s);
-    if (l.gpt == 2) return layer_few<XT, 2, 2>(l, c, s);
-    return layer_few<XT, 2, 4>(l, c, s);
+    if (l.gpt == 1) return layer_rows<XT, 2, 1>(l, c, s);
+    if (l.gpt == 2) return layer_rows<XT, 2, 2>(l, c, s);
+    return layer_rows<XT, 2, 4>(l, c, s);
 }
 
 }  // namespace
@@ -392,6 +629,13 @@ hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, v
     else
         hipLaunchKernelGGL(k_layer_pack<__bf16>, g, b, 0, s, l, src, w, (__bf16 *)scales, zeros, bias);
     return hipGetLastError();
+}
+
+size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype)
+{
+    if (!many_tiles(l, rows)) return 0;
+    const size_t blocks = (size_t)((rows + kRowsM - 1) / kRowsM) * l.kb;
+    return operand_bytes(l, rows, x_dtype) + (x_dtype == kF16 ? 0 : blocks * kRowsM * 4);
 }
 
 hipError_t launch_layer(const Layer &l, const LayerCall &c, hipStream_t s)

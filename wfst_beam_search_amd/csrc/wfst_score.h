@@ -63,8 +63,10 @@ struct LayerCall {
     int32_t M;
     int32_t x_dtype, out_dtype;
     RowSet rows;
+    void *workspace;            // layer_workspace bytes
 };
 
+size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype);
 hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, void *scales, uint8_t *zeros,
                              float *bias, hipStream_t s);
 hipError_t launch_layer(const Layer &l, const LayerCall &c, hipStream_t s);

@@ -108,9 +108,9 @@ int check_stream(void *stream, int device)
     return WFST_OK;
 }
 
-int check_aligned(const void *p, size_t elem, const char *what)
+int check_aligned(const void *p, size_t align, const char *what)
 {
-    if ((uintptr_t)p % elem) return api_fail(WFST_EINVAL, std::string(what) + " is not aligned to its elements");
+    if ((uintptr_t)p % align) return api_fail(WFST_EINVAL, std::string(what) + " is not aligned");
     return WFST_OK;
 }
 
@@ -126,6 +126,19 @@ int check_lengths(const int32_t *lengths, int64_t rows, int32_t T, int device)
     if (T < 1 || rows % T) return api_fail(WFST_EINVAL, "with lengths, rows must be a multiple of T >= 1");
     TRY(check_aligned(lengths, 4, "lengths"));
     return api_check_buffer(lengths, (size_t)(rows / T) * 4, device, "lengths");
+}
+
+int check_workspace(const void *w, int64_t bytes, size_t need, int device, const void *x, int64_t xb, const void *out,
+                    int64_t ob)
+{
+    if (!need) return WFST_OK;
+    if (!w || bytes < 0 || (size_t)bytes < need)
+        return api_fail(WFST_EINVAL, "workspace must hold " + std::to_string(need) + " bytes");
+    TRY(check_aligned(w, 16, "workspace"));
+    TRY(api_check_buffer(w, need, device, "workspace"));
+    if (ranges_meet(w, (int64_t)need, out, ob) || ranges_meet(w, (int64_t)need, x, xb))
+        return api_fail(WFST_EINVAL, "workspace must not overlap the input or the output");
+    return WFST_OK;
 }
 
 }  // namespace
@@ -217,9 +230,20 @@ extern "C" int wfst_layer_release(wfst_layer_t layer)
     });
 }
 
+extern "C" int wfst_layer_workspace(wfst_layer_t layer, int32_t x_dtype, int32_t rows, int64_t *bytes)
+{
+    return guarded([&]() -> int {
+        if (!layer || !bytes) return api_fail(WFST_EINVAL, "a pointer is null");
+        if (!dtype_ok(x_dtype)) return api_fail(WFST_EINVAL, "not an element type");
+        if (rows < 0 || rows > (1 << 20) - 16) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^20 - 16]");
+        *bytes = (int64_t)layer_workspace(layer->l, rows, x_dtype);
+        return WFST_OK;
+    });
+}
+
 extern "C" int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_t x_stride, int32_t rows,
                                  const int32_t *lengths, int32_t T, void *out, int32_t out_dtype, int64_t out_stride,
-                                 void *stream)
+                                 void *workspace, int64_t workspace_bytes, void *stream)
 {
     return guarded([&]() -> int {
         if (!layer) return api_fail(WFST_EINVAL, "layer is null");
@@ -242,7 +266,8 @@ extern "C" int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dt
         TRY(check_lengths(lengths, rows, T, layer->device));
         TRY(check_stream(stream, layer->device));
         if (ranges_meet(x, xb, out, ob)) return api_fail(WFST_EINVAL, "out must not overlap x");
-        const LayerCall c{x, out, x_stride, out_stride, rows, x_dtype, out_dtype, {lengths, T}};
+        TRY(check_workspace(workspace, workspace_bytes, layer_workspace(l, rows, x_dtype), layer->device, x, xb, out, ob));
+        const LayerCall c{x, out, x_stride, out_stride, rows, x_dtype, out_dtype, {lengths, T}, workspace};
         HIP_TRY(launch_layer(l, c, (hipStream_t)stream));
         return WFST_OK;
     });
@@ -283,15 +308,8 @@ extern "C" int wfst_log_softmax(const void *x, int32_t x_dtype, int64_t x_stride
             return api_fail(WFST_EINVAL, "out must be x itself (same type and stride) or not overlap it");
         if (bias && ranges_meet(bias, (int64_t)V * 4, out, ob))
             return api_fail(WFST_EINVAL, "out must not overlap bias");
-        const size_t need = norm_workspace(rows, V, x_dtype, out_dtype);
-        if (need) {
-            if (!workspace || workspace_bytes < 0 || (size_t)workspace_bytes < need)
-                return api_fail(WFST_EINVAL, "workspace must hold " + std::to_string(need) + " bytes");
-            TRY(check_aligned(workspace, 4, "workspace"));
-            TRY(api_check_buffer(workspace, need, device, "workspace"));
-            if (ranges_meet(workspace, (int64_t)need, out, ob) || ranges_meet(workspace, (int64_t)need, x, xb))
-                return api_fail(WFST_EINVAL, "workspace must not overlap x or out");
-        }
+        TRY(check_workspace(workspace, workspace_bytes, norm_workspace(rows, V, x_dtype, out_dtype), device, x, xb, out,
+                            ob));
         const NormCall c{x, out, bias, x_stride, out_stride, rows, V, x_dtype, out_dtype, scale, {lengths, T}, workspace};
         HIP_TRY(launch_log_softmax(c, (hipStream_t)stream));
         return WFST_OK;

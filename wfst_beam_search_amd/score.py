@@ -215,6 +215,7 @@ class OutputLayer:
         _check(lib.wfst_layer_create(ctypes.byref(desc), device.index, raw, ctypes.byref(h)))
         self.handle = h
         self._logits = lib.wfst_layer_logits
+        self._bytes = {}                        # (element type, rows) -> workspace bytes
         self.device = device
         self.in_features, self.out_features = K, N
 
@@ -232,8 +233,16 @@ class OutputLayer:
         lengths, T = _lengths(lengths, lead, self.device, other)
         out = _out(out, (*lead, self.out_features), _named(dtype), self.device, other)
         _, ostep = _rows(out, "out")
+        need = self._bytes.get((code, rows))
+        if need is None:
+            n = ctypes.c_int64(0)
+            _check(load_library().wfst_layer_workspace(self.handle, code, rows, ctypes.byref(n)))
+            if len(self._bytes) > 256:
+                self._bytes.clear()
+            need = self._bytes[code, rows] = n.value
+        work = _workspace(need, self.device, other)
         _check(self._logits(self.handle, hidden.data_ptr(), code, step, rows, _p(lengths), T, out.data_ptr(),
-                            DTYPES[dtype], ostep, raw))
+                            DTYPES[dtype], ostep, _p(work), need, raw))
         return out
 
     def log_probs(self, hidden, dtype: str = "f32", scale: float = 1.0, bias=None, lengths=None, out=None,
