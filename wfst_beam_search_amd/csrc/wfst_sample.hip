@@ -8,20 +8,18 @@ namespace wfst {
 // top_p of theirs, of these the ones with mass >= min_p. The token is the first
 // kept i, in index order, whose running mass exceeds u times the kept mass.
 //
-// Every rule cuts at a value: the kept set is {key > tau} and the first r
-// entries with key == tau, key being the score's bits in an order that integers
-// compare. tau is found by digit (8 bits of the key at a time) from histograms
-// of counts (top_k) or masses (top_p); nothing is sorted. Masses are computed in
-// binary64 and summed as integers of 2^-bits, so sums do not depend on the order
-// in which threads add, and a draw falls on the side of a border that the exact
-// sums give except within about 2^-45 of it.
+// Nothing is sorted. Labels are ordered by one integer, (max key - key) << bits
+// of an index | index, key being the score's bits in an order that integers
+// compare: top_k and top_p each cut at one value of it, `last`, found digit by
+// digit (8 bits at a time) from histograms of counts or masses. Masses are
+// binary64 powers rounded to multiples of 2^-unit and added as integers, so no
+// sum depends on the order in which threads add, sums of any two groupings
+// agree, and a draw falls on the exact sums' side of a border except within
+// about 2^-45 of it.
 
 namespace {
 
-constexpr int kSampleThreads = 1024;
-constexpr int kSampleWaves = kSampleThreads / kWaveSize;
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
-constexpr uint32_t kKeyPosInf = 0xFF800000u;
 
 // Integers that compare as the scores do; -0 as +0, NaN as -inf.
 __device__ __forceinline__ uint32_t score_key(float x)
@@ -36,33 +34,177 @@ __device__ __forceinline__ float key_score(uint32_t k)
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// 2^t for t <= 0, relative error below 2^-51: the nearest integer leaves f in
+// [-1/2, 1/2], a polynomial of degree 10 (interpolating 2^f at Chebyshev nodes)
+// gives 2^f, and the integer is added to its exponent. Below 2^-1000: 2^-1000.
+__device__ __forceinline__ double exp2_neg(double t)
+{
+    t = fmax(t, -1000.0);
+    const double shift = 6755399441055744.0;           // 1.5 * 2^52: adding it rounds to an integer
+    const double r = t + shift;
+    const double f = t - (r - shift);
+    double p = 7.072585949269224e-09;
+    p = fma(p, f, 1.0208690299958306e-07);
+    p = fma(p, f, 1.321544258792169e-06);
+    p = fma(p, f, 1.5252657260200837e-05);
+    p = fma(p, f, 1.540353044173605e-04);
+    p = fma(p, f, 1.3333558230164974e-03);
+    p = fma(p, f, 9.618129107606888e-03);
+    p = fma(p, f, 5.550410866444772e-02);
+    p = fma(p, f, 2.4022650695910097e-01);
+    p = fma(p, f, 6.9314718055995e-01);
+    p = fma(p, f, 1.0);
+    const long long n = __double_as_longlong(r);       // its low bits hold the integer
+    return __longlong_as_double(__double_as_longlong(p) + (n << 52));
+}
+
+// The mass of a score, times 2^unit.
 struct MassOf {
-    double m, t;       // the row's maximum, the temperature
-    double unit;       // 2^bits
-    bool inf;          // the maximum is +inf: only +inf has mass
-    __device__ __forceinline__ double operator()(uint32_t key) const
+    double m, a;       // the row's maximum; log2(e) / T
+    double one;        // 2^unit
+    double lim;        // min_p * 2^unit (0: no limit)
+    bool inf;          // the maximum is +inf: only +inf is valid, all masses alike
+
+    __device__ __forceinline__ bool valid(float x) const { return inf ? x == INFINITY : x > -INFINITY; }
+    __device__ __forceinline__ double operator()(float x) const
     {
-        if (inf) return key == kKeyPosInf ? 1.0 : 0.0;
-        if (key <= kKeyNegInf) return 0.0;
-        return exp(((double)key_score(key) - m) / t);
+        return inf ? one : exp2_neg(((double)x - m) * a) * one;
     }
-    __device__ __forceinline__ uint64_t fixed(uint32_t key) const { return (uint64_t)rint((*this)(key) * unit); }
+    // As an integer (one < 2^52, so that adding 2^52 leaves it in the low bits).
+    static __device__ __forceinline__ uint64_t fixed(double w)
+    {
+        return (uint64_t)__double_as_longlong(w + 4503599627370496.0) - 0x4330000000000000ull;
+    }
 };
 
-template <typename XT>
-__global__ __launch_bounds__(kSampleThreads) void k_sample(SampleCall c, int bits)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v)
 {
-    __shared__ unsigned long long hmass[256];
-    __shared__ uint32_t hcnt[256];
-    __shared__ unsigned long long wsum[kSampleWaves + 1];
-    __shared__ uint32_t wcnt[kSampleWaves], wtie[kSampleWaves];
-    __shared__ uint32_t sel[4];
-    __shared__ unsigned long long selm[2];
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+    return (uint64_t)hi << 32 | lo;
+}
+
+// Inclusive running sum over the wavefront (all lanes active).
+__device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v)
+{
+    v += dpp_u64<0x111, 0xf>(v);
+    v += dpp_u64<0x112, 0xf>(v);
+    v += dpp_u64<0x114, 0xf>(v);
+    v += dpp_u64<0x118, 0xf>(v);
+    v += dpp_u64<0x142, 0xa>(v);
+    v += dpp_u64<0x143, 0xc>(v);
+    return v;
+}
+
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+    return (uint64_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) { return lane_u64(wave_scan_u64(v), 63); }
+
+// Histograms of 256 digits, three in turn: a round adds to one while the next is
+// cleared, and the third may still be read by wavefronts of the round before.
+struct Hist {
+    unsigned long long mass[3][256];
+    uint32_t cnt[3][256];
+};
+
+template <int THREADS>
+__device__ __forceinline__ void clear_hist(Hist &h, int slot)
+{
+    for (int i = threadIdx.x; i < 256; i += THREADS) { h.mass[slot][i] = 0; h.cnt[slot][i] = 0; }
+}
+
+// The value `last` at which the elements, taken in ascending order of their
+// 64-bit numbers, reach `target` (in counts, or in masses): the one that
+// reaches it and all before are <= last. each(f) calls f(number, mass) for the
+// thread's elements; numbers are unique or `enough` ends the search. digits:
+// the position of the highest bit set in any number, plus one. `skip`: numbers
+// hold nothing between bits `skip_to` and `skip`. `round` counts the histograms
+// used in this workgroup; its slot is clear on entry and on return.
+// With `enough`, counts: also ends when at most that many are <= last.
+template <int THREADS, bool MASS, typename Each>
+__device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each each, int digits, uint64_t target,
+                                                uint64_t enough)
+{
+    const int lane = threadIdx.x & 63;
+    uint64_t prefix = 0, above = 0;
+    int shift = digits;                                // the digits above it are fixed
+    for (;;) {
+        const int width = min(8, shift), next = shift - width;
+        const int slot = round % 3;
+        clear_hist<THREADS>(h, (round + 1) % 3);
+        each([&](uint64_t num, uint64_t w) {
+            if ((shift >= 64 ? 0 : num >> shift) == prefix) {
+                const uint32_t d = (uint32_t)(num >> next) & ((1u << width) - 1u);
+                atomicAdd(&h.cnt[slot][d], 1u);
+                if (MASS) atomicAdd(&h.mass[slot][d], (unsigned long long)w);
+            }
+        });
+        __syncthreads();
+        ++round;
+        // every wavefront finds the digit: four to a lane
+        uint32_t c[4];
+        uint64_t w[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = h.cnt[slot][lane * 4 + i];
+            w[i] = MASS ? (uint64_t)h.mass[slot][lane * 4 + i] : c[i];
+            sum += w[i];
+        }
+        uint64_t acc = above + wave_scan_u64(sum) - sum;
+        int d = 4;
+        uint64_t before = 0, mine = 0;
+        uint32_t count = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (d == 4 && acc + w[i] >= target) { d = i; before = acc; mine = w[i]; count = c[i]; }
+            acc += w[i];
+        }
+        const uint64_t hit = __ballot(d < 4);
+        const int src = hit ? __ffsll((unsigned long long)hit) - 1 : 63;     // (targets never pass the total)
+        const uint32_t digit = __builtin_amdgcn_readlane(src * 4 + d, src);
+        before = lane_u64(before, src);
+        mine = lane_u64(mine, src);
+        count = __builtin_amdgcn_readlane(count, src);
+        prefix = prefix << width | (digit & 255u);
+        above = before;
+        shift = next;
+        const bool whole = !MASS && above + mine <= enough;
+        if (count <= 1 || whole || shift == 0) return ((prefix + 1) << shift) - 1;
+    }
+}
+
+// What a workgroup of THREADS threads keeps of a row. HOLD: the row itself, E
+// scores a thread (rows of at most E * THREADS labels); otherwise the list of
+// labels that may be kept, E a thread.
+template <int THREADS, int E, bool HOLD> struct DrawShared {
+    Hist hist;
+    unsigned long long sum[THREADS / 64 + 1];
+    uint32_t a[THREADS / 64], b[THREADS / 64];
+    uint32_t count, first;
+    unsigned long long list[HOLD ? 1 : E * THREADS];
+};
+
+template <typename XT, int THREADS, int E, bool HOLD>
+__global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ibits)
+{
+    constexpr int WAVES = THREADS / 64;
+    constexpr int VEC = 16 / sizeof(XT);
+    constexpr int kStepW = 64 * VEC;                   // labels a wavefront takes at once
+    constexpr int kCap = E * THREADS;
+    __shared__ DrawShared<THREADS, E, HOLD> s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int V = c.V;
     // each wavefront owns one contiguous piece of the row
-    const int seg = ((V + kSampleThreads - 1) / kSampleThreads) * kWaveSize;
+    const int seg = (V + WAVES * kStepW - 1) / (WAVES * kStepW) * kStepW;
     const int v0 = min(V, wave * seg), v1 = min(V, v0 + seg);
+    uint32_t round = 0;
+    clear_hist<THREADS>(s.hist, 0);
 
     for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
         if (!row_active(c.set, r)) continue;
@@ -74,223 +216,421 @@ __global__ __launch_bounds__(kSampleThreads) void k_sample(SampleCall c, int bit
         const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
         const bool greedy = !(T > 0.0f);
 
-        uint32_t kmax = 0, valid = 0;
-        for (int v = v0 + lane; v < v1; v += kWaveSize) {
-            const uint32_t k = score_key((float)x[v]);
-            kmax = max(kmax, k);
-            valid += k > kKeyNegInf;
-        }
+        // labels v .. v + VEC - 1 of the row (-inf past its end)
+        const auto load = [&](int v, float (&y)[VEC]) {
+            if (v + VEC <= V) {
+                const Pack<XT, VEC> p = *(const Pack<XT, VEC> *)(x + v);
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) kmax = max(kmax, (uint32_t)__shfl_xor((int)kmax, d, 64));
-        valid = wave_sum_t(valid);
-        if (lane == 0) { wcnt[wave] = valid; wtie[wave] = kmax; }
-        __syncthreads();
-        kmax = 0;
-        valid = 0;
-        for (int w = 0; w < kSampleWaves; ++w) { kmax = max(kmax, wtie[w]); valid += wcnt[w]; }
-        __syncthreads();
-        if (valid == 0) {
-            if (tid == 0) {
-                c.token[r] = -1;
-                if (c.log_prob) c.log_prob[r] = -INFINITY;
-                if (c.kept) c.kept[r] = 0;
+                for (int j = 0; j < VEC; ++j) y[j] = (float)p.v[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[j] = v + j < V ? (float)x[v + j] : -INFINITY;
             }
+        };
+        const auto emit = [&](int token, float lp, uint32_t kept) {
+            c.token[r] = token;
+            if (c.log_prob) c.log_prob[r] = lp;
+            if (c.kept) c.kept[r] = (int32_t)kept;
+        };
+
+        // the row's largest score, and each thread's own
+        float own = -INFINITY;
+#pragma unroll 4
+        for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+            float y[VEC];
+            load(v, y);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) own = fmaxf(own, y[j]);       // (NaN leaves it)
+        }
+        float top = wave_max_f(own);
+        if (WAVES > 1) {
+            if (lane == 0) s.a[wave] = __float_as_uint(top);
+            if (tid == 0) { s.count = 0; s.first = 0xFFFFFFFFu; }
+            __syncthreads();
+            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, __uint_as_float(s.a[w]));
+        } else if (tid == 0) {
+            s.count = 0;
+            s.first = 0xFFFFFFFFu;
+        }
+        if (top == -INFINITY) {
+            if (tid == 0) emit(-1, -INFINITY, 0);
             continue;
         }
-        if (kmax == kKeyPosInf) {                  // +inf scores leave only each other
-            uint32_t n = 0;
-            for (int v = v0 + lane; v < v1; v += kWaveSize) n += score_key((float)x[v]) == kKeyPosInf;
-            n = wave_sum_t(n);
-            if (lane == 0) wcnt[wave] = n;
+        if (greedy) {
+            // the first label with the largest score
             __syncthreads();
-            valid = 0;
-            for (int w = 0; w < kSampleWaves; ++w) valid += wcnt[w];
-            __syncthreads();
-        }
-        MassOf mass;
-        mass.m = (double)key_score(kmax);
-        mass.t = greedy ? 1.0 : (double)T;
-        mass.unit = (double)(1ull << bits);
-        mass.inf = kmax == kKeyPosInf;
-
-        // tau = 0, ties = 0: nothing cut yet (every valid key lies above tau)
-        uint32_t tau = mass.inf ? kKeyPosInf - 1u : kKeyNegInf, ties = 0;
-        for (int rule = 0; rule < 2; ++rule) {
-            uint64_t target;     // rule 0: entries to keep, rule 1: mass to reach
-            if (rule == 0) {
-                const uint32_t k = greedy ? 1u : (topk > 0 ? (uint32_t)topk : 0u);
-                if (k == 0 || k >= valid) continue;
-                target = k;
-            } else {
-                if (greedy || !(topp < 1.0f)) continue;
-                // the mass kept so far
-                uint64_t z = 0;
-                for (int v = v0 + lane; v < v1; v += kWaveSize) {
-                    const uint32_t k = score_key((float)x[v]);
-                    if (k > tau) z += mass.fixed(k);
-                }
-                z = wave_sum_t((unsigned long long)z);
-                if (lane == 0) wsum[wave] = z;
-                __syncthreads();
-                z = 0;
-                for (int w = 0; w < kSampleWaves; ++w) z += wsum[w];
-                if (ties) z += (uint64_t)ties * mass.fixed(tau);
-                const double want = ceil((double)topp * (double)z);
-                target = want >= 1.0 ? (uint64_t)want : 1ull;
-                if (target > z) target = z;
-                __syncthreads();
-            }
-            // digits of tau from the top; `above` is what lies over the digits found so far
-            const uint32_t tau0 = tau, ties0 = ties;
-            const uint64_t tiemass0 = ties0 ? mass.fixed(tau0) : 0;
-            uint32_t prefix = 0;
-            uint64_t above = 0;
-            uint64_t unit_w = 0;
-            uint32_t nlast = 0;
-            for (int shift = 24; shift >= 0; shift -= 8) {
-                for (int i = tid; i < 256; i += kSampleThreads) { hmass[i] = 0; hcnt[i] = 0; }
-                __syncthreads();
-                for (int v = v0 + lane; v < v1; v += kWaveSize) {
-                    const uint32_t k = score_key((float)x[v]);
-                    if (k > tau0 && (shift == 24 || (k >> (shift + 8)) == prefix)) {
-                        const uint32_t d = (k >> shift) & 255u;
-                        atomicAdd(&hcnt[d], 1u);
-                        if (rule == 1) atomicAdd(&hmass[d], (unsigned long long)mass.fixed(k));
-                    }
-                }
-                // the ties that an earlier rule kept
-                if (tid == 0 && ties0 && (shift == 24 || (tau0 >> (shift + 8)) == prefix)) {
-                    atomicAdd(&hcnt[(tau0 >> shift) & 255u], ties0);
-                    if (rule == 1) atomicAdd(&hmass[(tau0 >> shift) & 255u], (unsigned long long)(ties0 * tiemass0));
-                }
-                __syncthreads();
-                if (tid == 0) {
-                    uint64_t acc = above;
-                    int d = 255;
-                    for (; d > 0; --d) {
-                        const uint64_t w = rule == 0 ? hcnt[d] : hmass[d];
-                        if (acc + w >= target) break;
-                        acc += w;
-                    }
-                    sel[0] = (uint32_t)d;
-                    sel[1] = hcnt[d];
-                    selm[0] = acc;
-                    selm[1] = rule == 0 ? hcnt[d] : hmass[d];
-                }
-                __syncthreads();
-                prefix = prefix << 8 | sel[0];
-                nlast = sel[1];
-                above = selm[0];
-                unit_w = selm[1];
-                __syncthreads();
-            }
-            tau = prefix;
-            // nlast equal entries of one mass each: the fewest that reach the target
-            const uint64_t each = rule == 0 ? 1 : (nlast ? unit_w / nlast : 0);
-            uint64_t need = each ? (target - above + each - 1) / each : nlast;
-            if (need < 1) need = 1;
-            ties = (uint32_t)(need < nlast ? need : nlast);
-        }
-
-        // kept mass, count and equal entries of each wavefront's piece
-        const bool cut = !greedy && minp > 0.0f;
-        const double lim = minp < 1.0f ? (double)minp : 1.0;
-        uint64_t z = 0;
-        uint32_t cnt = 0, tie = 0;
-        for (int v = v0 + lane; v < v1; v += kWaveSize) {
-            const uint32_t k = score_key((float)x[v]);
-            if (k < tau || k <= kKeyNegInf) continue;
-            if (k == tau) { ++tie; continue; }
-            const double w = mass(k);
-            if (cut && !(w >= lim)) continue;
-            z += (uint64_t)rint(w * mass.unit);
-            ++cnt;
-        }
-        z = wave_sum_t((unsigned long long)z);
-        cnt = wave_sum_t(cnt);
-        tie = wave_sum_t(tie);
-        if (lane == 0) { wsum[wave] = z; wcnt[wave] = cnt; wtie[wave] = tie; }
-        __syncthreads();
-        if (tid == 0) {
-            const double wt = mass(tau);
-            const bool tie_ok = ties && !(cut && !(wt >= lim));
-            const uint64_t ft = (uint64_t)rint(wt * mass.unit);
-            uint32_t left = tie_ok ? ties : 0, total = 0;
-            uint64_t acc = 0;
-            for (int w = 0; w < kSampleWaves; ++w) {      // wsum: mass before the piece; wtie: ties it keeps
-                const uint32_t t = min(left, wtie[w]);
-                left -= t;
-                const uint64_t mine = wsum[w] + t * ft;
-                total += wcnt[w] + t;
-                wtie[w] = t;
-                wsum[w] = acc;
-                acc += mine;
-            }
-            wsum[kSampleWaves] = acc;
-            double want = (double)c.u[r];
-            want = want > 0.0 ? floor(want * (double)acc) : 0.0;
-            uint64_t t64 = want >= (double)acc ? acc - 1 : (uint64_t)want;
-            if (t64 > acc - 1) t64 = acc - 1;
-            selm[0] = t64;
-            selm[1] = ft;
-            sel[2] = total;
-        }
-        __syncthreads();
-        const uint64_t want = selm[0], total = wsum[kSampleWaves], ft = selm[1];
-        if (wsum[wave] <= want && want < wsum[wave + 1]) {   // exactly one wavefront: its piece holds the token
-            uint64_t base = wsum[wave];
-            uint32_t left = wtie[wave];
-            for (int vb = v0; vb < v1; vb += kWaveSize) {
-                const int v = vb + lane;
-                const uint32_t k = v < v1 ? score_key((float)x[v]) : 0u;
-                const bool is_tie = v < v1 && k == tau && k > kKeyNegInf;
-                const unsigned long long tm = __ballot(is_tie);
-                const uint32_t rank = __popcll(tm & ((1ull << lane) - 1ull));
-                uint64_t w = 0;
-                if (is_tie) w = rank < left ? ft : 0;
-                else if (v < v1 && k > tau && k > kKeyNegInf) {
-                    const double d = mass(k);
-                    if (!(cut && !(d >= lim))) w = (uint64_t)rint(d * mass.unit);
-                }
-                uint64_t run = w;
+            for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+                float y[VEC];
+                load(v, y);
+                uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
-                for (int d = 1; d < 64; d <<= 1) {
-                    const unsigned long long o = __shfl_up((unsigned long long)run, d, 64);
-                    if (lane >= d) run += o;
+                for (int j = VEC - 1; j >= 0; --j)
+                    if (y[j] == top) at = v + j;
+                if (at != 0xFFFFFFFFu) atomicMin(&s.first, at);
+                if (__ballot(at != 0xFFFFFFFFu)) break;
+            }
+            __syncthreads();
+            if (tid == 0) emit((int)s.first, 0.0f, 1);
+            continue;
+        }
+
+        MassOf mass;
+        mass.one = (double)(1ull << unit);
+        mass.m = (double)top;
+        mass.a = 1.4426950408889634 / (double)T;
+        mass.inf = top == INFINITY;
+        mass.lim = minp > 0.0f ? (minp < 1.0f ? (double)minp : 1.0) * mass.one : 0.0;
+        const uint32_t kmax = score_key(top);
+        const bool cut_k = topk > 0 && topk < V, cut_p = topp < 1.0f;
+        const auto number = [&](float y, uint32_t i) {
+            return (uint64_t)(kmax - score_key(y)) << ibits | i;
+        };
+        uint64_t last = ~0ull;                         // kept: number <= last
+        uint64_t el[E], ew[E];                         // the thread's elements: number, mass
+        bool listed = HOLD;                            // the kept labels are all among the elements
+        int digits = ibits + 32;
+
+        if (cut_k || cut_p) {
+            uint64_t z = 0;                            // mass of all valid labels (top_p without top_k)
+            bool have_z = false;
+            if (HOLD) {
+#pragma unroll
+                for (int i = 0; i < E / VEC; ++i) {
+                    const int v = (i * THREADS + tid) * VEC;
+                    float y[VEC];
+                    if (v < V) load(v, y);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const bool ok = v < V && mass.valid(y[j]);
+                        el[i * VEC + j] = ok ? number(y[j], v + j) : ~0ull;
+                        ew[i * VEC + j] = ok ? MassOf::fixed(mass(y[j])) : 0;
+                    }
                 }
-                const unsigned long long hit = __ballot(base + run > want);
+            } else {
+                // A bound that at least `want` threads' largest scores reach: the labels that reach it are
+                // that many or more, and among random ones not many more than that
+                const uint32_t want = cut_k ? (uint32_t)topk : THREADS * 3 / 4;
+                if (want <= THREADS * 7 / 8) {
+                    const uint32_t mine = mass.valid(own) ? kmax - score_key(own) : 0xFFFFFFFFu;
+                    uint32_t far = mine == 0xFFFFFFFFu ? 0 : mine, n = __popcll(__ballot(mine != 0xFFFFFFFFu));
+#pragma unroll
+                    for (int d = 32; d >= 1; d >>= 1) far = max(far, (uint32_t)__shfl_xor((int)far, d, 64));
+                    if (lane == 0) { s.b[wave] = far; s.sum[wave] = n; }
+                    __syncthreads();
+                    n = 0;
+                    for (int w = 0; w < WAVES; ++w) { far = max(far, s.b[w]); n += (uint32_t)s.sum[w]; }
+                    __syncthreads();
+                    uint32_t bound = kmax - kKeyNegInf - 1u;                    // all valid labels
+                    if (n > want) {
+                        const int bits = far ? 32 - __clz((int)far) : 1;
+                        bound = (uint32_t)select_last<THREADS, false>(
+                            s.hist, round,
+                            [&](auto f) {
+                                if (mine != 0xFFFFFFFFu) f((uint64_t)mine, (uint64_t)1);
+                            },
+                            bits, want, want + want / 4 + 8);
+                        bound = min(bound, kmax - kKeyNegInf - 1u);
+                    }
+                    if (mass.inf) bound = 0;
+                    const float floor_x = key_score(kmax - bound);
+                    have_z = cut_p && !cut_k;
+                    for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+                        float y[VEC];
+                        load(v, y);
+                        uint32_t hits = 0;
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) hits |= (y[j] >= floor_x ? 1u : 0u) << j;
+                        if (have_z) {
+#pragma unroll
+                            for (int j = 0; j < VEC; ++j) z += mass.valid(y[j]) ? MassOf::fixed(mass(y[j])) : 0;
+                        }
+                        if (hits) {
+                            uint32_t at = atomicAdd(&s.count, (uint32_t)__popc(hits));
+#pragma unroll
+                            for (int j = 0; j < VEC; ++j)
+                                if (hits >> j & 1u) {
+                                    if (at < kCap) s.list[at] = number(y[j], v + j);
+                                    ++at;
+                                }
+                        }
+                    }
+                    if (have_z) {
+                        z = wave_sum_u64(z);
+                        if (lane == 0) s.sum[wave] = z;
+                    }
+                    __syncthreads();
+                    if (have_z) {
+                        z = 0;
+                        for (int w = 0; w < WAVES; ++w) z += s.sum[w];
+                    }
+                    const uint32_t count = s.count;
+                    if (count <= kCap) {
+                        listed = true;
+                        digits = ibits + (bound ? 32 - __clz((int)bound) : 1);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            const uint32_t at = i * THREADS + tid;
+                            el[i] = at < count ? s.list[at] : ~0ull;
+                            ew[i] = 0;
+                            if (at < count) ew[i] = MassOf::fixed(mass(key_score(kmax - (uint32_t)(el[i] >> ibits))));
+                        }
+                    }
+                    __syncthreads();
+                }
+            }
+
+            // the thread's labels: elements, or its share of the row
+            const auto each_element = [&](auto f) {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (el[i] <= last) f(el[i], ew[i]);
+            };
+            const auto each_label = [&](auto f) {
+                for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+                    float y[VEC];
+                    load(v, y);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        if (!mass.valid(y[j])) continue;
+                        const uint64_t n = number(y[j], v + j);
+                        if (n <= last) f(n, MassOf::fixed(mass(y[j])));
+                    }
+                }
+            };
+            if (HOLD) last = ~0ull - 1;
+            // count and mass of what `last` leaves
+            const auto totals = [&](auto each, uint32_t &n, uint64_t &w) {
+                uint64_t tn = 0, tw = 0;
+                each([&](uint64_t, uint64_t m) { ++tn; tw += m; });
+                tn = wave_sum_u64(tn);
+                tw = wave_sum_u64(tw);
+                __syncthreads();
+                if (lane == 0) { s.sum[wave] = tw; s.b[wave] = (uint32_t)tn; }
+                __syncthreads();
+                n = 0;
+                w = 0;
+                for (int i = 0; i < WAVES; ++i) { n += s.b[i]; w += s.sum[i]; }
+            };
+            const auto cut = [&](auto each) {
+                uint32_t n;
+                uint64_t w;
+                if (cut_k) {
+                    totals(each, n, w);
+                    if ((uint32_t)topk < n)
+                        last = min(last, select_last<THREADS, false>(s.hist, round, each, digits, (uint64_t)topk,
+                                                                     (uint64_t)topk));
+                }
+                if (cut_p) {
+                    totals(each, n, w);
+                    const double t = ceil((double)topp * (double)(have_z ? z : w));
+                    uint64_t target = t >= 1.0 ? (uint64_t)t : 1ull;
+                    target = min(target, have_z ? z : w);
+                    if (target > w) return false;       // the list holds too little: the nucleus reaches past it
+                    // (the search may end above what top_k left: at the end of a digit that held one label)
+                    last = min(last, select_last<THREADS, true>(s.hist, round, each, digits, target, 0));
+                }
+                return true;
+            };
+            if (listed) {
+                if (!HOLD) last = ~0ull - 1;
+                listed = cut(each_element);
+            }
+            if (!HOLD && !listed) {
+                digits = ibits + 32;
+                have_z = false;
+                last = ~0ull;
+                cut(each_label);
+            }
+        }
+
+        // the draw
+        const float u = c.u[r];
+        const auto goal = [&](uint64_t total) {          // the running mass the token is the first to reach
+            const double t = u > 0.0f ? floor((double)u * (double)total) : 0.0;
+            return t < (double)total ? min((uint64_t)t + 1, total) : total;
+        };
+        const auto result = [&](uint32_t token, float y, uint64_t total, uint32_t kept) {
+            const double e = mass.inf ? 0.0 : ((double)y - mass.m) / (double)T;
+            emit((int)token, (float)(e - log((double)total / mass.one)), kept);
+        };
+        if (HOLD && !(cut_k || cut_p)) listed = false;
+        if (listed) {
+            uint64_t total = 0, n = 0;
+            const uint64_t imask = ((uint64_t)1 << ibits) - 1;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                bool keep = el[i] <= last;
+                if (keep && mass.lim > 0.0)
+                    keep = mass(key_score(kmax - (uint32_t)(el[i] >> ibits))) >= mass.lim;
+                if (!keep) el[i] = ~0ull;
+                else { total += ew[i]; ++n; }
+            }
+            total = wave_sum_u64(total);
+            n = wave_sum_u64(n);
+            __syncthreads();
+            if (lane == 0) { s.sum[wave] = total; s.b[wave] = (uint32_t)n; }
+            __syncthreads();
+            total = n = 0;
+            for (int i = 0; i < WAVES; ++i) { total += s.sum[i]; n += s.b[i]; }
+            const uint64_t end = select_last<THREADS, true>(
+                s.hist, round,
+                [&](auto f) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        if (el[i] != ~0ull && ew[i]) f(el[i] & imask, ew[i]);
+                },
+                max(ibits, 1), goal(total), 0);
+            // the last label at or before `end` with mass: one with more than the running mass before it. Its
+            // digit held no other, so it is the only one of its digits.
+            uint32_t at = 0;
+            float y = 0.0f;
+            bool have = false;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                if (el[i] != ~0ull && ew[i] && (el[i] & imask) <= end) {
+                    const uint32_t v = (uint32_t)(el[i] & imask);
+                    if (!have || v > at) { at = v; y = key_score(kmax - (uint32_t)(el[i] >> ibits)); have = true; }
+                }
+            }
+            uint32_t best = have ? at + 1 : 0;
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
+            if (WAVES > 1) {
+                if (lane == 0) s.a[wave] = best;
+                __syncthreads();
+                for (int i = 0; i < WAVES; ++i) best = max(best, s.a[i]);
+            }
+            if (have && at + 1 == best) result(at, y, total, (uint32_t)n);
+            continue;
+        }
+
+        // in the row itself: mass of a label (0: not kept)
+        const auto kept_mass = [&](float y, int v, bool &keep) {
+            keep = false;
+            if (!mass.valid(y)) return (uint64_t)0;
+            if (last != ~0ull && number(y, v) > last) return (uint64_t)0;
+            const double w = mass(y);
+            keep = w >= mass.lim;
+            return keep ? MassOf::fixed(w) : 0;
+        };
+        uint64_t sum = 0;
+        uint32_t n = 0;
+#pragma unroll 2
+        for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+            float y[VEC];
+            load(v, y);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                bool keep;
+                sum += kept_mass(y[j], v + j, keep);
+                n += keep ? 1u : 0u;
+            }
+        }
+        sum = wave_sum_u64(sum);
+        n = (uint32_t)wave_sum_u64(n);
+        __syncthreads();
+        if (lane == 0) { s.sum[wave] = sum; s.b[wave] = n; }
+        __syncthreads();
+        uint64_t total = 0;
+        n = 0;
+        for (int w = 0; w < WAVES; ++w) { total += s.sum[w]; n += s.b[w]; }
+        uint64_t want = goal(total);
+        int p0 = 0, p1 = V;                              // the piece that holds the token
+        uint64_t before = 0;
+        for (int w = 0; w < WAVES; ++w) {
+            const uint64_t m = s.sum[w];
+            if (before + m >= want) { p0 = min(V, w * seg); p1 = min(V, p0 + seg); break; }
+            before += m;
+        }
+        want -= before;
+        if (WAVES > 1 && p1 - p0 > 4 * kStepW) {
+            // again among the wavefronts
+            const int part = (p1 - p0 + WAVES * kStepW - 1) / (WAVES * kStepW) * kStepW;
+            const int q0 = min(p1, p0 + wave * part), q1 = min(p1, q0 + part);
+            sum = 0;
+            for (int v = q0 + lane * VEC; v < q1; v += kStepW) {
+                float y[VEC];
+                load(v, y);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    bool keep;
+                    if (v + j < q1) sum += kept_mass(y[j], v + j, keep);
+                }
+            }
+            sum = wave_sum_u64(sum);
+            __syncthreads();
+            if (lane == 0) s.sum[wave] = sum;
+            __syncthreads();
+            before = 0;
+            for (int w = 0; w < WAVES; ++w) {
+                const uint64_t m = s.sum[w];
+                if (before + m >= want) {
+                    const int a = min(p1, p0 + w * part);
+                    p1 = min(p1, a + part);
+                    p0 = a;
+                    break;
+                }
+                before += m;
+            }
+            want -= before;
+        }
+        if (wave == 0) {
+            // one wavefront walks what is left
+            for (int vb = p0; vb < p1; vb += kStepW) {
+                const int v = vb + lane * VEC;
+                float y[VEC];
+                uint64_t w[VEC], mine = 0;
+                if (v < p1) load(v, y);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    bool keep;
+                    w[j] = v + j < p1 ? kept_mass(y[j], v + j, keep) : 0;
+                    mine += w[j];
+                }
+                const uint64_t run = wave_scan_u64(mine);
+                const uint64_t hit = __ballot(run >= want);
                 if (hit) {
                     if (lane == __ffsll((unsigned long long)hit) - 1) {
-                        c.token[r] = v;
-                        if (c.log_prob) {
-                            const double e = mass.inf || greedy ? 0.0 : ((double)key_score(k) - mass.m) / mass.t;
-                            c.log_prob[r] = (float)(e - log((double)total / mass.unit));
+                        uint64_t acc = run - mine;
+                        bool done = false;
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            acc += w[j];
+                            if (!done && acc >= want) {
+                                done = true;
+                                result(v + j, y[j], total, n);
+                            }
                         }
-                        if (c.kept) c.kept[r] = (int32_t)sel[2];
                     }
                     break;
                 }
-                base += __shfl((unsigned long long)run, 63, 64);
-                const uint32_t nt = __popcll(tm);
-                left -= min(left, nt);
+                want -= lane_u64(run, 63);
             }
         }
     }
+}
+
+template <typename XT>
+hipError_t sample_xt(const SampleCall &c, hipStream_t s)
+{
+    // V masses of at most 2^unit each stay below 2^62
+    int ibits = 0;
+    while ((1ll << ibits) < (long long)c.V) ++ibits;
+    const int unit = std::min(51, 62 - ibits);
+    const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid));
+    if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits);
+    else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits);
+    else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_sample(const SampleCall &c, hipStream_t s)
 {
-    // V masses of at most 2^bits each stay below 2^62
-    int lg = 0;
-    while ((1ll << lg) < (long long)c.V) ++lg;
-    const int bits = std::min(52, 62 - lg);
-    const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid)), b(kSampleThreads);
-    if (c.x_dtype == kF32) hipLaunchKernelGGL(k_sample<float>, g, b, 0, s, c, bits);
-    else if (c.x_dtype == kF16) hipLaunchKernelGGL(k_sample<_Float16>, g, b, 0, s, c, bits);
-    else hipLaunchKernelGGL(k_sample<__bf16>, g, b, 0, s, c, bits);
-    return hipGetLastError();
+    if (c.x_dtype == kF32) return sample_xt<float>(c, s);
+    if (c.x_dtype == kF16) return sample_xt<_Float16>(c, s);
+    return sample_xt<__bf16>(c, s);
 }
 
 }  // namespace wfst
