@@ -34,48 +34,99 @@ __device__ __forceinline__ float key_score(uint32_t k)
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// 2^t for t <= 0, relative error below 2^-51: the nearest integer leaves f in
-// [-1/2, 1/2], a polynomial of degree 10 (interpolating 2^f at Chebyshev nodes)
-// gives 2^f, and the integer is added to its exponent. Below 2^-1000: 2^-1000.
-__device__ __forceinline__ double exp2_neg(double t)
-{
-    t = fmax(t, -1000.0);
-    const double shift = 6755399441055744.0;           // 1.5 * 2^52: adding it rounds to an integer
-    const double r = t + shift;
-    const double f = t - (r - shift);
-    double p = 7.072585949269224e-09;
-    p = fma(p, f, 1.0208690299958306e-07);
-    p = fma(p, f, 1.321544258792169e-06);
-    p = fma(p, f, 1.5252657260200837e-05);
-    p = fma(p, f, 1.540353044173605e-04);
-    p = fma(p, f, 1.3333558230164974e-03);
-    p = fma(p, f, 9.618129107606888e-03);
-    p = fma(p, f, 5.550410866444772e-02);
-    p = fma(p, f, 2.4022650695910097e-01);
-    p = fma(p, f, 6.9314718055995e-01);
-    p = fma(p, f, 1.0);
-    const long long n = __double_as_longlong(r);       // its low bits hold the integer
-    return __longlong_as_double(__double_as_longlong(p) + (n << 52));
-}
-
-// The mass of a score, times 2^unit.
-struct MassOf {
-    double m, a;       // the row's maximum; log2(e) / T
-    double one;        // 2^unit
-    double lim;        // min_p * 2^unit (0: no limit)
-    bool inf;          // the maximum is +inf: only +inf is valid, all masses alike
-
-    __device__ __forceinline__ bool valid(float x) const { return inf ? x == INFINITY : x > -INFINITY; }
-    __device__ __forceinline__ double operator()(float x) const
+// The coefficients of 2^f on [-1/2, 1/2] (degree 10, interpolating at Chebyshev
+// nodes; relative error below 2^-51), in scalar registers: the compiler would
+// otherwise copy each into the accumulator of every multiply-add.
+struct Exp2Poly {
+    double c[10];
+    __device__ __forceinline__ Exp2Poly()
     {
-        return inf ? one : exp2_neg(((double)x - m) * a) * one;
-    }
-    // As an integer (one < 2^52, so that adding 2^52 leaves it in the low bits).
-    static __device__ __forceinline__ uint64_t fixed(double w)
-    {
-        return (uint64_t)__double_as_longlong(w + 4503599627370496.0) - 0x4330000000000000ull;
+        const double k[10] = {7.072585949269224e-09, 1.0208690299958306e-07, 1.321544258792169e-06,
+                              1.5252657260200837e-05, 1.540353044173605e-04, 1.3333558230164974e-03,
+                              9.618129107606888e-03, 5.550410866444772e-02, 2.4022650695910097e-01,
+                              6.9314718055995e-01};
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+            c[i] = k[i];
+            asm("" : "+s"(c[i]));
+        }
     }
 };
+
+// The mass of a score, times 2^unit. A row whose choice is already made (greedy,
+// or +inf scores, which leave only each other) is read with its largest scores
+// as 0 and all others as -inf, and keeps this one form.
+struct MassOf {
+    double m, a;       // the row's maximum; log2(e) / T
+    double t;          // T
+    double one, base;  // 2^unit; 1.5 * 2^52 + unit
+    double lim;        // min_p * 2^unit (0: no limit)
+    float top;         // the largest score as stored
+    bool pick;         // read as above
+
+    __device__ __forceinline__ MassOf(float top_, float T, float minp, int unit, bool greedy)
+    {
+        one = (double)(1ull << unit);
+        base = 6755399441055744.0 + (double)unit;
+        top = top_ > -INFINITY ? top_ : NAN;             // (an empty row: nothing is picked)
+        pick = greedy || top_ == INFINITY;
+        m = pick ? 0.0 : (double)top_;
+        t = greedy ? 1.0 : (double)T;
+        a = 1.4426950408889634 / t;
+        lim = minp > 0.0f ? (minp < 1.0f ? (double)minp : 1.0) * one : 0.0;
+    }
+    __device__ __forceinline__ float read(float x) const { return pick ? (x == top ? 0.0f : -INFINITY) : x; }
+    // 2^(t + unit), t = (x - m) a <= 0 (below -1000: as -1000): adding `base`
+    // rounds t to an integer, leaves unit + that integer in the low bits and f in
+    // [-1/2, 1/2]; the polynomial gives 2^f, the low bits go to its exponent.
+    __device__ __forceinline__ double operator()(float x, const Exp2Poly &k) const
+    {
+        const double e = fmax(((double)x - m) * a, -1000.0);
+        const double r = e + base;
+        const double f = e - (r - base);
+        double p = k.c[0];
+#pragma unroll
+        for (int i = 1; i < 10; ++i) p = fma(p, f, k.c[i]);
+        p = fma(p, f, 1.0);
+        return __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p));
+    }
+    // As an integer (one < 2^52: adding 2^52 leaves it in the low bits), first with the bits of 2^52 itself.
+    static constexpr uint64_t kRaw = 0x4330000000000000ull;
+    static __device__ __forceinline__ uint64_t raw(double w) { return (uint64_t)__double_as_longlong(w + 4503599627370496.0); }
+    static __device__ __forceinline__ uint64_t fixed(double w) { return raw(w) - kRaw; }
+    __device__ __forceinline__ float log_prob(float y, uint64_t total) const
+    {
+        return (float)(((double)y - m) / t - log((double)total / one));
+    }
+};
+
+// The running mass that the token is the first to reach: above u times the total.
+__device__ __forceinline__ uint64_t draw_goal(float u, uint64_t total)
+{
+    const double t = u > 0.0f ? floor((double)u * (double)total) : 0.0;
+    return t < (double)total ? min((uint64_t)t + 1, total) : total;
+}
+
+__device__ __forceinline__ void emit(const SampleCall &c, int64_t r, int token, float lp, uint32_t kept)
+{
+    c.token[r] = token;
+    if (c.log_prob) c.log_prob[r] = lp;
+    if (c.kept) c.kept[r] = (int32_t)kept;
+}
+
+// Labels v .. v + VEC - 1 of a row of V (-inf past its end).
+template <typename XT, int VEC>
+__device__ __forceinline__ void load_scores(const XT *x, int V, int v, float (&y)[VEC])
+{
+    if (v + VEC <= V) {
+        const Pack<XT, VEC> p = *(const Pack<XT, VEC> *)(x + v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) y[j] = (float)p.v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) y[j] = v + j < V ? (float)x[v + j] : -INFINITY;
+    }
+}
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint64_t dpp_u64(uint64_t v)
@@ -105,6 +156,127 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane)
 }
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) { return lane_u64(wave_scan_u64(v), 63); }
+
+// Rows without top_k and top_p, in the registers of WAVES wavefronts, each of
+// which holds NV consecutive packs of 64 * VEC labels. The sums of the wavefronts,
+// then of the packs, then of the lanes say which pack and lane hold the token;
+// that lane reads its labels again. A workgroup of one-wavefront rows holds four
+// of them and no barrier; the fixed work of a row (its scans, its logarithm) is
+// worth some 20 labels a lane, so a row takes few wavefronts.
+template <typename XT, int WAVES, int NV>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(SampleCall c, int unit)
+{
+    constexpr int VEC = 16 / sizeof(XT);
+    constexpr int kRows = WAVES == 1 ? 4 : 1;
+    constexpr int kPackW = 64 * VEC;
+    static_assert(WAVES <= 64 && NV <= 64, "one wavefront scans the sums");
+    __shared__ unsigned long long sums[WAVES];
+    __shared__ uint32_t red[2 * WAVES];
+    const int lane = threadIdx.x & 63, wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    const Exp2Poly poly;
+    for (int64_t r = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? threadIdx.x >> 6 : 0); r < c.rows; r += step) {
+        if (!row_active(c.set, r)) continue;
+        const XT *x = (const XT *)c.x + r * c.x_stride;
+        const int v0 = wave * NV * kPackW + lane * VEC;
+        Pack<XT, VEC> y[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = v0 + i * kPackW;
+            if (v + VEC <= c.V) {
+                y[i] = *(const Pack<XT, VEC> *)(x + v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[i].v[j] = v + j < c.V ? x[v + j] : (XT)-INFINITY;
+            }
+        }
+        const float T = c.temperatures ? c.temperatures[r] : c.temperature;
+        const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
+        const float u = c.u[r];
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) top = fmaxf(top, (float)y[i].v[j]);     // (NaN leaves it)
+        top = wave_max_f(top);
+        if (WAVES > 1) {
+            if (lane == 0) red[wave] = __float_as_uint(top);
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, __uint_as_float(red[w]));
+        }
+        const bool greedy = !(T > 0.0f);
+        const MassOf mass(top, T, greedy ? 0.0f : minp, unit, greedy);
+        // A mass that rounds to 0 needs no test: -inf and NaN have the mass 2^-1000
+        const auto mass_of = [&](float v, uint32_t &n) {
+            if (mass.pick) v = mass.read(v);
+            double w = mass(v == v ? v : -INFINITY, poly);
+            bool keep = v > -INFINITY;
+            if (mass.lim > 0.0) {
+                keep = keep && w >= mass.lim;
+                w = keep ? w : 0.0;
+            }
+            n += keep ? 1u : 0u;
+            return MassOf::raw(w);
+        };
+        uint64_t pack = 0, own = 0;                      // of pack `lane`; of all the wavefront's packs
+        uint32_t kept = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint64_t w = (uint64_t)0 - VEC * MassOf::kRaw;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w += mass_of((float)y[i].v[j], kept);
+            w = wave_sum_u64(w);
+            pack = lane == i ? w : pack;
+            own += w;
+        }
+        kept = (uint32_t)wave_sum_u64(kept);
+        uint64_t total = own, before = 0;                // `before`: the wavefronts in front
+        if (WAVES > 1) {
+            if (lane == 0) { sums[wave] = own; red[WAVES + wave] = kept; }
+            __syncthreads();
+            total = 0;
+            kept = 0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                before += w < wave ? (uint64_t)sums[w] : 0;
+                total += sums[w];
+                kept += red[WAVES + w];
+            }
+        }
+        const uint64_t goal = greedy ? 1 : draw_goal(u, total);
+        if (total == 0) {                                // (no label with a score above -inf)
+            if (lane == 0 && wave == 0) emit(c, r, -1, -INFINITY, 0);
+        } else if (before < goal && goal <= before + own) {
+            const uint64_t run = wave_scan_u64(pack);
+            const int at = __ffsll((unsigned long long)__ballot(before + run >= goal)) - 1;
+            before += lane_u64(run - pack, at);
+            const int v = v0 + at * kPackW;
+            float z[VEC];
+            load_scores<XT, VEC>(x, c.V, v, z);
+            uint64_t w[VEC], mine = 0;
+            uint32_t n = 0;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                w[j] = mass_of(z[j], n) - MassOf::kRaw;
+                mine += w[j];
+            }
+            const uint64_t upto = before + wave_scan_u64(mine);
+            if (lane == __ffsll((unsigned long long)__ballot(upto >= goal)) - 1) {
+                uint64_t acc = upto - mine;
+                int found = -1;
+                float score = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    acc += w[j];
+                    if (found < 0 && acc >= goal) { found = j; score = mass.read(z[j]); }
+                }
+                emit(c, r, v + found, greedy ? 0.0f : mass.log_prob(score, total), greedy ? 1 : kept);
+            }
+        }
+        if (WAVES > 1) __syncthreads();
+    }
+}
 
 // Histograms of 256 digits, three in turn: a round adds to one while the next is
 // cleared, and the third may still be read by wavefronts of the round before.
@@ -203,6 +375,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
     // each wavefront owns one contiguous piece of the row
     const int seg = (V + WAVES * kStepW - 1) / (WAVES * kStepW) * kStepW;
     const int v0 = min(V, wave * seg), v1 = min(V, v0 + seg);
+    const Exp2Poly poly;
     uint32_t round = 0;
     clear_hist<THREADS>(s.hist, 0);
 
@@ -216,29 +389,13 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
         const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
         const bool greedy = !(T > 0.0f);
 
-        // labels v .. v + VEC - 1 of the row (-inf past its end)
-        const auto load = [&](int v, float (&y)[VEC]) {
-            if (v + VEC <= V) {
-                const Pack<XT, VEC> p = *(const Pack<XT, VEC> *)(x + v);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) y[j] = (float)p.v[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) y[j] = v + j < V ? (float)x[v + j] : -INFINITY;
-            }
-        };
-        const auto emit = [&](int token, float lp, uint32_t kept) {
-            c.token[r] = token;
-            if (c.log_prob) c.log_prob[r] = lp;
-            if (c.kept) c.kept[r] = (int32_t)kept;
-        };
-
+        const auto load_raw = [&](int v, float (&y)[VEC]) { load_scores<XT, VEC>(x, V, v, y); };
         // the row's largest score, and each thread's own
         float own = -INFINITY;
 #pragma unroll 4
         for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
             float y[VEC];
-            load(v, y);
+            load_raw(v, y);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) own = fmaxf(own, y[j]);       // (NaN leaves it)
         }
@@ -253,7 +410,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
             s.first = 0xFFFFFFFFu;
         }
         if (top == -INFINITY) {
-            if (tid == 0) emit(-1, -INFINITY, 0);
+            if (tid == 0) emit(c, r, -1, -INFINITY, 0);
             continue;
         }
         if (greedy) {
@@ -261,7 +418,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
             __syncthreads();
             for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
                 float y[VEC];
-                load(v, y);
+                load_raw(v, y);
                 uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
                 for (int j = VEC - 1; j >= 0; --j)
@@ -270,17 +427,20 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                 if (__ballot(at != 0xFFFFFFFFu)) break;
             }
             __syncthreads();
-            if (tid == 0) emit((int)s.first, 0.0f, 1);
+            if (tid == 0) emit(c, r, (int)s.first, 0.0f, 1);
             continue;
         }
 
-        MassOf mass;
-        mass.one = (double)(1ull << unit);
-        mass.m = (double)top;
-        mass.a = 1.4426950408889634 / (double)T;
-        mass.inf = top == INFINITY;
-        mass.lim = minp > 0.0f ? (minp < 1.0f ? (double)minp : 1.0) * mass.one : 0.0;
-        const uint32_t kmax = score_key(top);
+        const MassOf mass(top, T, minp, unit, false);
+        const uint32_t kmax = score_key(mass.pick ? 0.0f : top);
+        own = mass.read(own);
+        const auto load = [&](int v, float (&y)[VEC]) {
+            load_scores<XT, VEC>(x, V, v, y);
+            if (mass.pick) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[j] = mass.read(y[j]);
+            }
+        };
         const bool cut_k = topk > 0 && topk < V, cut_p = topp < 1.0f;
         const auto number = [&](float y, uint32_t i) {
             return (uint64_t)(kmax - score_key(y)) << ibits | i;
@@ -301,9 +461,9 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                     if (v < V) load(v, y);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        const bool ok = v < V && mass.valid(y[j]);
+                        const bool ok = v < V && y[j] > -INFINITY;
                         el[i * VEC + j] = ok ? number(y[j], v + j) : ~0ull;
-                        ew[i * VEC + j] = ok ? MassOf::fixed(mass(y[j])) : 0;
+                        ew[i * VEC + j] = ok ? MassOf::fixed(mass(y[j], poly)) : 0;
                     }
                 }
             } else {
@@ -311,7 +471,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                 // that many or more, and among random ones not many more than that
                 const uint32_t want = cut_k ? (uint32_t)topk : THREADS * 3 / 4;
                 if (want <= THREADS * 7 / 8) {
-                    const uint32_t mine = mass.valid(own) ? kmax - score_key(own) : 0xFFFFFFFFu;
+                    const uint32_t mine = own > -INFINITY ? kmax - score_key(own) : 0xFFFFFFFFu;
                     uint32_t far = mine == 0xFFFFFFFFu ? 0 : mine, n = __popcll(__ballot(mine != 0xFFFFFFFFu));
 #pragma unroll
                     for (int d = 32; d >= 1; d >>= 1) far = max(far, (uint32_t)__shfl_xor((int)far, d, 64));
@@ -331,7 +491,6 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                             bits, want, want + want / 4 + 8);
                         bound = min(bound, kmax - kKeyNegInf - 1u);
                     }
-                    if (mass.inf) bound = 0;
                     const float floor_x = key_score(kmax - bound);
                     have_z = cut_p && !cut_k;
                     for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
@@ -342,7 +501,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                         for (int j = 0; j < VEC; ++j) hits |= (y[j] >= floor_x ? 1u : 0u) << j;
                         if (have_z) {
 #pragma unroll
-                            for (int j = 0; j < VEC; ++j) z += mass.valid(y[j]) ? MassOf::fixed(mass(y[j])) : 0;
+                            for (int j = 0; j < VEC; ++j) z += y[j] > -INFINITY ? MassOf::fixed(mass(y[j], poly)) : 0;
                         }
                         if (hits) {
                             uint32_t at = atomicAdd(&s.count, (uint32_t)__popc(hits));
@@ -372,7 +531,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                             const uint32_t at = i * THREADS + tid;
                             el[i] = at < count ? s.list[at] : ~0ull;
                             ew[i] = 0;
-                            if (at < count) ew[i] = MassOf::fixed(mass(key_score(kmax - (uint32_t)(el[i] >> ibits))));
+                            if (at < count) ew[i] = MassOf::fixed(mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly));
                         }
                     }
                     __syncthreads();
@@ -391,9 +550,9 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                     load(v, y);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        if (!mass.valid(y[j])) continue;
+                        if (!(y[j] > -INFINITY)) continue;
                         const uint64_t n = number(y[j], v + j);
-                        if (n <= last) f(n, MassOf::fixed(mass(y[j])));
+                        if (n <= last) f(n, MassOf::fixed(mass(y[j], poly)));
                     }
                 }
             };
@@ -445,13 +604,9 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
 
         // the draw
         const float u = c.u[r];
-        const auto goal = [&](uint64_t total) {          // the running mass the token is the first to reach
-            const double t = u > 0.0f ? floor((double)u * (double)total) : 0.0;
-            return t < (double)total ? min((uint64_t)t + 1, total) : total;
-        };
+        const auto goal = [&](uint64_t total) { return draw_goal(u, total); };
         const auto result = [&](uint32_t token, float y, uint64_t total, uint32_t kept) {
-            const double e = mass.inf ? 0.0 : ((double)y - mass.m) / (double)T;
-            emit((int)token, (float)(e - log((double)total / mass.one)), kept);
+            emit(c, r, (int)token, mass.log_prob(y, total), kept);
         };
         if (HOLD && !(cut_k || cut_p)) listed = false;
         if (listed) {
@@ -461,7 +616,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
             for (int i = 0; i < E; ++i) {
                 bool keep = el[i] <= last;
                 if (keep && mass.lim > 0.0)
-                    keep = mass(key_score(kmax - (uint32_t)(el[i] >> ibits))) >= mass.lim;
+                    keep = mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly) >= mass.lim;
                 if (!keep) el[i] = ~0ull;
                 else { total += ew[i]; ++n; }
             }
@@ -507,9 +662,9 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
         // in the row itself: mass of a label (0: not kept)
         const auto kept_mass = [&](float y, int v, bool &keep) {
             keep = false;
-            if (!mass.valid(y)) return (uint64_t)0;
+            if (!(y > -INFINITY)) return (uint64_t)0;
             if (last != ~0ull && number(y, v) > last) return (uint64_t)0;
-            const double w = mass(y);
+            const double w = mass(y, poly);
             keep = w >= mass.lim;
             return keep ? MassOf::fixed(w) : 0;
         };
@@ -610,6 +765,33 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
     }
 }
 
+template <typename XT, int WAVES, int NV>
+bool draw_all_nv(const SampleCall &c, int unit, hipStream_t s)
+{
+    constexpr int kRows = WAVES == 1 ? 4 : 1;
+    const dim3 g((unsigned)std::min<int64_t>((c.rows + kRows - 1) / kRows, kMaxRowGrid));
+    hipLaunchKernelGGL((k_draw_all<XT, WAVES, NV>), g, dim3(WAVES == 1 ? 256 : WAVES * 64), 0, s, c, unit);
+    return true;
+}
+
+// The row's number of packs decides; false: too long for registers.
+template <typename XT>
+bool draw_all(const SampleCall &c, int unit, hipStream_t s)
+{
+    constexpr int kPackW = 64 * (16 / (int)sizeof(XT));
+    constexpr int kTop = sizeof(XT) == 2 ? 1 : 2;        // the same labels in twice the packs
+    const int64_t packs = (c.V + kPackW - 1) / kPackW;
+    if (packs <= 1) return draw_all_nv<XT, 1, 1>(c, unit, s);
+    if (packs <= 2) return draw_all_nv<XT, 1, 2>(c, unit, s);
+    if (packs <= 4 * kTop) return draw_all_nv<XT, 1, 4 * kTop>(c, unit, s);
+    if (packs <= 7 * kTop) return draw_all_nv<XT, 1, 7 * kTop>(c, unit, s);
+    if (packs <= 10 * kTop) return draw_all_nv<XT, 1, 10 * kTop>(c, unit, s);
+    if (packs <= 16 * kTop) return draw_all_nv<XT, 4, 4 * kTop>(c, unit, s);
+    if (packs <= 32 * kTop) return draw_all_nv<XT, 4, 8 * kTop>(c, unit, s);
+    if (packs <= 64 * kTop) return draw_all_nv<XT, 16, 4 * kTop>(c, unit, s);
+    return false;
+}
+
 template <typename XT>
 hipError_t sample_xt(const SampleCall &c, hipStream_t s)
 {
@@ -618,6 +800,7 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
     while ((1ll << ibits) < (long long)c.V) ++ibits;
     const int unit = std::min(51, 62 - ibits);
     const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid));
+    if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps && draw_all<XT>(c, unit, s)) return hipGetLastError();
     if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits);
     else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits);
     else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits);
