@@ -63,9 +63,11 @@ struct MassOf {
     double lim;        // min_p * 2^unit (0: no limit)
     float top;         // the largest score as stored
     bool pick;         // read as above
+    bool greedy;
 
-    __device__ __forceinline__ MassOf(float top_, float T, float minp, int unit, bool greedy)
+    __device__ __forceinline__ MassOf(float top_, float T, float minp, int unit, bool greedy_)
     {
+        greedy = greedy_;
         one = (double)(1ull << unit);
         base = 6755399441055744.0 + (double)unit;
         top = top_ > -INFINITY ? top_ : NAN;             // (an empty row: nothing is picked)
@@ -157,122 +159,146 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane)
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) { return lane_u64(wave_scan_u64(v), 63); }
 
-// Rows without top_k and top_p, in the registers of WAVES wavefronts, each of
-// which holds NV consecutive packs of 64 * VEC labels. The sums of the wavefronts,
-// then of the packs, then of the lanes say which pack and lane hold the token;
-// that lane reads its labels again. A workgroup of one-wavefront rows holds four
-// of them and no barrier; the fixed work of a row (its scans, its logarithm) is
-// worth some 20 labels a lane, so a row takes few wavefronts.
-template <typename XT, int WAVES, int NV>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(SampleCall c, int unit)
+// LDS of draw_row.
+template <int WAVES> struct RowSums {
+    unsigned long long sum[WAVES];
+    uint32_t kept[WAVES];
+};
+
+// Draw from the row itself by the WAVES wavefronts of a workgroup (or each
+// wavefront on a row of its own). Every wavefront owns one contiguous run of
+// packs of 64 * VEC labels; the sums of the wavefronts, then of their packs, then
+// of the lanes say where the token lies. raw_of(score, label, kept) is a label's
+// MassOf::raw (score as MassOf::read gives it), counting it if it is kept.
+template <typename XT, int WAVES, typename Mass>
+__device__ __forceinline__ void draw_row(const SampleCall &c, int64_t r, const XT *x, const MassOf &mass, float u,
+                                         RowSums<WAVES> &s, Mass raw_of)
 {
     constexpr int VEC = 16 / sizeof(XT);
-    constexpr int kRows = WAVES == 1 ? 4 : 1;
     constexpr int kPackW = 64 * VEC;
-    static_assert(WAVES <= 64 && NV <= 64, "one wavefront scans the sums");
-    __shared__ unsigned long long sums[WAVES];
-    __shared__ uint32_t red[2 * WAVES];
     const int lane = threadIdx.x & 63, wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
-    const int64_t step = (int64_t)gridDim.x * kRows;
-    const Exp2Poly poly;
-    for (int64_t r = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? threadIdx.x >> 6 : 0); r < c.rows; r += step) {
-        if (!row_active(c.set, r)) continue;
-        const XT *x = (const XT *)c.x + r * c.x_stride;
-        const int v0 = wave * NV * kPackW + lane * VEC;
-        Pack<XT, VEC> y[NV];
+    const int packs = (c.V + WAVES * kPackW - 1) / (WAVES * kPackW);     // of one wavefront
+    const int group = (packs + 63) / 64;                                 // packs whose sum one lane keeps
+    const int v0 = wave * packs * kPackW;
+    uint64_t part = 0, own = 0;                      // of the lane's group of packs; of the wavefront
+    uint32_t kept = 0;
+    for (int i = 0, g = 0, in = 0; i < packs && v0 + i * kPackW < c.V; ++i) {
+        const int v = v0 + i * kPackW + lane * VEC;
+        float y[VEC];
+        load_scores<XT, VEC>(x, c.V, v, y);
+        uint64_t w = (uint64_t)0 - VEC * MassOf::kRaw;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = v0 + i * kPackW;
-            if (v + VEC <= c.V) {
-                y[i] = *(const Pack<XT, VEC> *)(x + v);
-            } else {
+        for (int j = 0; j < VEC; ++j) w += raw_of(y[j], v + j, kept);
+        w = wave_sum_u64(w);
+        part += lane == g ? w : 0;
+        own += w;
+        if (++in == group) { in = 0; ++g; }
+    }
+    kept = (uint32_t)wave_sum_u64(kept);
+    uint64_t total = own, before = 0;                // `before`: the wavefronts in front
+    if (WAVES > 1) {
+        if (lane == 0) { s.sum[wave] = own; s.kept[wave] = kept; }
+        __syncthreads();
+        total = 0;
+        kept = 0;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) y[i].v[j] = v + j < c.V ? x[v + j] : (XT)-INFINITY;
-            }
+        for (int w = 0; w < WAVES; ++w) {
+            before += w < wave ? (uint64_t)s.sum[w] : 0;
+            total += s.sum[w];
+            kept += s.kept[w];
         }
-        const float T = c.temperatures ? c.temperatures[r] : c.temperature;
-        const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
-        const float u = c.u[r];
-        float top = -INFINITY;
+    }
+    if (total == 0) {                                // (no label with a score above -inf)
+        if (lane == 0 && wave == 0) emit(c, r, -1, -INFINITY, 0);
+        return;
+    }
+    const uint64_t goal = mass.greedy ? 1 : draw_goal(u, total);
+    if (goal <= before || goal > before + own) return;       // (one wavefront goes on)
+    const uint64_t run = before + wave_scan_u64(part);
+    const int at = __ffsll((unsigned long long)__ballot(run >= goal)) - 1;
+    before = lane_u64(run - part, at);
+    for (int i = at * group; i < packs; ++i) {
+        const int v = v0 + i * kPackW + lane * VEC;
+        float y[VEC];
+        load_scores<XT, VEC>(x, c.V, v, y);
+        uint64_t w[VEC], mine = 0;
+        uint32_t n = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) top = fmaxf(top, (float)y[i].v[j]);     // (NaN leaves it)
-        top = wave_max_f(top);
-        if (WAVES > 1) {
-            if (lane == 0) red[wave] = __float_as_uint(top);
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, __uint_as_float(red[w]));
+        for (int j = 0; j < VEC; ++j) {
+            w[j] = raw_of(y[j], v + j, n) - MassOf::kRaw;
+            mine += w[j];
         }
-        const bool greedy = !(T > 0.0f);
-        const MassOf mass(top, T, greedy ? 0.0f : minp, unit, greedy);
-        // A mass that rounds to 0 needs no test: -inf and NaN have the mass 2^-1000
-        const auto mass_of = [&](float v, uint32_t &n) {
-            if (mass.pick) v = mass.read(v);
-            double w = mass(v == v ? v : -INFINITY, poly);
-            bool keep = v > -INFINITY;
-            if (mass.lim > 0.0) {
-                keep = keep && w >= mass.lim;
-                w = keep ? w : 0.0;
-            }
-            n += keep ? 1u : 0u;
-            return MassOf::raw(w);
-        };
-        uint64_t pack = 0, own = 0;                      // of pack `lane`; of all the wavefront's packs
-        uint32_t kept = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            uint64_t w = (uint64_t)0 - VEC * MassOf::kRaw;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) w += mass_of((float)y[i].v[j], kept);
-            w = wave_sum_u64(w);
-            pack = lane == i ? w : pack;
-            own += w;
-        }
-        kept = (uint32_t)wave_sum_u64(kept);
-        uint64_t total = own, before = 0;                // `before`: the wavefronts in front
-        if (WAVES > 1) {
-            if (lane == 0) { sums[wave] = own; red[WAVES + wave] = kept; }
-            __syncthreads();
-            total = 0;
-            kept = 0;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
-                before += w < wave ? (uint64_t)sums[w] : 0;
-                total += sums[w];
-                kept += red[WAVES + w];
-            }
-        }
-        const uint64_t goal = greedy ? 1 : draw_goal(u, total);
-        if (total == 0) {                                // (no label with a score above -inf)
-            if (lane == 0 && wave == 0) emit(c, r, -1, -INFINITY, 0);
-        } else if (before < goal && goal <= before + own) {
-            const uint64_t run = wave_scan_u64(pack);
-            const int at = __ffsll((unsigned long long)__ballot(before + run >= goal)) - 1;
-            before += lane_u64(run - pack, at);
-            const int v = v0 + at * kPackW;
-            float z[VEC];
-            load_scores<XT, VEC>(x, c.V, v, z);
-            uint64_t w[VEC], mine = 0;
-            uint32_t n = 0;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                w[j] = mass_of(z[j], n) - MassOf::kRaw;
-                mine += w[j];
-            }
-            const uint64_t upto = before + wave_scan_u64(mine);
-            if (lane == __ffsll((unsigned long long)__ballot(upto >= goal)) - 1) {
+        const uint64_t upto = before + wave_scan_u64(mine);
+        const uint64_t hit = __ballot(upto >= goal);
+        if (hit) {
+            if (lane == __ffsll((unsigned long long)hit) - 1) {
                 uint64_t acc = upto - mine;
                 int found = -1;
                 float score = 0.0f;
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     acc += w[j];
-                    if (found < 0 && acc >= goal) { found = j; score = mass.read(z[j]); }
+                    if (found < 0 && acc >= goal) { found = j; score = mass.read(y[j]); }
                 }
-                emit(c, r, v + found, greedy ? 0.0f : mass.log_prob(score, total), greedy ? 1 : kept);
+                emit(c, r, v + found, mass.greedy ? 0.0f : mass.log_prob(score, total), mass.greedy ? 1 : kept);
             }
+            return;
+        }
+        before = lane_u64(upto, 63);
+    }
+}
+
+// Rows without top_k and top_p. A workgroup of one-wavefront rows holds four of
+// them and no barrier.
+template <typename XT, int WAVES>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(SampleCall c, int unit)
+{
+    constexpr int VEC = 16 / sizeof(XT);
+    constexpr int kRows = WAVES == 1 ? 4 : 1;
+    constexpr int kPackW = 64 * VEC;
+    __shared__ RowSums<WAVES> s;
+    __shared__ float red[WAVES];
+    const int lane = threadIdx.x & 63, wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    const Exp2Poly poly;
+    for (int64_t r = (int64_t)blockIdx.x * kRows + (WAVES == 1 ? threadIdx.x >> 6 : 0); r < c.rows; r += step) {
+        if (!row_active(c.set, r)) continue;
+        const XT *x = (const XT *)c.x + r * c.x_stride;
+        const float T = c.temperatures ? c.temperatures[r] : c.temperature;
+        const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
+        const float u = c.u[r];
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int v = (wave * 64 + lane) * VEC; v < c.V; v += WAVES * kPackW) {
+            float y[VEC];
+            load_scores<XT, VEC>(x, c.V, v, y);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) top = fmaxf(top, y[j]);        // (NaN leaves it)
+        }
+        top = wave_max_f(top);
+        if (WAVES > 1) {
+            if (lane == 0) red[wave] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, red[w]);
+        }
+        const bool greedy = !(T > 0.0f);
+        const MassOf mass(top, T, greedy ? 0.0f : minp, unit, greedy);
+        // Two forms: the tests of the general one, as selects, take half as long again as the sum itself.
+        // Without them -inf and NaN have the mass 2^-1000, which rounds to 0.
+        if (__builtin_amdgcn_readfirstlane(mass.pick || mass.lim > 0.0)) {
+            draw_row<XT, WAVES>(c, r, x, mass, u, s, [&](float y, int, uint32_t &n) {
+                y = mass.read(y);
+                const double w = mass(y, poly);
+                const bool keep = y > -INFINITY && w >= mass.lim;
+                n += keep ? 1u : 0u;
+                return MassOf::raw(keep ? w : 0.0);
+            });
+        } else {
+            draw_row<XT, WAVES>(c, r, x, mass, u, s, [&](float y, int, uint32_t &n) {
+                n += y > -INFINITY ? 1u : 0u;
+                return MassOf::raw(mass(y, poly));
+            });
         }
         if (WAVES > 1) __syncthreads();
     }
@@ -356,7 +382,8 @@ __device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each e
 // labels that may be kept, E a thread.
 template <int THREADS, int E, bool HOLD> struct DrawShared {
     Hist hist;
-    unsigned long long sum[THREADS / 64 + 1];
+    RowSums<THREADS / 64> row;
+    unsigned long long sum[THREADS / 64];
     uint32_t a[THREADS / 64], b[THREADS / 64];
     uint32_t count, first;
     unsigned long long list[HOLD ? 1 : E * THREADS];
@@ -604,7 +631,6 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
 
         // the draw
         const float u = c.u[r];
-        const auto goal = [&](uint64_t total) { return draw_goal(u, total); };
         const auto result = [&](uint32_t token, float y, uint64_t total, uint32_t kept) {
             emit(c, r, (int)token, mass.log_prob(y, total), kept);
         };
@@ -634,7 +660,7 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
                     for (int i = 0; i < E; ++i)
                         if (el[i] != ~0ull && ew[i]) f(el[i] & imask, ew[i]);
                 },
-                max(ibits, 1), goal(total), 0);
+                max(ibits, 1), draw_goal(u, total), 0);
             // the last label at or before `end` with mass: one with more than the running mass before it. Its
             // digit held no other, so it is the only one of its digits.
             uint32_t at = 0;
@@ -659,137 +685,30 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
             continue;
         }
 
-        // in the row itself: mass of a label (0: not kept)
-        const auto kept_mass = [&](float y, int v, bool &keep) {
-            keep = false;
-            if (!(y > -INFINITY)) return (uint64_t)0;
-            if (last != ~0ull && number(y, v) > last) return (uint64_t)0;
+        __syncthreads();
+        draw_row<XT, WAVES>(c, r, x, mass, u, s.row, [&](float y, int v, uint32_t &n) {
+            y = mass.read(y);
             const double w = mass(y, poly);
-            keep = w >= mass.lim;
-            return keep ? MassOf::fixed(w) : 0;
-        };
-        uint64_t sum = 0;
-        uint32_t n = 0;
-#pragma unroll 2
-        for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-            float y[VEC];
-            load(v, y);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                bool keep;
-                sum += kept_mass(y[j], v + j, keep);
-                n += keep ? 1u : 0u;
-            }
-        }
-        sum = wave_sum_u64(sum);
-        n = (uint32_t)wave_sum_u64(n);
-        __syncthreads();
-        if (lane == 0) { s.sum[wave] = sum; s.b[wave] = n; }
-        __syncthreads();
-        uint64_t total = 0;
-        n = 0;
-        for (int w = 0; w < WAVES; ++w) { total += s.sum[w]; n += s.b[w]; }
-        uint64_t want = goal(total);
-        int p0 = 0, p1 = V;                              // the piece that holds the token
-        uint64_t before = 0;
-        for (int w = 0; w < WAVES; ++w) {
-            const uint64_t m = s.sum[w];
-            if (before + m >= want) { p0 = min(V, w * seg); p1 = min(V, p0 + seg); break; }
-            before += m;
-        }
-        want -= before;
-        if (WAVES > 1 && p1 - p0 > 4 * kStepW) {
-            // again among the wavefronts
-            const int part = (p1 - p0 + WAVES * kStepW - 1) / (WAVES * kStepW) * kStepW;
-            const int q0 = min(p1, p0 + wave * part), q1 = min(p1, q0 + part);
-            sum = 0;
-            for (int v = q0 + lane * VEC; v < q1; v += kStepW) {
-                float y[VEC];
-                load(v, y);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    bool keep;
-                    if (v + j < q1) sum += kept_mass(y[j], v + j, keep);
-                }
-            }
-            sum = wave_sum_u64(sum);
-            __syncthreads();
-            if (lane == 0) s.sum[wave] = sum;
-            __syncthreads();
-            before = 0;
-            for (int w = 0; w < WAVES; ++w) {
-                const uint64_t m = s.sum[w];
-                if (before + m >= want) {
-                    const int a = min(p1, p0 + w * part);
-                    p1 = min(p1, a + part);
-                    p0 = a;
-                    break;
-                }
-                before += m;
-            }
-            want -= before;
-        }
-        if (wave == 0) {
-            // one wavefront walks what is left
-            for (int vb = p0; vb < p1; vb += kStepW) {
-                const int v = vb + lane * VEC;
-                float y[VEC];
-                uint64_t w[VEC], mine = 0;
-                if (v < p1) load(v, y);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    bool keep;
-                    w[j] = v + j < p1 ? kept_mass(y[j], v + j, keep) : 0;
-                    mine += w[j];
-                }
-                const uint64_t run = wave_scan_u64(mine);
-                const uint64_t hit = __ballot(run >= want);
-                if (hit) {
-                    if (lane == __ffsll((unsigned long long)hit) - 1) {
-                        uint64_t acc = run - mine;
-                        bool done = false;
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            acc += w[j];
-                            if (!done && acc >= want) {
-                                done = true;
-                                result(v + j, y[j], total, n);
-                            }
-                        }
-                    }
-                    break;
-                }
-                want -= lane_u64(run, 63);
-            }
-        }
+            const bool keep = y > -INFINITY && w >= mass.lim && (last == ~0ull || number(y, v) <= last);
+            n += keep ? 1u : 0u;
+            return MassOf::raw(keep ? w : 0.0);
+        });
     }
 }
 
-template <typename XT, int WAVES, int NV>
-bool draw_all_nv(const SampleCall &c, int unit, hipStream_t s)
-{
-    constexpr int kRows = WAVES == 1 ? 4 : 1;
-    const dim3 g((unsigned)std::min<int64_t>((c.rows + kRows - 1) / kRows, kMaxRowGrid));
-    hipLaunchKernelGGL((k_draw_all<XT, WAVES, NV>), g, dim3(WAVES == 1 ? 256 : WAVES * 64), 0, s, c, unit);
-    return true;
-}
-
-// The row's number of packs decides; false: too long for registers.
+// Wavefronts a row: one where the rows are many (the fixed work of a row, its
+// scans and its logarithm, is then done once), more where few rows would leave
+// the card idle.
 template <typename XT>
-bool draw_all(const SampleCall &c, int unit, hipStream_t s)
+void draw_all(const SampleCall &c, int unit, hipStream_t s)
 {
     constexpr int kPackW = 64 * (16 / (int)sizeof(XT));
-    constexpr int kTop = sizeof(XT) == 2 ? 1 : 2;        // the same labels in twice the packs
     const int64_t packs = (c.V + kPackW - 1) / kPackW;
-    if (packs <= 1) return draw_all_nv<XT, 1, 1>(c, unit, s);
-    if (packs <= 2) return draw_all_nv<XT, 1, 2>(c, unit, s);
-    if (packs <= 4 * kTop) return draw_all_nv<XT, 1, 4 * kTop>(c, unit, s);
-    if (packs <= 7 * kTop) return draw_all_nv<XT, 1, 7 * kTop>(c, unit, s);
-    if (packs <= 10 * kTop) return draw_all_nv<XT, 1, 10 * kTop>(c, unit, s);
-    if (packs <= 16 * kTop) return draw_all_nv<XT, 4, 4 * kTop>(c, unit, s);
-    if (packs <= 32 * kTop) return draw_all_nv<XT, 4, 8 * kTop>(c, unit, s);
-    if (packs <= 64 * kTop) return draw_all_nv<XT, 16, 4 * kTop>(c, unit, s);
-    return false;
+    const int64_t want = std::min<int64_t>(packs, 4096 / std::max<int64_t>(c.rows, 1));
+    const auto grid = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxRowGrid)); };
+    if (want < 4) hipLaunchKernelGGL((k_draw_all<XT, 1>), grid((c.rows + 3) / 4), dim3(256), 0, s, c, unit);
+    else if (want < 16) hipLaunchKernelGGL((k_draw_all<XT, 4>), grid(c.rows), dim3(256), 0, s, c, unit);
+    else hipLaunchKernelGGL((k_draw_all<XT, 16>), grid(c.rows), dim3(1024), 0, s, c, unit);
 }
 
 template <typename XT>
@@ -800,8 +719,8 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
     while ((1ll << ibits) < (long long)c.V) ++ibits;
     const int unit = std::min(51, 62 - ibits);
     const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid));
-    if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps && draw_all<XT>(c, unit, s)) return hipGetLastError();
-    if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits);
+    if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps) draw_all<XT>(c, unit, s);
+    else if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits);
     else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits);
     else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits);
     return hipGetLastError();
