@@ -317,19 +317,55 @@ __device__ __forceinline__ void clear_hist(Hist &h, int slot)
     for (int i = threadIdx.x; i < 256; i += THREADS) { h.mass[slot][i] = 0; h.cnt[slot][i] = 0; }
 }
 
+// The digit in which the running sum over a histogram, from `above`, reaches
+// target: the sum before it, its own, its count; digit 256 if none does. Every
+// wavefront finds it, four digits to a lane.
+struct Digit {
+    uint32_t digit, count;
+    uint64_t before, mine;
+};
+
+template <bool MASS>
+__device__ __forceinline__ Digit find_digit(const Hist &h, int slot, uint64_t above, uint64_t target)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t c[4];
+    uint64_t w[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = h.cnt[slot][lane * 4 + i];
+        w[i] = MASS ? (uint64_t)h.mass[slot][lane * 4 + i] : c[i];
+        sum += w[i];
+    }
+    uint64_t acc = above + wave_scan_u64(sum) - sum;
+    int d = 4;
+    Digit r = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (d == 4 && acc + w[i] >= target) { d = i; r.before = acc; r.mine = w[i]; r.count = c[i]; }
+        acc += w[i];
+    }
+    const uint64_t hit = __ballot(d < 4);
+    const int src = hit ? __ffsll((unsigned long long)hit) - 1 : 63;
+    r.digit = __builtin_amdgcn_readlane(src * 4 + d, src);
+    r.before = lane_u64(r.before, src);
+    r.mine = lane_u64(r.mine, src);
+    r.count = __builtin_amdgcn_readlane(r.count, src);
+    return r;
+}
+
 // The value `last` at which the elements, taken in ascending order of their
-// 64-bit numbers, reach `target` (in counts, or in masses): the one that
-// reaches it and all before are <= last. each(f) calls f(number, mass) for the
-// thread's elements; numbers are unique or `enough` ends the search. digits:
-// the position of the highest bit set in any number, plus one. `skip`: numbers
-// hold nothing between bits `skip_to` and `skip`. `round` counts the histograms
-// used in this workgroup; its slot is clear on entry and on return.
-// With `enough`, counts: also ends when at most that many are <= last.
+// numbers, reach `target` (in counts, or in masses): the one that reaches it and
+// all before are <= last, the others are not. each(f) calls f(number, mass) for
+// the thread's elements; digits is the position of the highest bit set in any
+// number, plus one. The search goes down by digits of 8 bits until a digit holds
+// one element, or (counts) the elements up to its end are at most `enough`.
+// `round` counts the histograms used in this workgroup; its slot is clear on
+// entry and on return. target must not pass the elements' total.
 template <int THREADS, bool MASS, typename Each>
 __device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each each, int digits, uint64_t target,
                                                 uint64_t enough)
 {
-    const int lane = threadIdx.x & 63;
     uint64_t prefix = 0, above = 0;
     int shift = digits;                                // the digits above it are fixed
     for (;;) {
@@ -337,7 +373,7 @@ __device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each e
         const int slot = round % 3;
         clear_hist<THREADS>(h, (round + 1) % 3);
         each([&](uint64_t num, uint64_t w) {
-            if ((shift >= 64 ? 0 : num >> shift) == prefix) {
+            if (num >> shift == prefix) {
                 const uint32_t d = (uint32_t)(num >> next) & ((1u << width) - 1u);
                 atomicAdd(&h.cnt[slot][d], 1u);
                 if (MASS) atomicAdd(&h.mass[slot][d], (unsigned long long)w);
@@ -345,41 +381,44 @@ __device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each e
         });
         __syncthreads();
         ++round;
-        // every wavefront finds the digit: four to a lane
-        uint32_t c[4];
-        uint64_t w[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c[i] = h.cnt[slot][lane * 4 + i];
-            w[i] = MASS ? (uint64_t)h.mass[slot][lane * 4 + i] : c[i];
-            sum += w[i];
-        }
-        uint64_t acc = above + wave_scan_u64(sum) - sum;
-        int d = 4;
-        uint64_t before = 0, mine = 0;
-        uint32_t count = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (d == 4 && acc + w[i] >= target) { d = i; before = acc; mine = w[i]; count = c[i]; }
-            acc += w[i];
-        }
-        const uint64_t hit = __ballot(d < 4);
-        const int src = hit ? __ffsll((unsigned long long)hit) - 1 : 63;     // (targets never pass the total)
-        const uint32_t digit = __builtin_amdgcn_readlane(src * 4 + d, src);
-        before = lane_u64(before, src);
-        mine = lane_u64(mine, src);
-        count = __builtin_amdgcn_readlane(count, src);
-        prefix = prefix << width | (digit & 255u);
-        above = before;
+        const Digit d = find_digit<MASS>(h, slot, above, target);
+        prefix = prefix << width | (d.digit & 255u);
+        above = d.before;
         shift = next;
-        const bool whole = !MASS && above + mine <= enough;
-        if (count <= 1 || whole || shift == 0) return ((prefix + 1) << shift) - 1;
+        const bool whole = !MASS && above + d.mine <= enough;
+        if (d.count <= 1 || whole || shift == 0) return ((prefix + 1) << shift) - 1;
     }
 }
 
-// What a workgroup of THREADS threads keeps of a row. HOLD: the row itself, E
-// scores a thread (rows of at most E * THREADS labels); otherwise the list of
-// labels that may be kept, E a thread.
+// A row's settings.
+struct RowRules {
+    float T, topp, minp, u;
+    int topk;
+    bool greedy, cut_k, cut_p;
+
+    __device__ __forceinline__ RowRules(const SampleCall &c, int64_t r)
+    {
+        T = c.temperatures ? c.temperatures[r] : c.temperature;
+        topk = c.top_ks ? c.top_ks[r] : c.top_k;
+        topp = c.top_ps ? c.top_ps[r] : c.top_p;
+        minp = c.min_ps ? c.min_ps[r] : c.min_p;
+        u = c.u[r];
+        greedy = !(T > 0.0f);
+        if (greedy) minp = 0.0f;
+        cut_k = !greedy && topk > 0 && topk < c.V;
+        cut_p = !greedy && topp < 1.0f;
+    }
+};
+
+// The mass to reach for top_p of `total`.
+__device__ __forceinline__ uint64_t top_p_goal(float topp, uint64_t total)
+{
+    const double t = ceil((double)topp * (double)total);
+    return min(t >= 1.0 ? (uint64_t)t : (uint64_t)1, total);
+}
+
+// What a workgroup of THREADS threads keeps of a row, with a list of labels that
+// may be kept, E a thread.
 template <int THREADS, int E, bool HOLD> struct DrawShared {
     Hist hist;
     RowSums<THREADS / 64> row;
@@ -389,310 +428,388 @@ template <int THREADS, int E, bool HOLD> struct DrawShared {
     unsigned long long list[HOLD ? 1 : E * THREADS];
 };
 
+// Count and mass of the elements that each() gives, in the whole workgroup.
+template <int WAVES, typename S, typename Each>
+__device__ __forceinline__ void element_totals(S &s, Each each, uint32_t &n, uint64_t &w)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t tn = 0, tw = 0;
+    each([&](uint64_t, uint64_t m) { ++tn; tw += m; });
+    tn = wave_sum_u64(tn);
+    tw = wave_sum_u64(tw);
+    __syncthreads();
+    if (lane == 0) { s.sum[wave] = tw; s.b[wave] = (uint32_t)tn; }
+    __syncthreads();
+    n = 0;
+    w = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) { n += s.b[i]; w += s.sum[i]; }
+}
+
+// Cut by top_k and top_p among the elements that each(last, f) gives; total: the
+// mass top_p is a share of where that is not the elements' own (0 otherwise).
+// False: their mass falls short of it.
+template <int THREADS, typename S, typename Each>
+__device__ __forceinline__ bool cut_elements(S &s, uint32_t &round, const RowRules &row, Each each, int digits,
+                                             uint64_t total, uint64_t &last)
+{
+    constexpr int WAVES = THREADS / 64;
+    const auto now = [&](auto f) { each(last, f); };
+    uint32_t n;
+    uint64_t w;
+    if (row.cut_k) {
+        element_totals<WAVES>(s, now, n, w);
+        if ((uint32_t)row.topk < n)
+            last = min(last, select_last<THREADS, false>(s.hist, round, now, digits, (uint64_t)row.topk,
+                                                         (uint64_t)row.topk));
+    }
+    if (row.cut_p) {
+        element_totals<WAVES>(s, now, n, w);
+        const uint64_t target = top_p_goal(row.topp, total ? total : w);
+        if (target > w) return false;
+        // (the search may end above what top_k left: at the end of a digit that held one label)
+        last = min(last, select_last<THREADS, true>(s.hist, round, now, digits, target, 0));
+    }
+    return true;
+}
+
+// Cut a list of elements (number, mass; ~0: none) that holds all labels which may
+// be kept, and draw from it. False, and nothing written: see cut_elements.
+template <int THREADS, int E, typename S>
+__device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const RowRules &row, const MassOf &mass,
+                                          const Exp2Poly &poly, uint32_t kmax, int ibits, uint64_t (&el)[E],
+                                          const uint64_t (&ew)[E], int digits, uint64_t total_p, S &s, uint32_t &round)
+{
+    constexpr int WAVES = THREADS / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t last = ~0ull - 1;
+    if (!cut_elements<THREADS>(
+            s, round, row,
+            [&](uint64_t upto, auto f) {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (el[i] <= upto) f(el[i], ew[i]);
+            },
+            digits, total_p, last))
+        return false;
+    const uint64_t imask = ((uint64_t)1 << ibits) - 1;
+    // (by selects: the compiler has been seen to lose stores to such arrays under divergent branches)
+    if (mass.lim > 0.0) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const double w = mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly);
+            el[i] = w >= mass.lim ? el[i] : ~0ull;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) el[i] = el[i] <= last ? el[i] : ~0ull;
+    uint32_t n;
+    uint64_t total;
+    element_totals<WAVES>(
+        s,
+        [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (el[i] != ~0ull) f(el[i], ew[i]);
+        },
+        n, total);
+    const uint64_t end = select_last<THREADS, true>(
+        s.hist, round,
+        [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (el[i] != ~0ull && ew[i]) f(el[i] & imask, ew[i]);
+        },
+        max(ibits, 1), row.greedy ? 1 : draw_goal(row.u, total), 0);
+    // the last label with mass at or before `end`: no other shares its digits
+    uint32_t at = 0;
+    float y = 0.0f;
+    bool have = false;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const uint32_t v = (uint32_t)(el[i] & imask);
+        if (el[i] != ~0ull && ew[i] && v <= end && (!have || v > at)) {
+            at = v;
+            y = key_score(kmax - (uint32_t)(el[i] >> ibits));
+            have = true;
+        }
+    }
+    uint32_t best = have ? at + 1 : 0;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
+    if (WAVES > 1) {
+        if (lane == 0) s.a[wave] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) best = max(best, s.a[i]);
+    }
+    if (have && at + 1 == best) emit(c, r, (int)at, row.greedy ? 0.0f : mass.log_prob(y, total), row.greedy ? 1 : n);
+    return true;
+}
+
+// One row by one workgroup. HOLD: the row in registers, E scores a thread (rows
+// of at most E * THREADS labels), all of them elements. Otherwise a short list of
+// labels that are sure to hold the kept ones is tried first.
 template <typename XT, int THREADS, int E, bool HOLD>
-__global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ibits)
+__device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const RowRules &row, const Exp2Poly &poly,
+                                         int unit, int ibits, DrawShared<THREADS, E, HOLD> &s, uint32_t &round)
 {
     constexpr int WAVES = THREADS / 64;
     constexpr int VEC = 16 / sizeof(XT);
     constexpr int kStepW = 64 * VEC;                   // labels a wavefront takes at once
     constexpr int kCap = E * THREADS;
-    __shared__ DrawShared<THREADS, E, HOLD> s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int V = c.V;
+    const XT *x = (const XT *)c.x + r * c.x_stride;
     // each wavefront owns one contiguous piece of the row
     const int seg = (V + WAVES * kStepW - 1) / (WAVES * kStepW) * kStepW;
     const int v0 = min(V, wave * seg), v1 = min(V, v0 + seg);
-    const Exp2Poly poly;
-    uint32_t round = 0;
-    clear_hist<THREADS>(s.hist, 0);
 
-    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
-        if (!row_active(c.set, r)) continue;
-        __syncthreads();
-        const XT *x = (const XT *)c.x + r * c.x_stride;
-        const float T = c.temperatures ? c.temperatures[r] : c.temperature;
-        const int topk = c.top_ks ? c.top_ks[r] : c.top_k;
-        const float topp = c.top_ps ? c.top_ps[r] : c.top_p;
-        const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
-        const bool greedy = !(T > 0.0f);
-
-        const auto load_raw = [&](int v, float (&y)[VEC]) { load_scores<XT, VEC>(x, V, v, y); };
-        // the row's largest score, and each thread's own
-        float own = -INFINITY;
+    // the row's largest score, and each thread's own
+    float own = -INFINITY;
 #pragma unroll 4
+    for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+        float y[VEC];
+        load_scores<XT, VEC>(x, V, v, y);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) own = fmaxf(own, y[j]);       // (NaN leaves it)
+    }
+    float top = wave_max_f(own);
+    __syncthreads();
+    if (lane == 0) s.a[wave] = __float_as_uint(top);
+    if (tid == 0) { s.count = 0; s.first = 0xFFFFFFFFu; }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, __uint_as_float(s.a[w]));
+    if (top == -INFINITY) {
+        if (tid == 0) emit(c, r, -1, -INFINITY, 0);
+        return;
+    }
+    if (row.greedy) {
+        // the first label with the largest score
         for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
             float y[VEC];
-            load_raw(v, y);
+            load_scores<XT, VEC>(x, V, v, y);
+            uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) own = fmaxf(own, y[j]);       // (NaN leaves it)
+            for (int j = VEC - 1; j >= 0; --j)
+                if (y[j] == top) at = v + j;
+            if (at != 0xFFFFFFFFu) atomicMin(&s.first, at);
+            if (__ballot(at != 0xFFFFFFFFu)) break;
         }
-        float top = wave_max_f(own);
-        if (WAVES > 1) {
-            if (lane == 0) s.a[wave] = __float_as_uint(top);
-            if (tid == 0) { s.count = 0; s.first = 0xFFFFFFFFu; }
+        __syncthreads();
+        if (tid == 0) emit(c, r, (int)s.first, 0.0f, 1);
+        return;
+    }
+
+    const MassOf mass(top, row.T, row.minp, unit, false);
+    const float high = mass.read(top);                 // the largest score as it is read
+    const uint32_t kmax = score_key(high);
+    own = mass.read(own);
+    const auto load = [&](int v, float (&y)[VEC]) {
+        load_scores<XT, VEC>(x, V, v, y);
+        if (mass.pick) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[j] = mass.read(y[j]);
+        }
+    };
+    const auto number = [&](float y, uint32_t i) { return (uint64_t)(kmax - score_key(y)) << ibits | i; };
+    uint64_t last = ~0ull;                             // kept: number <= last
+
+    if (row.cut_k || row.cut_p) {
+        uint64_t el[E], ew[E];                         // the thread's elements: number, mass
+        if (HOLD) {
+#pragma unroll
+            for (int i = 0; i < E / VEC; ++i) {
+                const int v = (i * THREADS + tid) * VEC;
+                float y[VEC];
+                load(v, y);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    el[i * VEC + j] = y[j] > -INFINITY ? number(y[j], v + j) : ~0ull;
+                    ew[i * VEC + j] = MassOf::fixed(mass(y[j], poly));      // (0 for -inf and NaN)
+                }
+            }
+            draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, ibits + 32, 0, s, round);
+            return;
+        }
+        // the list's labels become the threads' elements
+        const auto take = [&](uint32_t count) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const uint32_t at = i * THREADS + tid;
+                const uint64_t n = s.list[at];                 // (past the count: whatever the list held)
+                const uint64_t w = MassOf::fixed(mass(key_score(kmax - (uint32_t)(n >> ibits)), poly));
+                el[i] = at < count ? n : ~0ull;
+                ew[i] = at < count ? w : 0;
+            }
+        };
+        uint64_t z = 0;                                // mass of all labels (top_p without top_k)
+        // A bound that at least `want` threads' largest scores reach: the labels that reach it are that many or
+        // more, and among labels in random order not many more than that
+        const uint32_t want = row.cut_k ? (uint32_t)row.topk : THREADS * 3 / 4;
+        if (want <= THREADS * 7 / 8) {
+            const uint32_t mine = own > -INFINITY ? kmax - score_key(own) : 0xFFFFFFFFu;
+            uint32_t far = mine == 0xFFFFFFFFu ? 0 : mine, n = __popcll(__ballot(mine != 0xFFFFFFFFu));
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1) far = max(far, (uint32_t)__shfl_xor((int)far, d, 64));
+            if (lane == 0) { s.b[wave] = far; s.sum[wave] = n; }
             __syncthreads();
-            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, __uint_as_float(s.a[w]));
-        } else if (tid == 0) {
-            s.count = 0;
-            s.first = 0xFFFFFFFFu;
-        }
-        if (top == -INFINITY) {
-            if (tid == 0) emit(c, r, -1, -INFINITY, 0);
-            continue;
-        }
-        if (greedy) {
-            // the first label with the largest score
+            n = 0;
+            for (int w = 0; w < WAVES; ++w) { far = max(far, s.b[w]); n += (uint32_t)s.sum[w]; }
             __syncthreads();
+            uint32_t bound = kmax - kKeyNegInf - 1u;                    // all labels above -inf
+            if (n > want) {
+                const int bits = far ? 32 - __clz((int)far) : 1;
+                const uint64_t b = select_last<THREADS, false>(
+                    s.hist, round,
+                    [&](auto f) {
+                        if (mine != 0xFFFFFFFFu) f((uint64_t)mine, (uint64_t)1);
+                    },
+                    bits, want, want + want / 4 + 8);
+                bound = (uint32_t)min(b, (uint64_t)bound);
+            }
+            const float floor_x = key_score(kmax - bound);
+            const bool need_z = !row.cut_k;
             for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
                 float y[VEC];
-                load_raw(v, y);
-                uint32_t at = 0xFFFFFFFFu;
+                load(v, y);
+                uint32_t hits = 0;
 #pragma unroll
-                for (int j = VEC - 1; j >= 0; --j)
-                    if (y[j] == top) at = v + j;
-                if (at != 0xFFFFFFFFu) atomicMin(&s.first, at);
-                if (__ballot(at != 0xFFFFFFFFu)) break;
+                for (int j = 0; j < VEC; ++j) hits |= (y[j] >= floor_x ? 1u : 0u) << j;
+                if (need_z) {
+                    // (-inf and NaN have the mass 2^-1000, which rounds to 0)
+                    z -= VEC * MassOf::kRaw;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) z += MassOf::raw(mass(y[j], poly));
+                }
+                if (hits) {
+                    uint32_t at = atomicAdd(&s.count, (uint32_t)__popc(hits));
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        if (hits >> j & 1u) {
+                            if (at < kCap) s.list[at] = number(y[j], v + j);
+                            ++at;
+                        }
+                }
+            }
+            if (need_z) {
+                z = wave_sum_u64(z);
+                if (lane == 0) s.sum[wave] = z;
             }
             __syncthreads();
-            if (tid == 0) emit(c, r, (int)s.first, 0.0f, 1);
-            continue;
+            if (need_z) {
+                z = 0;
+                for (int w = 0; w < WAVES; ++w) z += s.sum[w];
+            }
+            const uint32_t count = s.count;
+            take(min(count, (uint32_t)kCap));
+            __syncthreads();
+            if (count <= kCap) {
+                const int digits = ibits + (bound ? 32 - __clz((int)bound) : 1);
+                if (draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, z, s, round)) return;
+            }
         }
 
-        const MassOf mass(top, T, minp, unit, false);
-        const uint32_t kmax = score_key(mass.pick ? 0.0f : top);
-        own = mass.read(own);
-        const auto load = [&](int v, float (&y)[VEC]) {
-            load_scores<XT, VEC>(x, V, v, y);
-            if (mass.pick) {
+        bool done = false;
+        if (z) {
+            // top_p alone, its labels more than the list holds: masses by 256 equal steps of the score, from the
+            // top down to where all labels below together weigh less than 1 - top_p; then a list of the step that
+            // reaches the target
+            const uint64_t target = top_p_goal(row.topp, z);
+            const double least = (1.0 - (double)row.topp) * (double)z / (mass.one * (double)V);
+            double low = mass.m + mass.t * log(least);
+            low -= 1e-6 * (fabs(low) + fabs(mass.m));
+            const float y_low = low > -3.4028234663852886e38 ? (float)low : -3.4028234663852886e38f;
+            const float steps = 255.9f / (high - y_low);
+            const float scale = steps < INFINITY && steps > 0.0f ? steps : 0.0f;
+            const auto step_of = [&](float y) { return min(255u, (uint32_t)((high - y) * scale)); };
+            const int slot = round % 3;
+            clear_hist<THREADS>(s.hist, (round + 1) % 3);
+            if (tid == 0) { s.count = 0; s.first = 0; }
+            for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+                float y[VEC];
+                load(v, y);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) y[j] = mass.read(y[j]);
+                for (int j = 0; j < VEC; ++j)
+                    if (y[j] >= y_low) {
+                        const uint32_t d = step_of(y[j]);
+                        atomicAdd(&s.hist.cnt[slot][d], 1u);
+                        atomicAdd(&s.hist.mass[slot][d], (unsigned long long)MassOf::fixed(mass(y[j], poly)));
+                    }
             }
-        };
-        const bool cut_k = topk > 0 && topk < V, cut_p = topp < 1.0f;
-        const auto number = [&](float y, uint32_t i) {
-            return (uint64_t)(kmax - score_key(y)) << ibits | i;
-        };
-        uint64_t last = ~0ull;                         // kept: number <= last
-        uint64_t el[E], ew[E];                         // the thread's elements: number, mass
-        bool listed = HOLD;                            // the kept labels are all among the elements
-        int digits = ibits + 32;
-
-        if (cut_k || cut_p) {
-            uint64_t z = 0;                            // mass of all valid labels (top_p without top_k)
-            bool have_z = false;
-            if (HOLD) {
-#pragma unroll
-                for (int i = 0; i < E / VEC; ++i) {
-                    const int v = (i * THREADS + tid) * VEC;
-                    float y[VEC];
-                    if (v < V) load(v, y);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const bool ok = v < V && y[j] > -INFINITY;
-                        el[i * VEC + j] = ok ? number(y[j], v + j) : ~0ull;
-                        ew[i * VEC + j] = ok ? MassOf::fixed(mass(y[j], poly)) : 0;
-                    }
-                }
-            } else {
-                // A bound that at least `want` threads' largest scores reach: the labels that reach it are
-                // that many or more, and among random ones not many more than that
-                const uint32_t want = cut_k ? (uint32_t)topk : THREADS * 3 / 4;
-                if (want <= THREADS * 7 / 8) {
-                    const uint32_t mine = own > -INFINITY ? kmax - score_key(own) : 0xFFFFFFFFu;
-                    uint32_t far = mine == 0xFFFFFFFFu ? 0 : mine, n = __popcll(__ballot(mine != 0xFFFFFFFFu));
-#pragma unroll
-                    for (int d = 32; d >= 1; d >>= 1) far = max(far, (uint32_t)__shfl_xor((int)far, d, 64));
-                    if (lane == 0) { s.b[wave] = far; s.sum[wave] = n; }
-                    __syncthreads();
-                    n = 0;
-                    for (int w = 0; w < WAVES; ++w) { far = max(far, s.b[w]); n += (uint32_t)s.sum[w]; }
-                    __syncthreads();
-                    uint32_t bound = kmax - kKeyNegInf - 1u;                    // all valid labels
-                    if (n > want) {
-                        const int bits = far ? 32 - __clz((int)far) : 1;
-                        bound = (uint32_t)select_last<THREADS, false>(
-                            s.hist, round,
-                            [&](auto f) {
-                                if (mine != 0xFFFFFFFFu) f((uint64_t)mine, (uint64_t)1);
-                            },
-                            bits, want, want + want / 4 + 8);
-                        bound = min(bound, kmax - kKeyNegInf - 1u);
-                    }
-                    const float floor_x = key_score(kmax - bound);
-                    have_z = cut_p && !cut_k;
-                    for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-                        float y[VEC];
-                        load(v, y);
-                        uint32_t hits = 0;
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) hits |= (y[j] >= floor_x ? 1u : 0u) << j;
-                        if (have_z) {
-#pragma unroll
-                            for (int j = 0; j < VEC; ++j) z += y[j] > -INFINITY ? MassOf::fixed(mass(y[j], poly)) : 0;
-                        }
-                        if (hits) {
-                            uint32_t at = atomicAdd(&s.count, (uint32_t)__popc(hits));
-#pragma unroll
-                            for (int j = 0; j < VEC; ++j)
-                                if (hits >> j & 1u) {
-                                    if (at < kCap) s.list[at] = number(y[j], v + j);
-                                    ++at;
-                                }
-                        }
-                    }
-                    if (have_z) {
-                        z = wave_sum_u64(z);
-                        if (lane == 0) s.sum[wave] = z;
-                    }
-                    __syncthreads();
-                    if (have_z) {
-                        z = 0;
-                        for (int w = 0; w < WAVES; ++w) z += s.sum[w];
-                    }
-                    const uint32_t count = s.count;
-                    if (count <= kCap) {
-                        listed = true;
-                        digits = ibits + (bound ? 32 - __clz((int)bound) : 1);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            const uint32_t at = i * THREADS + tid;
-                            el[i] = at < count ? s.list[at] : ~0ull;
-                            ew[i] = 0;
-                            if (at < count) ew[i] = MassOf::fixed(mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly));
-                        }
-                    }
-                    __syncthreads();
-                }
-            }
-
-            // the thread's labels: elements, or its share of the row
-            const auto each_element = [&](auto f) {
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (el[i] <= last) f(el[i], ew[i]);
-            };
-            const auto each_label = [&](auto f) {
+            __syncthreads();
+            ++round;
+            const Digit d = find_digit<true>(s.hist, slot, 0, target);
+            if (d.digit < 256 && d.count <= kCap) {
                 for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
                     float y[VEC];
                     load(v, y);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        if (!(y[j] > -INFINITY)) continue;
-                        const uint64_t n = number(y[j], v + j);
-                        if (n <= last) f(n, MassOf::fixed(mass(y[j], poly)));
+                    for (int j = 0; j < VEC; ++j)
+                        if (y[j] >= y_low && step_of(y[j]) == d.digit) {
+                            const uint64_t n = number(y[j], v + j);
+                            const uint32_t at = atomicAdd(&s.count, 1u);
+                            if (at < kCap) s.list[at] = n;
+                            atomicMax(&s.first, (uint32_t)(n >> ibits));
+                        }
+                }
+                __syncthreads();
+                const uint32_t far = s.first;
+                take(s.count);
+                // (scores below the step lie below `far`, the search's end need not)
+                last = min(((uint64_t)far << ibits) + (((uint64_t)1 << ibits) - 1),
+                           select_last<THREADS, true>(
+                               s.hist, round,
+                               [&](auto f) {
+#pragma unroll
+                                   for (int i = 0; i < E; ++i)
+                                       if (el[i] != ~0ull) f(el[i], ew[i]);
+                               },
+                               ibits + (far ? 32 - __clz((int)far) : 1), target - d.before, 0));
+                done = true;
+            }
+        }
+        if (!done)
+            cut_elements<THREADS>(
+                s, round, row,
+                [&](uint64_t upto, auto f) {
+                    for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
+                        float y[VEC];
+                        load(v, y);
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            if (!(y[j] > -INFINITY)) continue;
+                            const uint64_t n = number(y[j], v + j);
+                            if (n <= upto) f(n, MassOf::fixed(mass(y[j], poly)));
+                        }
                     }
-                }
-            };
-            if (HOLD) last = ~0ull - 1;
-            // count and mass of what `last` leaves
-            const auto totals = [&](auto each, uint32_t &n, uint64_t &w) {
-                uint64_t tn = 0, tw = 0;
-                each([&](uint64_t, uint64_t m) { ++tn; tw += m; });
-                tn = wave_sum_u64(tn);
-                tw = wave_sum_u64(tw);
-                __syncthreads();
-                if (lane == 0) { s.sum[wave] = tw; s.b[wave] = (uint32_t)tn; }
-                __syncthreads();
-                n = 0;
-                w = 0;
-                for (int i = 0; i < WAVES; ++i) { n += s.b[i]; w += s.sum[i]; }
-            };
-            const auto cut = [&](auto each) {
-                uint32_t n;
-                uint64_t w;
-                if (cut_k) {
-                    totals(each, n, w);
-                    if ((uint32_t)topk < n)
-                        last = min(last, select_last<THREADS, false>(s.hist, round, each, digits, (uint64_t)topk,
-                                                                     (uint64_t)topk));
-                }
-                if (cut_p) {
-                    totals(each, n, w);
-                    const double t = ceil((double)topp * (double)(have_z ? z : w));
-                    uint64_t target = t >= 1.0 ? (uint64_t)t : 1ull;
-                    target = min(target, have_z ? z : w);
-                    if (target > w) return false;       // the list holds too little: the nucleus reaches past it
-                    // (the search may end above what top_k left: at the end of a digit that held one label)
-                    last = min(last, select_last<THREADS, true>(s.hist, round, each, digits, target, 0));
-                }
-                return true;
-            };
-            if (listed) {
-                if (!HOLD) last = ~0ull - 1;
-                listed = cut(each_element);
-            }
-            if (!HOLD && !listed) {
-                digits = ibits + 32;
-                have_z = false;
-                last = ~0ull;
-                cut(each_label);
-            }
-        }
-
-        // the draw
-        const float u = c.u[r];
-        const auto result = [&](uint32_t token, float y, uint64_t total, uint32_t kept) {
-            emit(c, r, (int)token, mass.log_prob(y, total), kept);
-        };
-        if (HOLD && !(cut_k || cut_p)) listed = false;
-        if (listed) {
-            uint64_t total = 0, n = 0;
-            const uint64_t imask = ((uint64_t)1 << ibits) - 1;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                bool keep = el[i] <= last;
-                if (keep && mass.lim > 0.0)
-                    keep = mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly) >= mass.lim;
-                if (!keep) el[i] = ~0ull;
-                else { total += ew[i]; ++n; }
-            }
-            total = wave_sum_u64(total);
-            n = wave_sum_u64(n);
-            __syncthreads();
-            if (lane == 0) { s.sum[wave] = total; s.b[wave] = (uint32_t)n; }
-            __syncthreads();
-            total = n = 0;
-            for (int i = 0; i < WAVES; ++i) { total += s.sum[i]; n += s.b[i]; }
-            const uint64_t end = select_last<THREADS, true>(
-                s.hist, round,
-                [&](auto f) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        if (el[i] != ~0ull && ew[i]) f(el[i] & imask, ew[i]);
                 },
-                max(ibits, 1), draw_goal(u, total), 0);
-            // the last label at or before `end` with mass: one with more than the running mass before it. Its
-            // digit held no other, so it is the only one of its digits.
-            uint32_t at = 0;
-            float y = 0.0f;
-            bool have = false;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                if (el[i] != ~0ull && ew[i] && (el[i] & imask) <= end) {
-                    const uint32_t v = (uint32_t)(el[i] & imask);
-                    if (!have || v > at) { at = v; y = key_score(kmax - (uint32_t)(el[i] >> ibits)); have = true; }
-                }
-            }
-            uint32_t best = have ? at + 1 : 0;
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
-            if (WAVES > 1) {
-                if (lane == 0) s.a[wave] = best;
-                __syncthreads();
-                for (int i = 0; i < WAVES; ++i) best = max(best, s.a[i]);
-            }
-            if (have && at + 1 == best) result(at, y, total, (uint32_t)n);
-            continue;
-        }
+                ibits + 32, 0, last);
+    }
 
+    __syncthreads();
+    draw_row<XT, WAVES>(c, r, x, mass, row.u, s.row, [&](float y, int v, uint32_t &n) {
+        y = mass.read(y);
+        const double w = mass(y, poly);
+        const bool keep = y > -INFINITY && w >= mass.lim && (last == ~0ull || number(y, v) <= last);
+        n += keep ? 1u : 0u;
+        return MassOf::raw(keep ? w : 0.0);
+    });
+}
+
+template <typename XT, int THREADS, int E, bool HOLD>
+__global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ibits)
+{
+    __shared__ DrawShared<THREADS, E, HOLD> s;
+    const Exp2Poly poly;
+    uint32_t round = 0;
+    clear_hist<THREADS>(s.hist, 0);
+    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+        if (!row_active(c.set, r)) continue;
         __syncthreads();
-        draw_row<XT, WAVES>(c, r, x, mass, u, s.row, [&](float y, int v, uint32_t &n) {
-            y = mass.read(y);
-            const double w = mass(y, poly);
-            const bool keep = y > -INFINITY && w >= mass.lim && (last == ~0ull || number(y, v) <= last);
-            n += keep ? 1u : 0u;
-            return MassOf::raw(keep ? w : 0.0);
-        });
+        const RowRules row(c, r);
+        draw_one<XT, THREADS, E, HOLD>(c, r, row, poly, unit, ibits, s, round);
     }
 }
 
