@@ -689,12 +689,15 @@ typedef struct wfst_sample_config {
  * computed in binary64 and added as multiples of 2^-52 or of V * 2^-62 rounded up
  * to a power of two, whichever is larger: results do not depend on any order of
  * addition, and labels whose mass rounds to 0 are not drawn. V in [1, 2^24].
- * Outputs must not overlap each other or the inputs.
+ * Outputs must not overlap each other or the inputs. workspace: device memory,
+ * 16-byte aligned, of at least wfst_sample_workspace's bytes (null when those are
+ * 0), in use until the stream has passed the call.
  * Errors: WFST_EINVAL, WFST_EDEVICE.
  */
 int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, const float *u,
                 const wfst_sample_config *cfg, const int32_t *lengths, int32_t T, int32_t *out_tokens,
-                float *out_log_probs, int32_t *out_kept, void *stream);
+                float *out_log_probs, int32_t *out_kept, void *workspace, int64_t workspace_bytes, void *stream);
+int wfst_sample_workspace(int32_t x_dtype, int64_t rows, int32_t V, int64_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -375,7 +375,7 @@ def _sample_check(res, x, u, **kw):
 
 SETTINGS = [dict(), dict(temperature=0.0), dict(temperature=0.7, top_k=1), dict(top_k=5), dict(top_k=50, top_p=0.9),
             dict(top_p=0.95), dict(top_p=0.3, temperature=1.7), dict(min_p=0.1), dict(top_p=0.0), dict(min_p=1.0),
-            dict(temperature=0.8, top_k=700, top_p=0.97, min_p=0.01), dict(temperature=3.0, top_k=100000, top_p=0.999)]
+            dict(top_k=50, min_p=0.01), dict(temperature=0.8, top_k=700, top_p=0.97, min_p=0.01), dict(top_p=0.9, min_p=1e-4), dict(temperature=3.0, top_k=100000, top_p=0.999)]
 
 
 @pytest.mark.parametrize("V", [1, 2, 5, 64, 65, 257, 500, 1025, 5000, 32003])
@@ -391,9 +391,8 @@ def test_sample(V, x):
             _sample_check(wb.sample(t, u, **s), t, u, **s)
 
 
-@pytest.mark.parametrize("V", [40, 3000, 20011])
-def test_sample_settings_per_row(V):
-    R = 64
+@pytest.mark.parametrize("V,R", [(40, 64), (3000, 64), (20011, 64), (20011, 150)])
+def test_sample_settings_per_row(V, R):
     g = torch.Generator(device="cuda").manual_seed(V + 1)
     t = torch.randn(R, V, generator=g, device="cuda") * 3
     u = torch.rand(R, generator=g, device="cuda")
@@ -420,7 +419,7 @@ def test_sample_ties_go_to_the_lowest_index():
         _sample_check(wb.sample(q, u, **s), q, u, **s)
 
 
-@pytest.mark.parametrize("V", [9, 700, 9001])
+@pytest.mark.parametrize("V", [9, 700, 5001, 9001])
 def test_sample_masks_and_specials(V):
     inf = float("inf")
     t = torch.randn(10, V)
@@ -465,6 +464,40 @@ def test_sample_strides_lengths_and_untouched_rows():
     nan = x.contiguous()
     nan[0, 2:] = float("nan")                       # frames behind the last are not read
     assert torch.equal(wb.sample(nan, u, top_p=0.9, lengths=L, out=out).tokens, r.tokens)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("R", [3, 140])
+def test_sample_orders_that_mislead_the_lists(R, x):
+    """Scores in falling order, in rising order, all equal, all masked but a few,
+    and a nucleus of most labels: the short lists do not hold the kept labels."""
+    V = 30011
+    t = torch.empty(5, V)
+    t[0] = -torch.arange(V) * 1e-3
+    t[1] = torch.arange(V) * 1e-3
+    t[2] = 1.5
+    t[3] = -1e30
+    t[3, 20000:20040] = torch.randn(40)
+    t[4] = torch.randn(V) * 0.1
+    t = t.repeat(-(-R // 5), 1)[:R].to(DT[x]).cuda()
+    u = torch.rand(R, generator=torch.Generator(device="cuda").manual_seed(R), device="cuda")
+    for s in (dict(), dict(top_k=40), dict(top_k=900), dict(top_k=5000), dict(top_p=0.9), dict(top_p=0.9, top_k=3000),
+              dict(min_p=0.5), dict(top_p=0.31, temperature=20.0), dict(temperature=0.0)):
+        _say("orders", R, x, s)
+        _sample_check(wb.sample(t, u, **s), t, u, **s)
+
+
+@pytest.mark.parametrize("R", [2, 130])
+def test_sample_language_model_rows(R):
+    """A power law over a shuffled vocabulary, odd and large."""
+    V = 70001
+    g = torch.Generator(device="cuda").manual_seed(R)
+    rank = torch.randperm(V, generator=g, device="cuda").float() + 1
+    t = (torch.randn(R, V, generator=g, device="cuda") - 1.3 * rank.log() + 9).bfloat16()
+    u = torch.rand(R, generator=g, device="cuda")
+    for s in SETTINGS:
+        _say("language model", R, s)
+        _sample_check(wb.sample(t, u, **s), t, u, **s)
 
 
 def test_sample_far_rows():

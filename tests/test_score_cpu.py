@@ -87,13 +87,14 @@ def test_sample_refuses(lib, kw, word):
     a.update(kw)
     cfg = score._SampleConfig(a["T"], a["k"], a["p"], a["mp"], None, None, None, None)
     rc = lib.wfst_sample(a["x"], a["xt"], a["xs"], a["rows"], a["V"], a["u"], ctypes.byref(cfg), None, 1, a["tok"],
-                         None, None, None)
+                         None, None, None, 0, None)
     assert rc == EINVAL and word in lib.wfst_last_error().decode()
 
 
 def test_no_rows_is_no_work(lib):
     cfg = score._SampleConfig(1.0, 0, 1.0, 0.0, None, None, None, None)
-    assert lib.wfst_sample(None, 0, 8, 0, 8, None, ctypes.byref(cfg), None, 1, None, None, None, None) == 0
+    assert lib.wfst_sample(None, 0, 8, 0, 8, None, ctypes.byref(cfg), None, 1, None, None, None, None, 0,
+                           None) == 0
     assert lib.wfst_log_softmax(None, 0, 8, 0, 8, 1.0, None, None, 1, None, 0, 8, None, 0, None) == 0
 
 

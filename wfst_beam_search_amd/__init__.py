@@ -30,7 +30,7 @@ EXPORTED_SYMBOLS = ("wfst_last_error", "wfst_graph_upload", "wfst_graph_release"
                     "wfst_decoder_kernel_times", "wfst_create_stream", "wfst_advance_chunk",
                     "wfst_finalize_stream", "wfst_finalize_streams", "wfst_create_streams", "wfst_release_stream", "wfst_lattice_records",
                     "wfst_blank_skip", "wfst_decode_noalloc", "wfst_layer_create", "wfst_layer_release",
-                    "wfst_layer_logits", "wfst_layer_workspace", "wfst_log_softmax", "wfst_log_softmax_workspace", "wfst_sample")
+                    "wfst_layer_logits", "wfst_layer_workspace", "wfst_log_softmax", "wfst_log_softmax_workspace", "wfst_sample", "wfst_sample_workspace")
 KERNELS = ("clear", "init", "lpmax", "max", "expand", "finalize", "eps_expand", "eps_resolve",
            "eps_apply", "backtrack", "stream_begin", "stream_end", "reclass", "lat_resolve", "lat_init",
            "lat_back", "gc_begin", "gc_mark", "gc_scan", "gc_compact", "gc_commit", "gc_roots", "gc_clear",
@@ -131,7 +131,8 @@ def load_library():
         lib.wfst_layer_workspace.argtypes = [vp, i32, i32, vp]
         lib.wfst_log_softmax.argtypes = [vp, i32, i64, i64, i32, f32, vp, vp, i32, vp, i32, i64, vp, i64, vp]
         lib.wfst_log_softmax_workspace.argtypes = [i32, i64, i32, i32, vp]
-        lib.wfst_sample.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, i32, vp, vp, vp, vp]
+        lib.wfst_sample.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, i32, vp, vp, vp, vp, i64, vp]
+        lib.wfst_sample_workspace.argtypes = [i32, i64, i32, vp]
         for name in EXPORTED_SYMBOLS:
             if name != "wfst_last_error":
                 getattr(lib, name).restype = ctypes.c_int

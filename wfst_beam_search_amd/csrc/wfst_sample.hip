@@ -813,6 +813,288 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
     }
 }
 
+// Few long rows: a first launch cuts each row into chunks of kChunkPacks packs a
+// thread of 256, one workgroup each, which reads its chunk once and leaves its
+// largest score, its mass relative to that (where a row needs its whole mass),
+// its number of labels above -inf, and a list of its labels above a bound of its
+// own. A second launch joins a row's chunks: labels at or above the largest of the
+// chunks' bounds are in the lists for certain, and draw_list works on those; where
+// they do not settle the row, draw_one takes it from its scores.
+constexpr int kChunkThreads = 256;
+constexpr int kChunkPacks = 2;
+constexpr int kChunkList = 256;                        // entries of a chunk's list
+constexpr int kMaxChunks = 1024;                       // of a row: one a thread of the join
+
+struct ChunkStat {
+    unsigned long long mass;                           // relative to `top`
+    float top;
+    uint32_t bound;                                    // key: all labels with a key above or at it are listed
+    uint32_t listed;                                   // may pass kChunkList: the list does not hold
+    uint32_t labels;                                   // above -inf
+};
+
+// What a row needs of its chunks.
+__device__ __forceinline__ bool row_needs_mass(const RowRules &row) { return !row.greedy && !row.cut_k; }
+__device__ __forceinline__ bool row_needs_list(const RowRules &row)
+{
+    return row.greedy || row.cut_k || row.cut_p || row.minp > 0.0f;
+}
+
+template <typename XT>
+__global__ __launch_bounds__(kChunkThreads) void k_draw_chunk(SampleCall c, int unit, int chunks, ChunkStat *stats,
+                                                              unsigned long long *lists)
+{
+    constexpr int VEC = 16 / sizeof(XT);
+    constexpr int WAVES = kChunkThreads / 64;
+    constexpr int kSpan = kChunkThreads * VEC;
+    __shared__ Hist hist;
+    __shared__ unsigned long long sum[WAVES];
+    __shared__ uint32_t a[WAVES], b[WAVES], n_list;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const Exp2Poly poly;
+    uint32_t round = 0;
+    clear_hist<kChunkThreads>(hist, 0);
+    for (int64_t w = blockIdx.x; w < c.rows * chunks; w += gridDim.x) {
+        const int64_t r = w / chunks;
+        if (!row_active(c.set, r)) continue;
+        const int v0 = (int)(w - r * chunks) * (kSpan * kChunkPacks);
+        const XT *x = (const XT *)c.x + r * c.x_stride;
+        const RowRules row(c, r);
+        float y[kChunkPacks][VEC];
+        float own = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kChunkPacks; ++i) load_scores<XT, VEC>(x, c.V, v0 + i * kSpan + tid * VEC, y[i]);
+        uint32_t labels = 0;
+#pragma unroll
+        for (int i = 0; i < kChunkPacks; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                own = fmaxf(own, y[i][j]);
+                labels += y[i][j] > -INFINITY ? 1u : 0u;
+            }
+        float top = wave_max_f(own);
+        labels = (uint32_t)wave_sum_u64(labels);
+        const bool have = own > -INFINITY;
+        const uint32_t key = score_key(own);
+        uint32_t low = have ? key : 0xFFFFFFFFu;           // the smallest of the threads' largest
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) low = min(low, (uint32_t)__shfl_xor((int)low, d, 64));
+        const uint32_t threads = __popcll(__ballot(have));
+        __syncthreads();
+        if (lane == 0) { a[wave] = __float_as_uint(top); b[wave] = low; sum[wave] = (unsigned long long)threads << 32 | labels; }
+        if (tid == 0) n_list = 0;
+        __syncthreads();
+        uint64_t both = 0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            top = fmaxf(top, __uint_as_float(a[i]));
+            low = min(low, b[i]);
+            both += sum[i];
+        }
+        labels = (uint32_t)both;
+        uint64_t mass_sum = 0;
+        if (row_needs_mass(row) && top > -INFINITY) {
+            const MassOf mass(top, row.T, 0.0f, unit, false);
+            mass_sum -= kChunkPacks * VEC * MassOf::kRaw;
+#pragma unroll
+            for (int i = 0; i < kChunkPacks; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) mass_sum += MassOf::raw(mass(mass.read(y[i][j]), poly));
+        }
+        mass_sum = wave_sum_u64(mass_sum);
+        uint32_t bound = kKeyNegInf + 1u;                  // all labels above -inf
+        if (row_needs_list(row) && top > -INFINITY) {
+            // enough labels of every chunk that all rows' lists together hold about 2048, or eight times top_k
+            const uint32_t share = row.greedy ? 1u
+                                   : row.cut_k ? (uint32_t)min((int64_t)192, 8 + 8 * (int64_t)row.topk / chunks)
+                                               : (uint32_t)min(192, max(8, 2048 / chunks));
+            const uint32_t kmax = score_key(top);
+            if ((uint32_t)(both >> 32) > share) {
+                const uint32_t far = kmax - low;
+                const uint64_t d = select_last<kChunkThreads, false>(
+                    hist, round,
+                    [&](auto f) {
+                        if (have) f((uint64_t)(kmax - key), (uint64_t)1);
+                    },
+                    far ? 32 - __clz((int)far) : 1, share, share + share / 4 + 4);
+                bound = max(bound, d < kmax ? kmax - (uint32_t)d : 0u);
+            }
+            const float floor_x = key_score(bound);
+            unsigned long long *list = lists + w * kChunkList;
+#pragma unroll
+            for (int i = 0; i < kChunkPacks; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    if (y[i][j] >= floor_x) {
+                        const uint32_t at = atomicAdd(&n_list, 1u);
+                        if (at < kChunkList)
+                            list[at] = (unsigned long long)score_key(y[i][j]) << 32 | (uint32_t)(v0 + i * kSpan + tid * VEC + j);
+                    }
+        }
+        __syncthreads();
+        if (lane == 0) sum[wave] = mass_sum;
+        __syncthreads();
+        if (tid == 0) {
+            ChunkStat st = {0, top, bound, n_list, labels};
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i) st.mass += sum[i];
+            stats[w] = st;
+        }
+    }
+}
+
+// Exclusive running sum over a workgroup, and its total.
+template <int WAVES>
+__device__ __forceinline__ uint64_t block_before(uint64_t v, unsigned long long *sum, uint64_t &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t run = wave_scan_u64(v);
+    __syncthreads();
+    if (lane == 63) sum[wave] = run;
+    __syncthreads();
+    uint64_t before = run - v;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+        before += i < wave ? (uint64_t)sum[i] : 0;
+        total += sum[i];
+    }
+    return before;
+}
+
+template <typename XT>
+__global__ __launch_bounds__(1024) void k_draw_join(SampleCall c, int unit, int ibits, int chunks, const ChunkStat *stats,
+                                                    const unsigned long long *lists)
+{
+    constexpr int THREADS = 1024, WAVES = 16, E = 4;
+    constexpr int VEC = 16 / sizeof(XT);
+    constexpr int kChunk = kChunkThreads * VEC * kChunkPacks;
+    constexpr int kEach = kChunk / THREADS;
+    __shared__ DrawShared<THREADS, E, false> s;
+    __shared__ uint16_t n_listed[kMaxChunks];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const Exp2Poly poly;
+    uint32_t round = 0;
+    clear_hist<THREADS>(s.hist, 0);
+    for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+        if (!row_active(c.set, r)) continue;
+        __syncthreads();
+        const RowRules row(c, r);
+        const XT *x = (const XT *)c.x + r * c.x_stride;
+        const bool mine = tid < chunks;
+        ChunkStat st = {0, -INFINITY, kKeyNegInf + 1u, 0, 0};
+        if (mine) st = stats[r * chunks + tid];
+        float top = wave_max_f(st.top);
+        uint32_t bound = st.bound;
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) bound = max(bound, (uint32_t)__shfl_xor((int)bound, d, 64));
+        const uint64_t spilt = __ballot(st.listed > kChunkList);
+        if (lane == 0) { s.a[wave] = __float_as_uint(top); s.b[wave] = bound; s.sum[wave] = spilt; }
+        if (tid == 0) s.count = 0;
+        __syncthreads();
+        bool whole = true;                                 // every chunk's list holds
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            top = fmaxf(top, __uint_as_float(s.a[i]));
+            bound = max(bound, s.b[i]);
+            whole = whole && s.sum[i] == 0;
+        }
+        if (top == -INFINITY) {
+            if (tid == 0) emit(c, r, -1, -INFINITY, 0);
+            continue;
+        }
+        const bool all = bound == kKeyNegInf + 1u;         // the lists hold the whole row
+        const MassOf mass(top, row.T, row.minp, unit, row.greedy);
+        const uint32_t kmax = score_key(mass.read(top));
+        // the chunks' masses, brought to the row's largest score
+        uint64_t z = 0, before = 0;
+        if (row_needs_mass(row)) {
+            const double w = mass(mass.read(st.top), poly) * ((double)st.mass / mass.one);
+            const uint64_t m = st.top > -INFINITY ? (uint64_t)rint(w) : 0;
+            before = block_before<WAVES>(m, s.sum, z);
+            st.mass = m;
+        }
+        if (!row_needs_list(row)) {
+            // no rule but the temperature: the chunk that holds the token, then its labels
+            uint64_t labels;
+            (void)block_before<WAVES>(mass.pick ? 0 : st.labels, s.sum, labels);
+            const uint64_t goal = draw_goal(row.u, z);
+            __syncthreads();
+            if (before < goal && goal <= before + st.mass) { s.first = (uint32_t)tid; s.sum[0] = before; }
+            __syncthreads();
+            const int v = (int)s.first * kChunk + tid * kEach;
+            const uint64_t front = s.sum[0];
+            float y[kEach];
+            uint64_t w[kEach], own = 0, total;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                y[j] = v + j < c.V ? mass.read((float)x[v + j]) : -INFINITY;
+                w[j] = MassOf::fixed(mass(y[j], poly));
+                own += w[j];
+            }
+            uint64_t run = block_before<WAVES>(own, s.sum, total);
+            // (the chunk's own sum differs from its share of z by roundings)
+            const uint64_t left = min(goal - front, total);
+            uint32_t found = 0xFFFFFFFFu;
+            float score = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                if (run < left && left <= run + w[j]) { found = v + j; score = y[j]; }
+                run += w[j];
+            }
+            if (mass.pick) labels = (uint64_t)rint((double)z / mass.one);
+            if (found != 0xFFFFFFFFu) emit(c, r, (int)found, mass.log_prob(score, z), (uint32_t)labels);
+            if (total) continue;                           // (0 only where the chunk's whole share was one rounding)
+        } else if (whole && (all || row.greedy || row.cut_k || row.cut_p ||
+                             mass(mass.read(key_score(bound)), poly) < mass.lim)) {
+            // all lists at once, as many places of each as the longest fills (a power of two)
+            uint32_t most = st.listed;
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, d, 64));
+            if (lane == 0) s.b[wave] = most;
+            n_listed[tid] = (uint16_t)st.listed;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i) most = max(most, s.b[i]);
+            const int places = most > 1 ? 32 - __clz((int)most - 1) : 0;
+#pragma unroll 4
+            for (int i = tid; i < chunks << places; i += THREADS) {
+                const int q = i >> places;
+                const uint32_t at_q = i & ((1u << places) - 1u);
+                if (at_q < n_listed[q]) {
+                    const uint64_t e = lists[(r * chunks + q) * kChunkList + at_q];
+                    const float y = mass.read(key_score((uint32_t)(e >> 32)));
+                    if ((uint32_t)(e >> 32) >= bound && y > -INFINITY) {
+                        const uint32_t at = atomicAdd(&s.count, 1u);
+                        if (at < E * THREADS) s.list[at] = (uint64_t)(kmax - score_key(y)) << ibits | (uint32_t)e;
+                    }
+                }
+            }
+            __syncthreads();
+            const uint32_t n = s.count;
+            if (n <= E * THREADS && (all || row.greedy || !row.cut_k || n >= (uint32_t)row.topk)) {
+                uint64_t el[E], ew[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const uint32_t at = i * THREADS + tid;
+                    const uint64_t e = s.list[at];
+                    const uint64_t w = MassOf::fixed(mass(key_score(kmax - (uint32_t)(e >> ibits)), poly));
+                    el[i] = at < n ? e : ~0ull;
+                    ew[i] = at < n ? w : 0;
+                }
+                __syncthreads();
+                const uint32_t far = mass.pick ? 0u : kmax - bound;
+                const int digits = ibits + (far ? 32 - __clz((int)far) : 1);
+                if (draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits,
+                                          all || row.cut_k ? 0 : z, s, round))
+                    continue;
+            }
+        }
+        __syncthreads();
+        draw_one<XT, THREADS, E, false>(c, r, row, poly, unit, ibits, s, round);
+    }
+}
+
 // Wavefronts a row: one where the rows are many (the fixed work of a row, its
 // scans and its logarithm, is then done once), more where few rows would leave
 // the card idle.
@@ -836,7 +1118,14 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
     while ((1ll << ibits) < (long long)c.V) ++ibits;
     const int unit = std::min(51, 62 - ibits);
     const dim3 g((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid));
-    if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps) draw_all<XT>(c, unit, s);
+    const int chunks = sample_chunks(c.rows, c.V, c.x_dtype);
+    if (chunks) {
+        ChunkStat *stats = (ChunkStat *)c.workspace;
+        unsigned long long *lists = (unsigned long long *)(stats + c.rows * chunks);
+        const dim3 gc((unsigned)std::min<int64_t>(c.rows * chunks, kMaxRowGrid));
+        hipLaunchKernelGGL(k_draw_chunk<XT>, gc, dim3(kChunkThreads), 0, s, c, unit, chunks, stats, lists);
+        hipLaunchKernelGGL(k_draw_join<XT>, g, dim3(1024), 0, s, c, unit, ibits, chunks, stats, lists);
+    } else if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps) draw_all<XT>(c, unit, s);
     else if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits);
     else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits);
     else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits);
@@ -844,6 +1133,20 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
 }
 
 }  // namespace
+
+// Chunks a row is cut into, 0 for rows that stay whole.
+int sample_chunks(int64_t rows, int32_t V, int32_t x_dtype)
+{
+    const int chunk = kChunkThreads * kChunkPacks * (16 / (int)dtype_size(x_dtype));
+    const int chunks = (V + chunk - 1) / chunk;
+    const char *e = getenv("SPLIT_ROWS");
+    return rows <= (e ? atoi(e) : 128) && V > 8192 && chunks <= kMaxChunks ? chunks : 0;
+}
+
+size_t sample_workspace(int64_t rows, int32_t V, int32_t x_dtype)
+{
+    return (size_t)rows * sample_chunks(rows, V, x_dtype) * (sizeof(ChunkStat) + kChunkList * 8);
+}
 
 hipError_t launch_sample(const SampleCall &c, hipStream_t s)
 {

@@ -104,7 +104,11 @@ struct SampleCall {
     float *log_prob;            // may be null
     int32_t *kept;              // may be null
     RowSet set;
+    void *workspace;            // sample_workspace bytes
 };
+
+int sample_chunks(int64_t rows, int32_t V, int32_t x_dtype);
+size_t sample_workspace(int64_t rows, int32_t V, int32_t x_dtype);
 
 hipError_t launch_sample(const SampleCall &c, hipStream_t s);
 

@@ -328,9 +328,22 @@ extern "C" int wfst_log_softmax_workspace(int32_t x_dtype, int64_t rows, int32_t
     });
 }
 
+extern "C" int wfst_sample_workspace(int32_t x_dtype, int64_t rows, int32_t V, int64_t *bytes)
+{
+    return guarded([&]() -> int {
+        if (!dtype_ok(x_dtype)) return api_fail(WFST_EINVAL, "not an element type");
+        if (rows < 0 || rows > ((int64_t)1 << 40)) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^40]");
+        if (V < 1 || V > (1 << 24)) return api_fail(WFST_EINVAL, "V must lie in [1, 2^24]");
+        if (!bytes) return api_fail(WFST_EINVAL, "a pointer is null");
+        *bytes = (int64_t)sample_workspace(rows, V, x_dtype);
+        return WFST_OK;
+    });
+}
+
 extern "C" int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, const float *u,
                            const wfst_sample_config *cfg, const int32_t *lengths, int32_t T, int32_t *out_tokens,
-                           float *out_log_probs, int32_t *out_kept, void *stream)
+                           float *out_log_probs, int32_t *out_kept, void *workspace, int64_t workspace_bytes,
+                           void *stream)
 {
     return guarded([&]() -> int {
         if (!cfg) return api_fail(WFST_EINVAL, "config is null");
@@ -374,6 +387,12 @@ extern "C" int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int
         }
         TRY(check_lengths(lengths, rows, T, device));
         TRY(check_stream(stream, device));
+        const size_t need = sample_workspace(rows, V, x_dtype);
+        TRY(check_workspace(workspace, workspace_bytes, need, device, x, xb, out_tokens, rb));
+        if (need)
+            for (const auto &a : row_args)
+                if (a.p && ranges_meet(workspace, (int64_t)need, a.p, rb))
+                    return api_fail(WFST_EINVAL, std::string("workspace overlaps ") + a.name);
         SampleCall c{};
         c.x = x;
         c.x_stride = x_stride;
@@ -393,6 +412,7 @@ extern "C" int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int
         c.log_prob = out_log_probs;
         c.kept = out_kept;
         c.set = {lengths, T};
+        c.workspace = workspace;
         HIP_TRY(launch_sample(c, (hipStream_t)stream));
         return WFST_OK;
     });

@@ -321,6 +321,13 @@ def _setting(v, dtype, shape, device, name):
     return 0, v
 
 
+@functools.lru_cache(maxsize=256)
+def _sample_bytes(code, rows, V):
+    need = ctypes.c_int64(0)
+    _check(load_library().wfst_sample_workspace(code, rows, V, ctypes.byref(need)))
+    return need.value
+
+
 def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=None, out=None,
            stream=None) -> SampleResult:
     """Draw one token of each row of ``scores`` [..., V] (logits or
@@ -356,6 +363,9 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
             if o is None or not _out(o, shape, dt, device, other).is_contiguous():
                 raise ValueError("out must be three packed tensors (int32, float32, int32)")
     cfg = _SampleConfig(float(t), int(k), float(p), float(mp), _p(ts), _p(ks), _p(ps), _p(mps))
-    _check(lib.wfst_sample(scores.data_ptr(), code, step, rows, int(scores.shape[-1]), u.data_ptr(),
-                           ctypes.byref(cfg), _p(lengths), T, _p(res.tokens), _p(res.log_probs), _p(res.kept), raw))
+    V = int(scores.shape[-1])
+    need = _sample_bytes(code, rows, V)
+    work = _workspace(need, device, other)
+    _check(lib.wfst_sample(scores.data_ptr(), code, step, rows, V, u.data_ptr(), ctypes.byref(cfg), _p(lengths), T,
+                           _p(res.tokens), _p(res.log_probs), _p(res.kept), _p(work), need, raw))
     return res
