@@ -165,30 +165,37 @@ template <int WAVES> struct RowSums {
     uint32_t kept[WAVES];
 };
 
-// Draw from the row itself by the WAVES wavefronts of a workgroup (or each
-// wavefront on a row of its own). Every wavefront owns one contiguous run of
-// packs of 64 * VEC labels; the sums of the wavefronts, then of their packs, then
-// of the lanes say where the token lies. raw_of(score, label, kept) is a label's
-// MassOf::raw (score as MassOf::read gives it), counting it if it is kept.
+// Draw from the scores x[0 .. V) (labels base ..) by the WAVES wavefronts of a
+// workgroup (or each wavefront on a row of its own). Every wavefront owns one
+// contiguous run of packs of 64 * VEC labels; the sums of the wavefronts, then of
+// their packs, then of the lanes say where the token lies. raw_of(score, label,
+// kept) is a label's MassOf::raw, counting it if it is kept. span: the token is
+// known to lie here, where the running mass is span.goal, and the row's mass and
+// count are known.
+struct DrawSpan {
+    uint64_t goal, total;      // goal 0: not known
+    uint32_t kept;
+};
+
 template <typename XT, int WAVES, typename Mass>
-__device__ __forceinline__ void draw_row(const SampleCall &c, int64_t r, const XT *x, const MassOf &mass, float u,
-                                         RowSums<WAVES> &s, Mass raw_of)
+__device__ __forceinline__ void draw_row(const SampleCall &c, int64_t r, const XT *x, int V, int base, const MassOf &mass,
+                                         float u, RowSums<WAVES> &s, const DrawSpan &span, Mass raw_of)
 {
     constexpr int VEC = 16 / sizeof(XT);
     constexpr int kPackW = 64 * VEC;
     const int lane = threadIdx.x & 63, wave = WAVES == 1 ? 0 : threadIdx.x >> 6;
-    const int packs = (c.V + WAVES * kPackW - 1) / (WAVES * kPackW);     // of one wavefront
+    const int packs = (V + WAVES * kPackW - 1) / (WAVES * kPackW);       // of one wavefront
     const int group = (packs + 63) / 64;                                 // packs whose sum one lane keeps
     const int v0 = wave * packs * kPackW;
     uint64_t part = 0, own = 0;                      // of the lane's group of packs; of the wavefront
     uint32_t kept = 0;
-    for (int i = 0, g = 0, in = 0; i < packs && v0 + i * kPackW < c.V; ++i) {
+    for (int i = 0, g = 0, in = 0; i < packs && v0 + i * kPackW < V; ++i) {
         const int v = v0 + i * kPackW + lane * VEC;
         float y[VEC];
-        load_scores<XT, VEC>(x, c.V, v, y);
+        load_scores<XT, VEC>(x, V, v, y);
         uint64_t w = (uint64_t)0 - VEC * MassOf::kRaw;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w += raw_of(y[j], v + j, kept);
+        for (int j = 0; j < VEC; ++j) w += raw_of(y[j], base + v + j, kept);
         w = wave_sum_u64(w);
         part += lane == g ? w : 0;
         own += w;
@@ -208,11 +215,17 @@ __device__ __forceinline__ void draw_row(const SampleCall &c, int64_t r, const X
             kept += s.kept[w];
         }
     }
-    if (total == 0) {                                // (no label with a score above -inf)
-        if (lane == 0 && wave == 0) emit(c, r, -1, -INFINITY, 0);
-        return;
+    uint64_t goal = span.goal;
+    if (goal) {
+        total = span.total;
+        kept = span.kept;
+    } else {
+        if (total == 0) {                            // (no label with a score above -inf)
+            if (lane == 0 && wave == 0) emit(c, r, -1, -INFINITY, 0);
+            return;
+        }
+        goal = mass.greedy ? 1 : draw_goal(u, total);
     }
-    const uint64_t goal = mass.greedy ? 1 : draw_goal(u, total);
     if (goal <= before || goal > before + own) return;       // (one wavefront goes on)
     const uint64_t run = before + wave_scan_u64(part);
     const int at = __ffsll((unsigned long long)__ballot(run >= goal)) - 1;
@@ -220,12 +233,12 @@ __device__ __forceinline__ void draw_row(const SampleCall &c, int64_t r, const X
     for (int i = at * group; i < packs; ++i) {
         const int v = v0 + i * kPackW + lane * VEC;
         float y[VEC];
-        load_scores<XT, VEC>(x, c.V, v, y);
+        load_scores<XT, VEC>(x, V, v, y);
         uint64_t w[VEC], mine = 0;
         uint32_t n = 0;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            w[j] = raw_of(y[j], v + j, n) - MassOf::kRaw;
+            w[j] = raw_of(y[j], base + v + j, n) - MassOf::kRaw;
             mine += w[j];
         }
         const uint64_t upto = before + wave_scan_u64(mine);
@@ -240,7 +253,7 @@ __device__ __forceinline__ void draw_row(const SampleCall &c, int64_t r, const X
                     acc += w[j];
                     if (found < 0 && acc >= goal) { found = j; score = mass.read(y[j]); }
                 }
-                emit(c, r, v + found, mass.greedy ? 0.0f : mass.log_prob(score, total), mass.greedy ? 1 : kept);
+                emit(c, r, base + v + found, mass.greedy ? 0.0f : mass.log_prob(score, total), mass.greedy ? 1 : kept);
             }
             return;
         }
@@ -287,7 +300,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
         // Two forms: the tests of the general one, as selects, take half as long again as the sum itself.
         // Without them -inf and NaN have the mass 2^-1000, which rounds to 0.
         if (__builtin_amdgcn_readfirstlane(mass.pick || mass.lim > 0.0)) {
-            draw_row<XT, WAVES>(c, r, x, mass, u, s, [&](float y, int, uint32_t &n) {
+            draw_row<XT, WAVES>(c, r, x, c.V, 0, mass, u, s, {0, 0, 0}, [&](float y, int, uint32_t &n) {
                 y = mass.read(y);
                 const double w = mass(y, poly);
                 const bool keep = y > -INFINITY && w >= mass.lim;
@@ -295,7 +308,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
                 return MassOf::raw(keep ? w : 0.0);
             });
         } else {
-            draw_row<XT, WAVES>(c, r, x, mass, u, s, [&](float y, int, uint32_t &n) {
+            draw_row<XT, WAVES>(c, r, x, c.V, 0, mass, u, s, {0, 0, 0}, [&](float y, int, uint32_t &n) {
                 n += y > -INFINITY ? 1u : 0u;
                 return MassOf::raw(mass(y, poly));
             });
@@ -304,11 +317,17 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
     }
 }
 
+struct Digit {
+    uint32_t digit, count;
+    uint64_t before, mine;
+};
+
 // Histograms of 256 digits, three in turn: a round adds to one while the next is
-// cleared, and the third may still be read by wavefronts of the round before.
+// cleared, and the third may still be read for the round before.
 struct Hist {
     unsigned long long mass[3][256];
     uint32_t cnt[3][256];
+    Digit found;
 };
 
 template <int THREADS>
@@ -317,24 +336,20 @@ __device__ __forceinline__ void clear_hist(Hist &h, int slot)
     for (int i = threadIdx.x; i < 256; i += THREADS) { h.mass[slot][i] = 0; h.cnt[slot][i] = 0; }
 }
 
-// The digit in which the running sum over a histogram, from `above`, reaches
-// target: the sum before it, its own, its count; digit 256 if none does. Every
-// wavefront finds it, four digits to a lane.
-struct Digit {
-    uint32_t digit, count;
-    uint64_t before, mine;
-};
+// The digit in which the running sum over 256 bins, from `above`, reaches target:
+// the sum before it, its own, its count; digit 256 if none does. By one wavefront,
+// four digits to a lane.
 
-template <bool MASS>
-__device__ __forceinline__ Digit find_digit(const Hist &h, int slot, uint64_t above, uint64_t target)
+__device__ __forceinline__ Digit find_digit(const unsigned long long *mass, const uint32_t *cnt, bool by_mass,
+                                            uint64_t above, uint64_t target)
 {
     const int lane = threadIdx.x & 63;
     uint32_t c[4];
     uint64_t w[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        c[i] = h.cnt[slot][lane * 4 + i];
-        w[i] = MASS ? (uint64_t)h.mass[slot][lane * 4 + i] : c[i];
+        c[i] = cnt[lane * 4 + i];
+        w[i] = by_mass ? (uint64_t)mass[lane * 4 + i] : c[i];
         sum += w[i];
     }
     uint64_t acc = above + wave_scan_u64(sum) - sum;
@@ -342,7 +357,11 @@ __device__ __forceinline__ Digit find_digit(const Hist &h, int slot, uint64_t ab
     Digit r = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (d == 4 && acc + w[i] >= target) { d = i; r.before = acc; r.mine = w[i]; r.count = c[i]; }
+        const bool hit = d == 4 && acc + w[i] >= target;
+        d = hit ? i : d;
+        r.before = hit ? acc : r.before;
+        r.mine = hit ? w[i] : r.mine;
+        r.count = hit ? c[i] : r.count;
         acc += w[i];
     }
     const uint64_t hit = __ballot(d < 4);
@@ -355,16 +374,18 @@ __device__ __forceinline__ Digit find_digit(const Hist &h, int slot, uint64_t ab
 }
 
 // The value `last` at which the elements, taken in ascending order of their
-// numbers, reach `target` (in counts, or in masses): the one that reaches it and
+// numbers, reach `target` (in masses, or in counts): the one that reaches it and
 // all before are <= last, the others are not. each(f) calls f(number, mass) for
 // the thread's elements; digits is the position of the highest bit set in any
 // number, plus one. The search goes down by digits of 8 bits until a digit holds
 // one element, or (counts) the elements up to its end are at most `enough`.
 // `round` counts the histograms used in this workgroup; its slot is clear on
-// entry and on return. target must not pass the elements' total.
-template <int THREADS, bool MASS, typename Each>
-__device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each each, int digits, uint64_t target,
-                                                uint64_t enough)
+// entry and on return. target must not pass the elements' total. The first
+// wavefront looks for the digit: all sixteen at once would take its time four
+// times over.
+template <int THREADS, typename Each>
+__device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each each, bool by_mass, int digits,
+                                                uint64_t target, uint64_t enough)
 {
     uint64_t prefix = 0, above = 0;
     int shift = digits;                                // the digits above it are fixed
@@ -376,16 +397,21 @@ __device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each e
             if (num >> shift == prefix) {
                 const uint32_t d = (uint32_t)(num >> next) & ((1u << width) - 1u);
                 atomicAdd(&h.cnt[slot][d], 1u);
-                if (MASS) atomicAdd(&h.mass[slot][d], (unsigned long long)w);
+                if (by_mass) atomicAdd(&h.mass[slot][d], (unsigned long long)w);
             }
         });
         __syncthreads();
+        if (threadIdx.x < 64) {
+            const Digit d = find_digit(h.mass[slot], h.cnt[slot], by_mass, above, target);
+            if (threadIdx.x == 0) h.found = d;
+        }
+        __syncthreads();
         ++round;
-        const Digit d = find_digit<MASS>(h, slot, above, target);
+        const Digit d = h.found;
         prefix = prefix << width | (d.digit & 255u);
         above = d.before;
         shift = next;
-        const bool whole = !MASS && above + d.mine <= enough;
+        const bool whole = !by_mass && above + d.mine <= enough;
         if (d.count <= 1 || whole || shift == 0) return ((prefix + 1) << shift) - 1;
     }
 }
@@ -446,35 +472,31 @@ __device__ __forceinline__ void element_totals(S &s, Each each, uint32_t &n, uin
     for (int i = 0; i < WAVES; ++i) { n += s.b[i]; w += s.sum[i]; }
 }
 
-// Cut by top_k and top_p among the elements that each(last, f) gives; total: the
-// mass top_p is a share of where that is not the elements' own (0 otherwise).
-// False: their mass falls short of it.
+// Cut by top_k and top_p among the elements that each(last, f) gives.
 template <int THREADS, typename S, typename Each>
-__device__ __forceinline__ bool cut_elements(S &s, uint32_t &round, const RowRules &row, Each each, int digits,
-                                             uint64_t total, uint64_t &last)
+__device__ __forceinline__ void cut_elements(S &s, uint32_t &round, const RowRules &row, Each each, int digits,
+                                             uint64_t &last)
 {
-    constexpr int WAVES = THREADS / 64;
     const auto now = [&](auto f) { each(last, f); };
-    uint32_t n;
-    uint64_t w;
-    if (row.cut_k) {
-        element_totals<WAVES>(s, now, n, w);
-        if ((uint32_t)row.topk < n)
-            last = min(last, select_last<THREADS, false>(s.hist, round, now, digits, (uint64_t)row.topk,
-                                                         (uint64_t)row.topk));
-    }
-    if (row.cut_p) {
-        element_totals<WAVES>(s, now, n, w);
-        const uint64_t target = top_p_goal(row.topp, total ? total : w);
-        if (target > w) return false;
+#pragma unroll 1
+    for (int rule = 0; rule < 2; ++rule) {
+        if (!(rule ? row.cut_p : row.cut_k)) continue;
+        uint32_t n;
+        uint64_t w;
+        element_totals<THREADS / 64>(s, now, n, w);
+        if (!rule && (uint32_t)row.topk >= n) continue;
+        const uint64_t target = rule ? top_p_goal(row.topp, w) : (uint64_t)row.topk;
         // (the search may end above what top_k left: at the end of a digit that held one label)
-        last = min(last, select_last<THREADS, true>(s.hist, round, now, digits, target, 0));
+        last = min(last, select_last<THREADS>(s.hist, round, now, rule, digits, target, (uint64_t)row.topk));
     }
-    return true;
 }
 
 // Cut a list of elements (number, mass; ~0: none) that holds all labels which may
-// be kept, and draw from it. False, and nothing written: see cut_elements.
+// be kept, and draw from it. total_p: the mass top_p is a share of where that is
+// not the elements' own (0 otherwise); false, and nothing written, if their mass
+// falls short of it. The three searches (top_k, top_p, the draw by index) share
+// one piece of code: a row's time here is latency, and code that runs once is
+// fetched as it runs.
 template <int THREADS, int E, typename S>
 __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const RowRules &row, const MassOf &mass,
                                           const Exp2Poly &poly, uint32_t kmax, int ibits, uint64_t (&el)[E],
@@ -482,57 +504,63 @@ __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const 
 {
     constexpr int WAVES = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t last = ~0ull - 1;
-    if (!cut_elements<THREADS>(
-            s, round, row,
-            [&](uint64_t upto, auto f) {
+    const uint64_t imask = ((uint64_t)1 << ibits) - 1;
+    uint64_t last = ~0ull - 1, mask = ~0ull, total = 0;
+    uint32_t n = 0;
+#pragma unroll 1
+    for (int rule = 0; rule < 3; ++rule) {
+        if (rule == 0 ? !row.cut_k : rule == 1 ? !row.cut_p : false) continue;
+        if (rule == 2) {
+            // (by selects: the compiler has been seen to lose stores to such arrays under divergent branches)
+            if (mass.lim > 0.0) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const double w = mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly);
+                    el[i] = w >= mass.lim ? el[i] : ~0ull;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < E; ++i) el[i] = el[i] <= last ? el[i] : ~0ull;
+            last = ~0ull - 1;
+            mask = imask;
+            digits = max(ibits, 1);
+        }
+        element_totals<WAVES>(
+            s,
+            [&](auto f) {
 #pragma unroll
                 for (int i = 0; i < E; ++i)
-                    if (el[i] <= upto) f(el[i], ew[i]);
+                    if (el[i] <= last) f(el[i], ew[i]);
             },
-            digits, total_p, last))
-        return false;
-    const uint64_t imask = ((uint64_t)1 << ibits) - 1;
-    // (by selects: the compiler has been seen to lose stores to such arrays under divergent branches)
-    if (mass.lim > 0.0) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const double w = mass(key_score(kmax - (uint32_t)(el[i] >> ibits)), poly);
-            el[i] = w >= mass.lim ? el[i] : ~0ull;
+            n, total);
+        if (rule == 0 && (uint32_t)row.topk >= n) continue;
+        uint64_t target = (uint64_t)row.topk;
+        if (rule == 1) {
+            target = top_p_goal(row.topp, total_p ? total_p : total);
+            if (target > total) return false;
         }
+        if (rule == 2) target = row.greedy ? 1 : draw_goal(row.u, total);
+        // (the search may end above what top_k left: at the end of a digit that held one label)
+        last = min(last, select_last<THREADS>(
+                             s.hist, round,
+                             [&](auto f) {
+#pragma unroll
+                                 for (int i = 0; i < E; ++i)
+                                     if (el[i] <= last && (rule < 2 || ew[i])) f(el[i] & mask, ew[i]);
+                             },
+                             rule > 0, digits, target, target));
     }
-#pragma unroll
-    for (int i = 0; i < E; ++i) el[i] = el[i] <= last ? el[i] : ~0ull;
-    uint32_t n;
-    uint64_t total;
-    element_totals<WAVES>(
-        s,
-        [&](auto f) {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (el[i] != ~0ull) f(el[i], ew[i]);
-        },
-        n, total);
-    const uint64_t end = select_last<THREADS, true>(
-        s.hist, round,
-        [&](auto f) {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (el[i] != ~0ull && ew[i]) f(el[i] & imask, ew[i]);
-        },
-        max(ibits, 1), row.greedy ? 1 : draw_goal(row.u, total), 0);
-    // the last label with mass at or before `end`: no other shares its digits
+    // the last label with mass at or before `last`: no other shares its digits
     uint32_t at = 0;
     float y = 0.0f;
     bool have = false;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const uint32_t v = (uint32_t)(el[i] & imask);
-        if (el[i] != ~0ull && ew[i] && v <= end && (!have || v > at)) {
-            at = v;
-            y = key_score(kmax - (uint32_t)(el[i] >> ibits));
-            have = true;
-        }
+        const bool later = el[i] != ~0ull && ew[i] && v <= last && (!have || v > at);
+        at = later ? v : at;
+        y = later ? key_score(kmax - (uint32_t)(el[i] >> ibits)) : y;
+        have = have || later;
     }
     uint32_t best = have ? at + 1 : 0;
 #pragma unroll
@@ -644,11 +672,11 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                 ew[i] = at < count ? w : 0;
             }
         };
-        uint64_t z = 0;                                // mass of all labels (top_p without top_k)
-        // A bound that at least `want` threads' largest scores reach: the labels that reach it are that many or
-        // more, and among labels in random order not many more than that
-        const uint32_t want = row.cut_k ? (uint32_t)row.topk : THREADS * 3 / 4;
-        if (want <= THREADS * 7 / 8) {
+        bool done = false;
+        if (row.cut_k && row.topk <= THREADS * 7 / 8) {
+            // A bound that at least top_k threads' largest scores reach: the labels that reach it are that many or
+            // more, and among labels in random order not many more than that
+            const uint32_t want = (uint32_t)row.topk;
             const uint32_t mine = own > -INFINITY ? kmax - score_key(own) : 0xFFFFFFFFu;
             uint32_t far = mine == 0xFFFFFFFFu ? 0 : mine, n = __popcll(__ballot(mine != 0xFFFFFFFFu));
 #pragma unroll
@@ -661,28 +689,22 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
             uint32_t bound = kmax - kKeyNegInf - 1u;                    // all labels above -inf
             if (n > want) {
                 const int bits = far ? 32 - __clz((int)far) : 1;
-                const uint64_t b = select_last<THREADS, false>(
+                const uint64_t b = select_last<THREADS>(
                     s.hist, round,
                     [&](auto f) {
                         if (mine != 0xFFFFFFFFu) f((uint64_t)mine, (uint64_t)1);
                     },
-                    bits, want, want + want / 4 + 8);
+                    false, bits, want, want + want / 4 + 8);
                 bound = (uint32_t)min(b, (uint64_t)bound);
             }
             const float floor_x = key_score(kmax - bound);
-            const bool need_z = !row.cut_k;
+#pragma unroll 2
             for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
                 float y[VEC];
                 load(v, y);
                 uint32_t hits = 0;
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) hits |= (y[j] >= floor_x ? 1u : 0u) << j;
-                if (need_z) {
-                    // (-inf and NaN have the mass 2^-1000, which rounds to 0)
-                    z -= VEC * MassOf::kRaw;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) z += MassOf::raw(mass(y[j], poly));
-                }
                 if (hits) {
                     uint32_t at = atomicAdd(&s.count, (uint32_t)__popc(hits));
 #pragma unroll
@@ -693,81 +715,137 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                         }
                 }
             }
-            if (need_z) {
-                z = wave_sum_u64(z);
-                if (lane == 0) s.sum[wave] = z;
-            }
             __syncthreads();
-            if (need_z) {
-                z = 0;
-                for (int w = 0; w < WAVES; ++w) z += s.sum[w];
-            }
             const uint32_t count = s.count;
-            take(min(count, (uint32_t)kCap));
-            __syncthreads();
             if (count <= kCap) {
+                take(count);
+                __syncthreads();
                 const int digits = ibits + (bound ? 32 - __clz((int)bound) : 1);
-                if (draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, z, s, round)) return;
+                draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, 0, s, round);
+                return;
             }
-        }
-
-        bool done = false;
-        if (z) {
-            // top_p alone, its labels more than the list holds: masses by 256 equal steps of the score, from the
-            // top down to where all labels below together weigh less than 1 - top_p; then a list of the step that
-            // reaches the target
-            const uint64_t target = top_p_goal(row.topp, z);
-            const double least = (1.0 - (double)row.topp) * (double)z / (mass.one * (double)V);
+            __syncthreads();
+        } else if (!row.cut_k) {
+            // top_p alone. In one pass the mass of all labels and, by 256 equal steps of the score and each
+            // wavefront's piece, of those that may be kept: the others weigh less than 1 - top_p even all together
+            // (and even if the largest score were the only other mass). The steps say in which the nucleus ends;
+            // a list of that step's labels, exactly where; the pieces' masses, in which piece the token lies.
+            const double least = (1.0 - (double)row.topp) / (double)V;
             double low = mass.m + mass.t * log(least);
             low -= 1e-6 * (fabs(low) + fabs(mass.m));
             const float y_low = low > -3.4028234663852886e38 ? (float)low : -3.4028234663852886e38f;
             const float steps = 255.9f / (high - y_low);
             const float scale = steps < INFINITY && steps > 0.0f ? steps : 0.0f;
             const auto step_of = [&](float y) { return min(255u, (uint32_t)((high - y) * scale)); };
-            const int slot = round % 3;
-            clear_hist<THREADS>(s.hist, (round + 1) % 3);
-            if (tid == 0) { s.count = 0; s.first = 0; }
+            // (the list's room serves as the pieces' histograms first)
+            unsigned long long *piece = s.list;
+            static_assert(HOLD || WAVES * 256 <= kCap, "histograms fit the list's room");
+            for (int i = tid; i < WAVES * 256; i += THREADS) piece[i] = 0;
+            __syncthreads();
+            uint64_t z = 0;
             for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
                 float y[VEC];
                 load(v, y);
+                z -= VEC * MassOf::kRaw;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    if (y[j] >= y_low) {
-                        const uint32_t d = step_of(y[j]);
-                        atomicAdd(&s.hist.cnt[slot][d], 1u);
-                        atomicAdd(&s.hist.mass[slot][d], (unsigned long long)MassOf::fixed(mass(y[j], poly)));
-                    }
+                for (int j = 0; j < VEC; ++j) {
+                    // (-inf and NaN have the mass 2^-1000, which rounds to 0)
+                    const uint64_t w = MassOf::raw(mass(y[j], poly));
+                    z += w;
+                    if (y[j] >= y_low) atomicAdd(&piece[wave * 256 + step_of(y[j])], (unsigned long long)(w - MassOf::kRaw));
+                }
+            }
+            z = wave_sum_u64(z);
+            if (lane == 0) s.sum[wave] = z;
+            if (tid == 0) { s.count = 0; s.first = 0; }
+            __syncthreads();
+            z = 0;
+            for (int w = 0; w < WAVES; ++w) z += s.sum[w];
+            const uint64_t target = top_p_goal(row.topp, z);
+            const int slot = round % 3;
+            for (int i = tid; i < 256; i += THREADS) {
+                unsigned long long w = 0;
+                for (int q = 0; q < WAVES; ++q) w += piece[q * 256 + i];
+                s.hist.mass[slot][i] = w;
+            }
+            clear_hist<THREADS>(s.hist, (round + 1) % 3);
+            __syncthreads();
+            if (wave == 0) {
+                const Digit d = find_digit(s.hist.mass[slot], s.hist.cnt[slot], true, 0, target);
+                if (tid == 0) s.hist.found = d;
             }
             __syncthreads();
             ++round;
-            const Digit d = find_digit<true>(s.hist, slot, 0, target);
-            if (d.digit < 256 && d.count <= kCap) {
+            const Digit d = s.hist.found;
+            if (d.digit < 256) {
+                // each wavefront's mass above the step
+                uint64_t over = 0;
+                for (uint32_t i = lane; i < d.digit; i += 64) over += piece[wave * 256 + i];
+                over = wave_sum_u64(over);
+                __syncthreads();                           // (the list's room is free)
+                uint32_t kept = 0;
+#pragma unroll 2
                 for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
                     float y[VEC];
                     load(v, y);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        if (y[j] >= y_low && step_of(y[j]) == d.digit) {
+                    for (int j = 0; j < VEC; ++j) {
+                        if (!(y[j] >= y_low)) continue;
+                        const uint32_t t = step_of(y[j]);
+                        kept += t < d.digit ? 1u : 0u;
+                        if (t == d.digit) {
                             const uint64_t n = number(y[j], v + j);
                             const uint32_t at = atomicAdd(&s.count, 1u);
                             if (at < kCap) s.list[at] = n;
                             atomicMax(&s.first, (uint32_t)(n >> ibits));
                         }
+                    }
                 }
                 __syncthreads();
-                const uint32_t far = s.first;
-                take(s.count);
-                // (scores below the step lie below `far`, the search's end need not)
-                last = min(((uint64_t)far << ibits) + (((uint64_t)1 << ibits) - 1),
-                           select_last<THREADS, true>(
-                               s.hist, round,
-                               [&](auto f) {
+                const uint32_t far = s.first, count = s.count;
+                if (count <= kCap) {
+                    take(count);
+                    // (scores below the step lie below `far`, the search's end need not)
+                    last = min(((uint64_t)far << ibits) + (((uint64_t)1 << ibits) - 1),
+                               select_last<THREADS>(
+                                   s.hist, round,
+                                   [&](auto f) {
 #pragma unroll
-                                   for (int i = 0; i < E; ++i)
-                                       if (el[i] != ~0ull) f(el[i], ew[i]);
-                               },
-                               ibits + (far ? 32 - __clz((int)far) : 1), target - d.before, 0));
-                done = true;
+                                       for (int i = 0; i < E; ++i)
+                                           if (el[i] != ~0ull) f(el[i], ew[i]);
+                                   },
+                                   true, ibits + (far ? 32 - __clz((int)far) : 1), target - d.before, 0));
+                    done = true;
+                    if (!(mass.lim > 0.0)) {
+                        // the step's kept labels to their pieces; then the piece that holds the token
+                        kept = (uint32_t)wave_sum_u64(kept);
+                        if (lane == 0) { s.sum[wave] = over; s.b[wave] = kept; }
+                        if (tid == 0) s.first = 0;
+                        __syncthreads();
+#pragma unroll
+                        for (int i = 0; i < E; ++i)
+                            if (el[i] <= last) {
+                                const uint32_t v = (uint32_t)(el[i] & (((uint64_t)1 << ibits) - 1));
+                                atomicAdd(&s.sum[v / (uint32_t)seg], (unsigned long long)ew[i]);
+                                atomicAdd(&s.first, 1u);
+                            }
+                        __syncthreads();
+                        uint64_t total = 0, before = 0, goal;
+                        kept = s.first;
+                        for (int w = 0; w < WAVES; ++w) { total += s.sum[w]; kept += s.b[w]; }
+                        goal = draw_goal(row.u, total);
+                        int at = 0;
+                        while (at < WAVES - 1 && before + s.sum[at] < goal) before += s.sum[at++];
+                        const int p0 = at * seg;
+                        draw_row<XT, WAVES>(c, r, x + p0, min(seg, V - p0), p0, mass, row.u, s.row,
+                                            {goal - before, total, kept}, [&](float y, int v, uint32_t &) {
+                                                y = mass.read(y);
+                                                const bool keep = y > -INFINITY && number(y, v) <= last;
+                                                return MassOf::raw(keep ? mass(y, poly) : 0.0);
+                                            });
+                        return;
+                    }
+                }
             }
         }
         if (!done)
@@ -785,11 +863,11 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                         }
                     }
                 },
-                ibits + 32, 0, last);
+                ibits + 32, last);
     }
 
     __syncthreads();
-    draw_row<XT, WAVES>(c, r, x, mass, row.u, s.row, [&](float y, int v, uint32_t &n) {
+    draw_row<XT, WAVES>(c, r, x, V, 0, mass, row.u, s.row, {0, 0, 0}, [&](float y, int v, uint32_t &n) {
         y = mass.read(y);
         const double w = mass(y, poly);
         const bool keep = y > -INFINITY && w >= mass.lim && (last == ~0ull || number(y, v) <= last);
@@ -911,12 +989,12 @@ __global__ __launch_bounds__(kChunkThreads) void k_draw_chunk(SampleCall c, int 
             const uint32_t kmax = score_key(top);
             if ((uint32_t)(both >> 32) > share) {
                 const uint32_t far = kmax - low;
-                const uint64_t d = select_last<kChunkThreads, false>(
+                const uint64_t d = select_last<kChunkThreads>(
                     hist, round,
                     [&](auto f) {
                         if (have) f((uint64_t)(kmax - key), (uint64_t)1);
                     },
-                    far ? 32 - __clz((int)far) : 1, share, share + share / 4 + 4);
+                    false, far ? 32 - __clz((int)far) : 1, share, share + share / 4 + 4);
                 bound = max(bound, d < kmax ? kmax - (uint32_t)d : 0u);
             }
             const float floor_x = key_score(bound);
