@@ -317,6 +317,19 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
     }
 }
 
+// Among the THREADS threads that work on a list: a workgroup, or (64) one
+// wavefront of it, whose LDS operations are in order by themselves.
+template <int THREADS>
+__device__ __forceinline__ void sync_list()
+{
+    if (THREADS > 64) {
+        __syncthreads();
+    } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 struct Digit {
     uint32_t digit, count;
     uint64_t before, mine;
@@ -333,7 +346,7 @@ struct Hist {
 template <int THREADS>
 __device__ __forceinline__ void clear_hist(Hist &h, int slot)
 {
-    for (int i = threadIdx.x; i < 256; i += THREADS) { h.mass[slot][i] = 0; h.cnt[slot][i] = 0; }
+    for (int i = threadIdx.x & (THREADS - 1); i < 256; i += THREADS) { h.mass[slot][i] = 0; h.cnt[slot][i] = 0; }
 }
 
 // The digit in which the running sum over 256 bins, from `above`, reaches target:
@@ -400,12 +413,12 @@ __device__ __forceinline__ uint64_t select_last(Hist &h, uint32_t &round, Each e
                 if (by_mass) atomicAdd(&h.mass[slot][d], (unsigned long long)w);
             }
         });
-        __syncthreads();
+        sync_list<THREADS>();
         if (threadIdx.x < 64) {
             const Digit d = find_digit(h.mass[slot], h.cnt[slot], by_mass, above, target);
             if (threadIdx.x == 0) h.found = d;
         }
-        __syncthreads();
+        sync_list<THREADS>();
         ++round;
         const Digit d = h.found;
         prefix = prefix << width | (d.digit & 255u);
@@ -445,27 +458,36 @@ __device__ __forceinline__ uint64_t top_p_goal(float topp, uint64_t total)
 
 // What a workgroup of THREADS threads keeps of a row, with a list of labels that
 // may be kept, E a thread.
-template <int THREADS, int E, bool HOLD> struct DrawShared {
+template <int THREADS> struct ListShared {
     Hist hist;
-    RowSums<THREADS / 64> row;
     unsigned long long sum[THREADS / 64];
     uint32_t a[THREADS / 64], b[THREADS / 64];
+};
+
+template <int THREADS, int E, bool HOLD> struct DrawShared : ListShared<THREADS> {
+    RowSums<THREADS / 64> row;
+    ListShared<64> small;                              // of the first wavefront alone
+    uint32_t settled;
     uint32_t count, first;
     unsigned long long list[HOLD ? 1 : E * THREADS];
 };
 
 // Count and mass of the elements that each() gives, in the whole workgroup.
-template <int WAVES, typename S, typename Each>
-__device__ __forceinline__ void element_totals(S &s, Each each, uint32_t &n, uint64_t &w)
+template <int THREADS, typename Each>
+__device__ __forceinline__ void element_totals(ListShared<THREADS> &s, Each each, uint32_t &n, uint64_t &w)
 {
+    constexpr int WAVES = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint64_t tn = 0, tw = 0;
     each([&](uint64_t, uint64_t m) { ++tn; tw += m; });
     tn = wave_sum_u64(tn);
     tw = wave_sum_u64(tw);
-    __syncthreads();
+    n = (uint32_t)tn;
+    w = tw;
+    if (WAVES == 1) return;
+    sync_list<THREADS>();
     if (lane == 0) { s.sum[wave] = tw; s.b[wave] = (uint32_t)tn; }
-    __syncthreads();
+    sync_list<THREADS>();
     n = 0;
     w = 0;
 #pragma unroll
@@ -473,8 +495,8 @@ __device__ __forceinline__ void element_totals(S &s, Each each, uint32_t &n, uin
 }
 
 // Cut by top_k and top_p among the elements that each(last, f) gives.
-template <int THREADS, typename S, typename Each>
-__device__ __forceinline__ void cut_elements(S &s, uint32_t &round, const RowRules &row, Each each, int digits,
+template <int THREADS, typename Each>
+__device__ __forceinline__ void cut_elements(ListShared<THREADS> &s, uint32_t &round, const RowRules &row, Each each, int digits,
                                              uint64_t &last)
 {
     const auto now = [&](auto f) { each(last, f); };
@@ -483,7 +505,7 @@ __device__ __forceinline__ void cut_elements(S &s, uint32_t &round, const RowRul
         if (!(rule ? row.cut_p : row.cut_k)) continue;
         uint32_t n;
         uint64_t w;
-        element_totals<THREADS / 64>(s, now, n, w);
+        element_totals<THREADS>(s, now, n, w);
         if (!rule && (uint32_t)row.topk >= n) continue;
         const uint64_t target = rule ? top_p_goal(row.topp, w) : (uint64_t)row.topk;
         // (the search may end above what top_k left: at the end of a digit that held one label)
@@ -497,10 +519,11 @@ __device__ __forceinline__ void cut_elements(S &s, uint32_t &round, const RowRul
 // falls short of it. The three searches (top_k, top_p, the draw by index) share
 // one piece of code: a row's time here is latency, and code that runs once is
 // fetched as it runs.
-template <int THREADS, int E, typename S>
+template <int THREADS, int E>
 __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const RowRules &row, const MassOf &mass,
                                           const Exp2Poly &poly, uint32_t kmax, int ibits, uint64_t (&el)[E],
-                                          const uint64_t (&ew)[E], int digits, uint64_t total_p, S &s, uint32_t &round)
+                                          const uint64_t (&ew)[E], int digits, uint64_t total_p, ListShared<THREADS> &s,
+                                          uint32_t &round)
 {
     constexpr int WAVES = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -525,7 +548,7 @@ __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const 
             mask = imask;
             digits = max(ibits, 1);
         }
-        element_totals<WAVES>(
+        element_totals<THREADS>(
             s,
             [&](auto f) {
 #pragma unroll
@@ -575,12 +598,47 @@ __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const 
     return true;
 }
 
+// draw_list on the first n labels of s.list, by the first wavefront where it can
+// hold them: alone it needs no barriers, and does not share its SIMD's issue slots
+// with three others that do the same. For the whole workgroup; n <= E * THREADS.
+template <int THREADS, int E>
+__device__ __forceinline__ bool draw_listed(const SampleCall &c, int64_t r, const RowRules &row, const MassOf &mass,
+                                            const Exp2Poly &poly, uint32_t kmax, int ibits, uint32_t n, int digits,
+                                            uint64_t total_p, DrawShared<THREADS, E, false> &s, uint32_t &round,
+                                            uint32_t &round_small)
+{
+    constexpr int kSmall = THREADS > 256 ? 4 : 8;     // (1024 threads: 128 registers each)
+    const auto take = [&](int at, uint64_t &num, uint64_t &w) {
+        const uint64_t v = s.list[at];                 // (past the count: whatever the list held)
+        const uint64_t m = MassOf::fixed(mass(key_score(kmax - (uint32_t)(v >> ibits)), poly));
+        num = (uint32_t)at < n ? v : ~0ull;
+        w = (uint32_t)at < n ? m : 0;
+    };
+    if (n <= kSmall * 64) {
+        if (threadIdx.x < 64) {
+            uint64_t el[kSmall], ew[kSmall];
+#pragma unroll
+            for (int i = 0; i < kSmall; ++i) take(i * 64 + threadIdx.x, el[i], ew[i]);
+            const bool ok = draw_list<64, kSmall>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, total_p, s.small,
+                                                  round_small);
+            if (threadIdx.x == 0) s.settled = ok;
+        }
+        __syncthreads();
+        return s.settled;
+    }
+    uint64_t el[E], ew[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) take(i * THREADS + threadIdx.x, el[i], ew[i]);
+    return draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, total_p, s, round);
+}
+
 // One row by one workgroup. HOLD: the row in registers, E scores a thread (rows
 // of at most E * THREADS labels), all of them elements. Otherwise a short list of
 // labels that are sure to hold the kept ones is tried first.
 template <typename XT, int THREADS, int E, bool HOLD>
 __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const RowRules &row, const Exp2Poly &poly,
-                                         int unit, int ibits, DrawShared<THREADS, E, HOLD> &s, uint32_t &round)
+                                         int unit, int ibits, DrawShared<THREADS, E, HOLD> &s, uint32_t &round,
+                                         uint32_t &round_small)
 {
     constexpr int WAVES = THREADS / 64;
     constexpr int VEC = 16 / sizeof(XT);
@@ -718,19 +776,24 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
             __syncthreads();
             const uint32_t count = s.count;
             if (count <= kCap) {
-                take(count);
-                __syncthreads();
                 const int digits = ibits + (bound ? 32 - __clz((int)bound) : 1);
-                draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, 0, s, round);
+                if constexpr (!HOLD)
+                    draw_listed<THREADS, E>(c, r, row, mass, poly, kmax, ibits, count, digits, 0, s, round, round_small);
                 return;
             }
             __syncthreads();
         } else if (!row.cut_k) {
             // top_p alone. In one pass the mass of all labels and, by 256 equal steps of the score and each
             // wavefront's piece, of those that may be kept: the others weigh less than 1 - top_p even all together
-            // (and even if the largest score were the only other mass). The steps say in which the nucleus ends;
+            // (all labels weighing no less than the threads' largest ones). The steps say in which the nucleus ends;
             // a list of that step's labels, exactly where; the pieces' masses, in which piece the token lies.
-            const double least = (1.0 - (double)row.topp) / (double)V;
+            uint64_t some = own > -INFINITY ? MassOf::fixed(mass(own, poly)) : 0;
+            some = wave_sum_u64(some);
+            if (lane == 0) s.sum[wave] = some;
+            __syncthreads();
+            some = 0;
+            for (int w = 0; w < WAVES; ++w) some += s.sum[w];
+            const double least = (1.0 - (double)row.topp) * ((double)some / mass.one) / (double)V;
             double low = mass.m + mass.t * log(least);
             low -= 1e-6 * (fabs(low) + fabs(mass.m));
             const float y_low = low > -3.4028234663852886e38 ? (float)low : -3.4028234663852886e38f;
@@ -877,17 +940,18 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
 }
 
 template <typename XT, int THREADS, int E, bool HOLD>
-__global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ibits)
+__global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ibits, const uint32_t *open)
 {
     __shared__ DrawShared<THREADS, E, HOLD> s;
     const Exp2Poly poly;
-    uint32_t round = 0;
+    uint32_t round = 0, round_small = 0;
     clear_hist<THREADS>(s.hist, 0);
+    clear_hist<THREADS>(s.small.hist, 0);
     for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
-        if (!row_active(c.set, r)) continue;
+        if (!row_active(c.set, r) || (open && !open[r])) continue;
         __syncthreads();
         const RowRules row(c, r);
-        draw_one<XT, THREADS, E, HOLD>(c, r, row, poly, unit, ibits, s, round);
+        draw_one<XT, THREADS, E, HOLD>(c, r, row, poly, unit, ibits, s, round, round_small);
     }
 }
 
@@ -896,12 +960,14 @@ __global__ __launch_bounds__(THREADS) void k_draw(SampleCall c, int unit, int ib
 // largest score, its mass relative to that (where a row needs its whole mass),
 // its number of labels above -inf, and a list of its labels above a bound of its
 // own. A second launch joins a row's chunks: labels at or above the largest of the
-// chunks' bounds are in the lists for certain, and draw_list works on those; where
-// they do not settle the row, draw_one takes it from its scores.
+// chunks' bounds are in the lists for certain, and draw_list works on those. Rows
+// that they do not settle are left to a third launch, which takes them from their
+// scores (in the second its code and registers would slow every row).
 constexpr int kChunkThreads = 256;
 constexpr int kChunkPacks = 2;
 constexpr int kChunkList = 256;                        // entries of a chunk's list
-constexpr int kMaxChunks = 1024;                       // of a row: one a thread of the join
+constexpr int kJoinThreads = 256;
+constexpr int kMaxChunks = kJoinThreads;               // of a row: one a thread of the join
 
 struct ChunkStat {
     unsigned long long mass;                           // relative to `top`
@@ -982,10 +1048,10 @@ __global__ __launch_bounds__(kChunkThreads) void k_draw_chunk(SampleCall c, int 
         mass_sum = wave_sum_u64(mass_sum);
         uint32_t bound = kKeyNegInf + 1u;                  // all labels above -inf
         if (row_needs_list(row) && top > -INFINITY) {
-            // enough labels of every chunk that all rows' lists together hold about 2048, or eight times top_k
+            // enough labels of every chunk that all rows' lists together hold about 1536, or eight times top_k
             const uint32_t share = row.greedy ? 1u
                                    : row.cut_k ? (uint32_t)min((int64_t)192, 8 + 8 * (int64_t)row.topk / chunks)
-                                               : (uint32_t)min(192, max(8, 2048 / chunks));
+                                               : (uint32_t)min(192, max(8, 1536 / chunks));
             const uint32_t kmax = score_key(top);
             if ((uint32_t)(both >> 32) > share) {
                 const uint32_t far = kmax - low;
@@ -1041,10 +1107,11 @@ __device__ __forceinline__ uint64_t block_before(uint64_t v, unsigned long long 
 }
 
 template <typename XT>
-__global__ __launch_bounds__(1024) void k_draw_join(SampleCall c, int unit, int ibits, int chunks, const ChunkStat *stats,
-                                                    const unsigned long long *lists)
+__global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int unit, int ibits, int chunks,
+                                                           const ChunkStat *stats, const unsigned long long *lists,
+                                                           uint32_t *open)
 {
-    constexpr int THREADS = 1024, WAVES = 16, E = 4;
+    constexpr int THREADS = kJoinThreads, WAVES = THREADS / 64, E = 8;
     constexpr int VEC = 16 / sizeof(XT);
     constexpr int kChunk = kChunkThreads * VEC * kChunkPacks;
     constexpr int kEach = kChunk / THREADS;
@@ -1052,13 +1119,15 @@ __global__ __launch_bounds__(1024) void k_draw_join(SampleCall c, int unit, int 
     __shared__ uint16_t n_listed[kMaxChunks];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Exp2Poly poly;
-    uint32_t round = 0;
+    uint32_t round = 0, round_small = 0;
     clear_hist<THREADS>(s.hist, 0);
+    clear_hist<THREADS>(s.small.hist, 0);
     for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
         if (!row_active(c.set, r)) continue;
         __syncthreads();
         const RowRules row(c, r);
         const XT *x = (const XT *)c.x + r * c.x_stride;
+        if (tid == 0) open[r] = 0;
         const bool mine = tid < chunks;
         ChunkStat st = {0, -INFINITY, kKeyNegInf + 1u, 0, 0};
         if (mine) st = stats[r * chunks + tid];
@@ -1135,41 +1204,37 @@ __global__ __launch_bounds__(1024) void k_draw_join(SampleCall c, int unit, int 
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) most = max(most, s.b[i]);
             const int places = most > 1 ? 32 - __clz((int)most - 1) : 0;
-#pragma unroll 4
-            for (int i = tid; i < chunks << places; i += THREADS) {
-                const int q = i >> places;
-                const uint32_t at_q = i & ((1u << places) - 1u);
-                if (at_q < n_listed[q]) {
-                    const uint64_t e = lists[(r * chunks + q) * kChunkList + at_q];
-                    const float y = mass.read(key_score((uint32_t)(e >> 32)));
-                    if ((uint32_t)(e >> 32) >= bound && y > -INFINITY) {
+            const unsigned long long *list = lists + r * chunks * kChunkList;
+            constexpr int kAhead = 4;                          // loads in flight (those past a list's end are dropped)
+            for (int i0 = tid; i0 < chunks << places; i0 += kAhead * THREADS) {
+                uint64_t e[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int i = min(i0 + k * THREADS, (chunks << places) - 1);
+                    e[k] = list[(size_t)(i >> places) * kChunkList + (i & ((1 << places) - 1))];
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int i = i0 + k * THREADS;
+                    if (i >= chunks << places || (uint32_t)(i & ((1 << places) - 1)) >= n_listed[i >> places]) continue;
+                    const float y = mass.read(key_score((uint32_t)(e[k] >> 32)));
+                    if ((uint32_t)(e[k] >> 32) >= bound && y > -INFINITY) {
                         const uint32_t at = atomicAdd(&s.count, 1u);
-                        if (at < E * THREADS) s.list[at] = (uint64_t)(kmax - score_key(y)) << ibits | (uint32_t)e;
+                        if (at < E * THREADS) s.list[at] = (uint64_t)(kmax - score_key(y)) << ibits | (uint32_t)e[k];
                     }
                 }
             }
             __syncthreads();
             const uint32_t n = s.count;
             if (n <= E * THREADS && (all || row.greedy || !row.cut_k || n >= (uint32_t)row.topk)) {
-                uint64_t el[E], ew[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const uint32_t at = i * THREADS + tid;
-                    const uint64_t e = s.list[at];
-                    const uint64_t w = MassOf::fixed(mass(key_score(kmax - (uint32_t)(e >> ibits)), poly));
-                    el[i] = at < n ? e : ~0ull;
-                    ew[i] = at < n ? w : 0;
-                }
-                __syncthreads();
                 const uint32_t far = mass.pick ? 0u : kmax - bound;
                 const int digits = ibits + (far ? 32 - __clz((int)far) : 1);
-                if (draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits,
-                                          all || row.cut_k ? 0 : z, s, round))
+                if (draw_listed<THREADS, E>(c, r, row, mass, poly, kmax, ibits, n, digits, all || row.cut_k ? 0 : z, s,
+                                            round, round_small))
                     continue;
             }
         }
-        __syncthreads();
-        draw_one<XT, THREADS, E, false>(c, r, row, poly, unit, ibits, s, round);
+        if (tid == 0) open[r] = 1;
     }
 }
 
@@ -1200,13 +1265,15 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
     if (chunks) {
         ChunkStat *stats = (ChunkStat *)c.workspace;
         unsigned long long *lists = (unsigned long long *)(stats + c.rows * chunks);
+        uint32_t *open = (uint32_t *)(lists + c.rows * chunks * kChunkList);
         const dim3 gc((unsigned)std::min<int64_t>(c.rows * chunks, kMaxRowGrid));
         hipLaunchKernelGGL(k_draw_chunk<XT>, gc, dim3(kChunkThreads), 0, s, c, unit, chunks, stats, lists);
-        hipLaunchKernelGGL(k_draw_join<XT>, g, dim3(1024), 0, s, c, unit, ibits, chunks, stats, lists);
+        hipLaunchKernelGGL(k_draw_join<XT>, g, dim3(kJoinThreads), 0, s, c, unit, ibits, chunks, stats, lists, open);
+        hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits, (const uint32_t *)open);
     } else if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps) draw_all<XT>(c, unit, s);
-    else if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits);
-    else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits);
-    else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits);
+    else if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
+    else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
+    else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
     return hipGetLastError();
 }
 
@@ -1223,7 +1290,9 @@ int sample_chunks(int64_t rows, int32_t V, int32_t x_dtype)
 
 size_t sample_workspace(int64_t rows, int32_t V, int32_t x_dtype)
 {
-    return (size_t)rows * sample_chunks(rows, V, x_dtype) * (sizeof(ChunkStat) + kChunkList * 8);
+    const int chunks = sample_chunks(rows, V, x_dtype);
+    if (!chunks) return 0;
+    return (size_t)rows * chunks * (sizeof(ChunkStat) + kChunkList * 8) + (size_t)rows * 4;
 }
 
 hipError_t launch_sample(const SampleCall &c, hipStream_t s)
