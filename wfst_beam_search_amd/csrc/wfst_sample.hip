@@ -77,6 +77,13 @@ struct MassOf {
         a = 1.4426950408889634 / t;
         lim = minp > 0.0f ? (minp < 1.0f ? (double)minp : 1.0) * one : 0.0;
     }
+    // A score below which no label passes min_p (a little low, for the roundings on the way).
+    __device__ __forceinline__ float least_score() const
+    {
+        if (!(lim > 0.0)) return -INFINITY;
+        const double y = m + t * log(lim / one);
+        return (float)(y - 1e-6 * (fabs(y) + fabs(m)));
+    }
     __device__ __forceinline__ float read(float x) const { return pick ? (x == top ? 0.0f : -INFINITY) : x; }
     // 2^(t + unit), t = (x - m) a <= 0 (below -1000: as -1000): adding `base`
     // rounds t to an integer, leaves unit + that integer in the low bits and f in
@@ -298,10 +305,13 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
         const bool greedy = !(T > 0.0f);
         const MassOf mass(top, T, greedy ? 0.0f : minp, unit, greedy);
         // Two forms: the tests of the general one, as selects, take half as long again as the sum itself.
-        // Without them -inf and NaN have the mass 2^-1000, which rounds to 0.
+        // Without them -inf and NaN have the mass 2^-1000, which rounds to 0. With min_p most labels fail a test
+        // of their score and need no mass.
         if (__builtin_amdgcn_readfirstlane(mass.pick || mass.lim > 0.0)) {
+            const float least = mass.least_score();
             draw_row<XT, WAVES>(c, r, x, c.V, 0, mass, u, s, {0, 0, 0}, [&](float y, int, uint32_t &n) {
                 y = mass.read(y);
+                if (!(y >= least)) return MassOf::kRaw;
                 const double w = mass(y, poly);
                 const bool keep = y > -INFINITY && w >= mass.lim;
                 n += keep ? 1u : 0u;
@@ -514,7 +524,7 @@ __device__ __forceinline__ void cut_elements(ListShared<THREADS> &s, uint32_t &r
 }
 
 // Cut a list of elements (number, mass; ~0: none) that holds all labels which may
-// be kept, and draw from it. total_p: the mass top_p is a share of where that is
+// be kept, n of them, and draw from it. total_p: the mass top_p is a share of where that is
 // not the elements' own (0 otherwise); false, and nothing written, if their mass
 // falls short of it. The three searches (top_k, top_p, the draw by index) share
 // one piece of code: a row's time here is latency, and code that runs once is
@@ -522,14 +532,13 @@ __device__ __forceinline__ void cut_elements(ListShared<THREADS> &s, uint32_t &r
 template <int THREADS, int E>
 __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const RowRules &row, const MassOf &mass,
                                           const Exp2Poly &poly, uint32_t kmax, int ibits, uint64_t (&el)[E],
-                                          const uint64_t (&ew)[E], int digits, uint64_t total_p, ListShared<THREADS> &s,
+                                          const uint64_t (&ew)[E], uint32_t n, int digits, uint64_t total_p, ListShared<THREADS> &s,
                                           uint32_t &round)
 {
     constexpr int WAVES = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t imask = ((uint64_t)1 << ibits) - 1;
     uint64_t last = ~0ull - 1, mask = ~0ull, total = 0;
-    uint32_t n = 0;
 #pragma unroll 1
     for (int rule = 0; rule < 3; ++rule) {
         if (rule == 0 ? !row.cut_k : rule == 1 ? !row.cut_p : false) continue;
@@ -548,14 +557,15 @@ __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const 
             mask = imask;
             digits = max(ibits, 1);
         }
-        element_totals<THREADS>(
-            s,
-            [&](auto f) {
+        if (rule > 0)
+            element_totals<THREADS>(
+                s,
+                [&](auto f) {
 #pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (el[i] <= last) f(el[i], ew[i]);
-            },
-            n, total);
+                    for (int i = 0; i < E; ++i)
+                        if (el[i] <= last) f(el[i], ew[i]);
+                },
+                n, total);
         if (rule == 0 && (uint32_t)row.topk >= n) continue;
         uint64_t target = (uint64_t)row.topk;
         if (rule == 1) {
@@ -607,7 +617,7 @@ __device__ __forceinline__ bool draw_listed(const SampleCall &c, int64_t r, cons
                                             uint64_t total_p, DrawShared<THREADS, E, false> &s, uint32_t &round,
                                             uint32_t &round_small)
 {
-    constexpr int kSmall = THREADS > 256 ? 4 : 8;     // (1024 threads: 128 registers each)
+    constexpr int kSmall = 4;
     const auto take = [&](int at, uint64_t &num, uint64_t &w) {
         const uint64_t v = s.list[at];                 // (past the count: whatever the list held)
         const uint64_t m = MassOf::fixed(mass(key_score(kmax - (uint32_t)(v >> ibits)), poly));
@@ -619,7 +629,7 @@ __device__ __forceinline__ bool draw_listed(const SampleCall &c, int64_t r, cons
             uint64_t el[kSmall], ew[kSmall];
 #pragma unroll
             for (int i = 0; i < kSmall; ++i) take(i * 64 + threadIdx.x, el[i], ew[i]);
-            const bool ok = draw_list<64, kSmall>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, total_p, s.small,
+            const bool ok = draw_list<64, kSmall>(c, r, row, mass, poly, kmax, ibits, el, ew, n, digits, total_p, s.small,
                                                   round_small);
             if (threadIdx.x == 0) s.settled = ok;
         }
@@ -629,7 +639,7 @@ __device__ __forceinline__ bool draw_listed(const SampleCall &c, int64_t r, cons
     uint64_t el[E], ew[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) take(i * THREADS + threadIdx.x, el[i], ew[i]);
-    return draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, digits, total_p, s, round);
+    return draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, n, digits, total_p, s, round);
 }
 
 // One row by one workgroup. HOLD: the row in registers, E scores a thread (rows
@@ -716,7 +726,11 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                     ew[i * VEC + j] = MassOf::fixed(mass(y[j], poly));      // (0 for -inf and NaN)
                 }
             }
-            draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, ibits + 32, 0, s, round);
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) n += el[i] != ~0ull ? 1u : 0u;
+            n = (uint32_t)wave_sum_u64(n);             // (a held row has one wavefront)
+            draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, n, ibits + 32, 0, s, round);
             return;
         }
         // the list's labels become the threads' elements
@@ -900,11 +914,12 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                         int at = 0;
                         while (at < WAVES - 1 && before + s.sum[at] < goal) before += s.sum[at++];
                         const int p0 = at * seg;
+                        const float least = key_score(kmax - (uint32_t)(last >> ibits));
                         draw_row<XT, WAVES>(c, r, x + p0, min(seg, V - p0), p0, mass, row.u, s.row,
                                             {goal - before, total, kept}, [&](float y, int v, uint32_t &) {
                                                 y = mass.read(y);
-                                                const bool keep = y > -INFINITY && number(y, v) <= last;
-                                                return MassOf::raw(keep ? mass(y, poly) : 0.0);
+                                                if (!(y >= least)) return MassOf::kRaw;
+                                                return MassOf::raw(number(y, v) <= last ? mass(y, poly) : 0.0);
                                             });
                         return;
                     }
@@ -930,8 +945,11 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
     }
 
     __syncthreads();
+    const float cut_score = last == ~0ull ? -INFINITY : key_score(kmax - (uint32_t)(last >> ibits));
+    const float least = fmaxf(cut_score, mass.least_score());
     draw_row<XT, WAVES>(c, r, x, V, 0, mass, row.u, s.row, {0, 0, 0}, [&](float y, int v, uint32_t &n) {
         y = mass.read(y);
+        if (!(y >= least)) return MassOf::kRaw;
         const double w = mass(y, poly);
         const bool keep = y > -INFINITY && w >= mass.lim && (last == ~0ull || number(y, v) <= last);
         n += keep ? 1u : 0u;
@@ -1048,9 +1066,10 @@ __global__ __launch_bounds__(kChunkThreads) void k_draw_chunk(SampleCall c, int 
         mass_sum = wave_sum_u64(mass_sum);
         uint32_t bound = kKeyNegInf + 1u;                  // all labels above -inf
         if (row_needs_list(row) && top > -INFINITY) {
-            // enough labels of every chunk that all rows' lists together hold about 1536, or eight times top_k
+            // enough labels of every chunk that a row's lists together hold about 1536; for top_k twice a chunk's
+            // share of it and 8, which the largest bound then rarely lies above (once in 10^4 rows in random order)
             const uint32_t share = row.greedy ? 1u
-                                   : row.cut_k ? (uint32_t)min((int64_t)192, 8 + 8 * (int64_t)row.topk / chunks)
+                                   : row.cut_k ? (uint32_t)min((int64_t)192, 8 + 2 * (int64_t)row.topk / chunks)
                                                : (uint32_t)min(192, max(8, 1536 / chunks));
             const uint32_t kmax = score_key(top);
             if ((uint32_t)(both >> 32) > share) {
@@ -1206,8 +1225,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int un
             const int places = most > 1 ? 32 - __clz((int)most - 1) : 0;
             const unsigned long long *list = lists + r * chunks * kChunkList;
             constexpr int kAhead = 4;                          // loads in flight (those past a list's end are dropped)
-            for (int i0 = tid; i0 < chunks << places; i0 += kAhead * THREADS) {
-                uint64_t e[kAhead];
+            for (int i0 = tid; i0 - tid < chunks << places; i0 += kAhead * THREADS) {
+                uint64_t e[kAhead], hit[kAhead];
+                uint32_t hits = 0;
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
                     const int i = min(i0 + k * THREADS, (chunks << places) - 1);
@@ -1215,13 +1235,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int un
                 }
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    const int i = i0 + k * THREADS;
-                    if (i >= chunks << places || (uint32_t)(i & ((1 << places) - 1)) >= n_listed[i >> places]) continue;
+                    const int i = min(i0 + k * THREADS, (chunks << places) - 1);
                     const float y = mass.read(key_score((uint32_t)(e[k] >> 32)));
-                    if ((uint32_t)(e[k] >> 32) >= bound && y > -INFINITY) {
-                        const uint32_t at = atomicAdd(&s.count, 1u);
-                        if (at < E * THREADS) s.list[at] = (uint64_t)(kmax - score_key(y)) << ibits | (uint32_t)e[k];
-                    }
+                    const bool take = i == i0 + k * THREADS && (uint32_t)(i & ((1 << places) - 1)) < n_listed[i >> places] &&
+                                      (uint32_t)(e[k] >> 32) >= bound && y > -INFINITY;
+                    e[k] = (uint64_t)(kmax - score_key(y)) << ibits | (uint32_t)e[k];
+                    hit[k] = __ballot(take);
+                    hits += __popcll(hit[k]);
+                }
+                uint32_t at = 0;
+                if (lane == 0 && hits) at = atomicAdd(&s.count, hits);
+                at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const uint32_t p = at + __popcll(hit[k] & ((1ull << lane) - 1ull));
+                    if ((hit[k] >> lane & 1ull) && p < E * THREADS) s.list[p] = e[k];
+                    at += __popcll(hit[k]);
                 }
             }
             __syncthreads();
