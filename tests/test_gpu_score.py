@@ -378,7 +378,7 @@ SETTINGS = [dict(), dict(temperature=0.0), dict(temperature=0.7, top_k=1), dict(
             dict(top_k=50, min_p=0.01), dict(temperature=0.8, top_k=700, top_p=0.97, min_p=0.01), dict(top_p=0.9, min_p=1e-4), dict(temperature=3.0, top_k=100000, top_p=0.999)]
 
 
-@pytest.mark.parametrize("V", [1, 2, 5, 64, 65, 257, 500, 1025, 5000, 32003])
+@pytest.mark.parametrize("V", [1, 2, 5, 64, 65, 257, 500, 1025, 5000, 32003, 70003])
 @pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
 def test_sample(V, x):
     g = torch.Generator(device="cuda").manual_seed(V)
@@ -391,7 +391,7 @@ def test_sample(V, x):
             _sample_check(wb.sample(t, u, **s), t, u, **s)
 
 
-@pytest.mark.parametrize("V,R", [(40, 64), (3000, 64), (20011, 64), (20011, 150)])
+@pytest.mark.parametrize("V,R", [(40, 64), (3000, 64), (20011, 64), (70011, 20)])
 def test_sample_settings_per_row(V, R):
     g = torch.Generator(device="cuda").manual_seed(V + 1)
     t = torch.randn(R, V, generator=g, device="cuda") * 3
@@ -419,7 +419,7 @@ def test_sample_ties_go_to_the_lowest_index():
         _sample_check(wb.sample(q, u, **s), q, u, **s)
 
 
-@pytest.mark.parametrize("V", [9, 700, 5001, 9001])
+@pytest.mark.parametrize("V", [9, 700, 5001, 9001, 66001])
 def test_sample_masks_and_specials(V):
     inf = float("inf")
     t = torch.randn(10, V)
@@ -471,7 +471,7 @@ def test_sample_strides_lengths_and_untouched_rows():
 def test_sample_orders_that_mislead_the_lists(R, x):
     """Scores in falling order, in rising order, all equal, all masked but a few,
     and a nucleus of most labels: the short lists do not hold the kept labels."""
-    V = 30011
+    V = 30011 if R > 32 else 66011
     t = torch.empty(5, V)
     t[0] = -torch.arange(V) * 1e-3
     t[1] = torch.arange(V) * 1e-3
@@ -487,7 +487,7 @@ def test_sample_orders_that_mislead_the_lists(R, x):
         _sample_check(wb.sample(t, u, **s), t, u, **s)
 
 
-@pytest.mark.parametrize("R", [2, 130])
+@pytest.mark.parametrize("R", [2, 40])
 def test_sample_language_model_rows(R):
     """A power law over a shuffled vocabulary, odd and large."""
     V = 70001

@@ -1,4 +1,6 @@
 // gfx950 (CDNA4) kernels of the draw of tokens from scores.
+#include <type_traits>
+
 #include "wfst_score_device.h"
 
 namespace wfst {
@@ -166,6 +168,36 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane)
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) { return lane_u64(wave_scan_u64(v), 63); }
 
+// f(v, scores v .. v + VEC - 1) for the lane's packs of labels v0 .. v1 - 1 of a row
+// of V, a wavefront taking 64 * VEC labels at once: AHEAD packs are loaded before
+// the first is used. v0 is the wavefront's; packs may reach past v1 (to V).
+template <typename XT, int AHEAD, typename F>
+__device__ __forceinline__ void each_pack(const XT *x, int V, int v0, int v1, F f)
+{
+    constexpr int VEC = 16 / sizeof(XT);
+    constexpr int kStepW = 64 * VEC;
+    const int lane = threadIdx.x & 63;
+    int v = v0;
+    for (; v + AHEAD * kStepW <= v1; v += AHEAD * kStepW) {
+        Pack<XT, VEC> p[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) p[i] = *(const Pack<XT, VEC> *)(x + v + i * kStepW + lane * VEC);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            float y[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[j] = (float)p[i].v[j];
+            f(v + i * kStepW + lane * VEC, y);
+        }
+    }
+    for (; v < v1; v += kStepW) {
+        if (v + lane * VEC >= v1) continue;
+        float y[VEC];
+        load_scores<XT, VEC>(x, V, v + lane * VEC, y);
+        f(v + lane * VEC, y);
+    }
+}
+
 // LDS of draw_row.
 template <int WAVES> struct RowSums {
     unsigned long long sum[WAVES];
@@ -288,13 +320,12 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
         const float minp = c.min_ps ? c.min_ps[r] : c.min_p;
         const float u = c.u[r];
         float top = -INFINITY;
-#pragma unroll 4
-        for (int v = (wave * 64 + lane) * VEC; v < c.V; v += WAVES * kPackW) {
-            float y[VEC];
-            load_scores<XT, VEC>(x, c.V, v, y);
+        const int packs = (c.V + WAVES * kPackW - 1) / (WAVES * kPackW);
+        const int p0 = min(c.V, wave * packs * kPackW);
+        each_pack<XT, 4>(x, c.V, p0, min(c.V, p0 + packs * kPackW), [&](int, const float (&y)[VEC]) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) top = fmaxf(top, y[j]);        // (NaN leaves it)
-        }
+        });
         top = wave_max_f(top);
         if (WAVES > 1) {
             if (lane == 0) red[wave] = top;
@@ -308,7 +339,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
         // Without them -inf and NaN have the mass 2^-1000, which rounds to 0. With min_p most labels fail a test
         // of their score and need no mass.
         if (__builtin_amdgcn_readfirstlane(mass.pick || mass.lim > 0.0)) {
-            const float least = mass.least_score();
+            const float least = mass.pick ? 0.0f : mass.least_score();
             draw_row<XT, WAVES>(c, r, x, c.V, 0, mass, u, s, {0, 0, 0}, [&](float y, int, uint32_t &n) {
                 y = mass.read(y);
                 if (!(y >= least)) return MassOf::kRaw;
@@ -663,13 +694,10 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
 
     // the row's largest score, and each thread's own
     float own = -INFINITY;
-#pragma unroll 4
-    for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-        float y[VEC];
-        load_scores<XT, VEC>(x, V, v, y);
+    each_pack<XT, 8>(x, V, v0, v1, [&](int, const float (&y)[VEC]) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) own = fmaxf(own, y[j]);       // (NaN leaves it)
-    }
+    });
     float top = wave_max_f(own);
     __syncthreads();
     if (lane == 0) s.a[wave] = __float_as_uint(top);
@@ -683,16 +711,16 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
     }
     if (row.greedy) {
         // the first label with the largest score
-        for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-            float y[VEC];
-            load_scores<XT, VEC>(x, V, v, y);
-            uint32_t at = 0xFFFFFFFFu;
+        uint32_t at = 0xFFFFFFFFu;
+        if (own == top)                                            // (one thread, as a rule)
+            for (int v = v0 + lane * VEC; v < v1 && at == 0xFFFFFFFFu; v += kStepW) {
+                float y[VEC];
+                load_scores<XT, VEC>(x, V, v, y);
 #pragma unroll
-            for (int j = VEC - 1; j >= 0; --j)
-                if (y[j] == top) at = v + j;
-            if (at != 0xFFFFFFFFu) atomicMin(&s.first, at);
-            if (__ballot(at != 0xFFFFFFFFu)) break;
-        }
+                for (int j = VEC - 1; j >= 0; --j)
+                    if (y[j] == top) at = v + j;
+            }
+        if (at != 0xFFFFFFFFu) atomicMin(&s.first, at);
         __syncthreads();
         if (tid == 0) emit(c, r, (int)s.first, 0.0f, 1);
         return;
@@ -709,6 +737,17 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
             for (int j = 0; j < VEC; ++j) y[j] = mass.read(y[j]);
         }
     };
+    const auto each = [&](auto ahead, auto f) {
+        each_pack<XT, decltype(ahead)::value>(x, V, v0, v1, [&](int v, float (&y)[VEC]) {
+            if (mass.pick) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[j] = mass.read(y[j]);
+            }
+            f(v, y);
+        });
+    };
+    using Ahead2 = std::integral_constant<int, 2>;
+    using Ahead4 = std::integral_constant<int, 4>;
     const auto number = [&](float y, uint32_t i) { return (uint64_t)(kmax - score_key(y)) << ibits | i; };
     uint64_t last = ~0ull;                             // kept: number <= last
 
@@ -770,10 +809,7 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                 bound = (uint32_t)min(b, (uint64_t)bound);
             }
             const float floor_x = key_score(kmax - bound);
-#pragma unroll 2
-            for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-                float y[VEC];
-                load(v, y);
+            each(Ahead4{}, [&](int v, const float (&y)[VEC]) {
                 uint32_t hits = 0;
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) hits |= (y[j] >= floor_x ? 1u : 0u) << j;
@@ -786,7 +822,7 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                             ++at;
                         }
                 }
-            }
+            });
             __syncthreads();
             const uint32_t count = s.count;
             if (count <= kCap) {
@@ -820,9 +856,7 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
             for (int i = tid; i < WAVES * 256; i += THREADS) piece[i] = 0;
             __syncthreads();
             uint64_t z = 0;
-            for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-                float y[VEC];
-                load(v, y);
+            each(Ahead2{}, [&](int, const float (&y)[VEC]) {
                 z -= VEC * MassOf::kRaw;
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -831,7 +865,7 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                     z += w;
                     if (y[j] >= y_low) atomicAdd(&piece[wave * 256 + step_of(y[j])], (unsigned long long)(w - MassOf::kRaw));
                 }
-            }
+            });
             z = wave_sum_u64(z);
             if (lane == 0) s.sum[wave] = z;
             if (tid == 0) { s.count = 0; s.first = 0; }
@@ -861,10 +895,7 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                 over = wave_sum_u64(over);
                 __syncthreads();                           // (the list's room is free)
                 uint32_t kept = 0;
-#pragma unroll 2
-                for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-                    float y[VEC];
-                    load(v, y);
+                each(Ahead4{}, [&](int v, const float (&y)[VEC]) {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
                         if (!(y[j] >= y_low)) continue;
@@ -877,7 +908,7 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                             atomicMax(&s.first, (uint32_t)(n >> ibits));
                         }
                     }
-                }
+                });
                 __syncthreads();
                 const uint32_t far = s.first, count = s.count;
                 if (count <= kCap) {
@@ -930,16 +961,14 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
             cut_elements<THREADS>(
                 s, round, row,
                 [&](uint64_t upto, auto f) {
-                    for (int v = v0 + lane * VEC; v < v1; v += kStepW) {
-                        float y[VEC];
-                        load(v, y);
+                    each(Ahead2{}, [&](int v, const float (&y)[VEC]) {
 #pragma unroll
                         for (int j = 0; j < VEC; ++j) {
                             if (!(y[j] > -INFINITY)) continue;
                             const uint64_t n = number(y[j], v + j);
                             if (n <= upto) f(n, MassOf::fixed(mass(y[j], poly)));
                         }
-                    }
+                    });
                 },
                 ibits + 32, last);
     }
@@ -1308,13 +1337,16 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
 
 }  // namespace
 
-// Chunks a row is cut into, 0 for rows that stay whole.
+// Chunks a row is cut into, 0 for rows that stay whole. Three launches pay for
+// long rows only, and for few of them: 131072 bfloat16 labels, whole / in chunks,
+// one row 34 / 19 us without cuts, 24 / 21 with top_k 50, 60 / 28 with top_p 0.9 (67 /
+// 85 where the nucleus outgrows the lists); 32 rows 34 / 20, 24 / 24, 61 / 36; 64 rows
+// 35 / 25, 24 / 30, 60 / 44; 32003 binary32 labels, one row 14 / 19, 18 / 19, 29 / 26.
 int sample_chunks(int64_t rows, int32_t V, int32_t x_dtype)
 {
     const int chunk = kChunkThreads * kChunkPacks * (16 / (int)dtype_size(x_dtype));
     const int chunks = (V + chunk - 1) / chunk;
-    const char *e = getenv("SPLIT_ROWS");
-    return rows <= (e ? atoi(e) : 128) && V > 8192 && chunks <= kMaxChunks ? chunks : 0;
+    return rows <= 32 && V > 65536 && chunks <= kMaxChunks ? chunks : 0;
 }
 
 size_t sample_workspace(int64_t rows, int32_t V, int32_t x_dtype)
