@@ -765,11 +765,17 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
                     ew[i * VEC + j] = MassOf::fixed(mass(y[j], poly));      // (0 for -inf and NaN)
                 }
             }
-            uint32_t n = 0;
+            uint32_t n = 0, far = 0;                   // labels; the lowest one's distance from the top
 #pragma unroll
-            for (int i = 0; i < E; ++i) n += el[i] != ~0ull ? 1u : 0u;
+            for (int i = 0; i < E; ++i) {
+                n += el[i] != ~0ull ? 1u : 0u;
+                far = max(far, el[i] != ~0ull ? (uint32_t)(el[i] >> ibits) : 0u);
+            }
             n = (uint32_t)wave_sum_u64(n);             // (a held row has one wavefront)
-            draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, n, ibits + 32, 0, s, round);
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1) far = max(far, (uint32_t)__shfl_xor((int)far, d, 64));
+            draw_list<THREADS, E>(c, r, row, mass, poly, kmax, ibits, el, ew, n, ibits + (far ? 32 - __clz((int)far) : 1),
+                                  0, s, round);
             return;
         }
         // the list's labels become the threads' elements
@@ -1329,6 +1335,7 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
         hipLaunchKernelGGL(k_draw_join<XT>, g, dim3(kJoinThreads), 0, s, c, unit, ibits, chunks, stats, lists, open);
         hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits, (const uint32_t *)open);
     } else if (c.top_k == 0 && !c.top_ks && c.top_p >= 1.0f && !c.top_ps) draw_all<XT>(c, unit, s);
+    else if (c.V <= 512) hipLaunchKernelGGL((k_draw<XT, 64, 8, true>), g, dim3(64), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
     else if (c.V <= 1024) hipLaunchKernelGGL((k_draw<XT, 64, 16, true>), g, dim3(64), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
     else if (c.V <= 8192) hipLaunchKernelGGL((k_draw<XT, 256, 4, false>), g, dim3(256), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
     else hipLaunchKernelGGL((k_draw<XT, 1024, 4, false>), g, dim3(1024), 0, s, c, unit, ibits, (const uint32_t *)nullptr);
