@@ -166,12 +166,18 @@ __device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, fl
 // the last one and their sums are dropped. KS = 1: a wavefront owns 16 output
 // features and walks all of K. KS = 4: the four wavefronts of a workgroup own
 // the same 16 features and a quarter of K each, joined in LDS at the end.
-// Weights stream D tiles ahead of their use.
-template <typename XT, int WS, int GPT, int KS>
+// Weights stream D tiles ahead of their use. SPL = 1 (at most 4 rows, whose staging
+// takes one run of 8 features a thread) leaves registers for 8 wavefronts a SIMD:
+// one row x 131072 x 4096 takes 59 us with 3 tiles ahead (62, 61, 71 with 4, 2, 6),
+// where the general staging's registers leave 5 and it takes 74; 278 MB at 4.7 TB/s,
+// 92 % of what a large copy moves on this card.
+template <int KS, int SPL> constexpr int kTilesAhead = KS == 1 ? (SPL == 1 ? 3 : 4) : 2;
+
+template <typename XT, int WS, int GPT, int KS, int SPL>
 __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall c, int RP, int kc)
 {
     constexpr int P = kParts<XT>;
-    constexpr int D = KS == 1 ? 4 : 2;
+    constexpr int D = kTilesAhead<KS, SPL>;
     extern __shared__ __align__(16) char smem[];
     half8_t *xs = (half8_t *)smem;                                      // [P][KS * kc * 16][RP]
     const int part = KS * kc * 16 * RP;
@@ -200,7 +206,7 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
 
     // staging: 16 * RP threads (at most 64) take a block of 128 features, each up to four runs of 8
     const int per = min(64, 16 * RP), bpw = 64 / per;
-    const int l2 = lane % per, sr = l2 % RP, s0 = l2 / RP, sstep = per / RP, spl = 16 / sstep;
+    const int l2 = lane % per, sr = l2 % RP, s0 = l2 / RP, sstep = per / RP, spl = SPL == 1 ? 1 : 16 / sstep;
     const bool there = sr < M && row_active(c.rows, m0 + sr);
     const int longest = (l.kb + KS - 1) / KS;
     float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -212,10 +218,10 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
             const int sl = u / kc, b = c0 + u % kc;
             const int sb0 = (int)((int64_t)l.kb * sl / KS), sbn = (int)((int64_t)l.kb * (sl + 1) / KS) - sb0;
             const bool in = b < sbn;
-            float v[4][8];
+            float v[SPL][8];
             float mx = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < SPL; ++i) {
                 if (i < spl) {
                     load_x<XT>(x + (int64_t)sr * c.x_stride, there && in, (sb0 + b) * kTileK + (s0 + i * sstep) * 8, l.K, v[i]);
                     if (kScaled<XT>) mx = finite_max(v[i], mx);
@@ -229,7 +235,7 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
                 if (s0 == 0) xf[u * RP + sr] = ldexpf(1.0f, e);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < SPL; ++i) {
                 if (i < spl) {
                     half8_t hi, lo;
                     to_half<XT>(v[i], inv, hi, lo);
@@ -515,13 +521,23 @@ __global__ __launch_bounds__(256) void k_layer_pack(Layer l, LayerSource src, ui
         for (int j = 0; j < 4; ++j) {
             const int k0 = kb * kTileK + j * 32 + (lane >> 4) * 8;
             uint32_t v = 0;
+            if (n < (size_t)l.N && k0 + 8 <= l.K) {
+                // four bytes at once: their low halves to bits 0 .. 15, their high halves to 16 .. 31
+                struct __attribute__((packed, aligned(1))) Word { uint32_t w; };
+                uint32_t b = ((const Word *)(src.w + n * rowb + k0 / 2))->w;
+                uint32_t lo = b & 0x0F0F0F0Fu, hi = (b >> 4) & 0x0F0F0F0Fu;
+                lo = (lo | lo >> 4) & 0x00FF00FFu;
+                hi = (hi | hi >> 4) & 0x00FF00FFu;
+                v = ((lo | lo >> 8) & 0xFFFFu) | (hi | hi >> 8) << 16;
+            } else {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int k = k0 + 2 * p;
-                uint32_t byte = 0;
-                if (n < (size_t)l.N && k < l.K) byte = src.w[n * rowb + k / 2];
-                if (k + 1 >= l.K) byte &= 15u;
-                v |= (byte & 15u) << (4 * p) | (byte >> 4) << (16 + 4 * p);
+                for (int p = 0; p < 4; ++p) {
+                    const int k = k0 + 2 * p;
+                    uint32_t byte = 0;
+                    if (n < (size_t)l.N && k < l.K) byte = src.w[n * rowb + k / 2];
+                    if (k + 1 >= l.K) byte &= 15u;
+                    v |= (byte & 15u) << (4 * p) | (byte >> 4) << (16 + 4 * p);
+                }
             }
             o[j] = v;
         }
@@ -542,26 +558,28 @@ __global__ __launch_bounds__(256) void k_layer_pack(Layer l, LayerSource src, ui
         for (size_t i = t0; i < (size_t)l.N; i += nthreads) bias[i] = src.bias[i];
 }
 
+template <typename XT, int WS, int GPT, int KS, int SPL>
+hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
+{
+    constexpr int D = kTilesAhead<KS, SPL>;
+    // blocks of 128 features staged at a time: all, or what 40 KiB hold
+    const int longest = (l.kb + KS - 1) / KS;
+    const size_t per = (size_t)KS * RP * (256 * kParts<XT> + 4);
+    const int kc = std::min<int>(longest, std::max<int>(D, (int)(40960 / per) / D * D));
+    const size_t lds = std::max<size_t>(per * kc, KS > 1 ? (KS - 1) * 64 * sizeof(float4_t) : 0);
+    const dim3 g(KS > 1 ? l.nt : (l.nt + kLayerWaves - 1) / kLayerWaves, (c.M + kRowsM - 1) / kRowsM);
+    hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, KS, SPL>), g, dim3(kLayerThreads), lds, s, l, c, RP, kc);
+    return hipGetLastError();
+}
+
+// Fewer than 2048 tiles of features: K over the wavefronts, to have enough of them.
 template <typename XT, int WS, int GPT>
 hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
 {
     int RP = 1;
     while (RP < std::min(c.M, kRowsM)) RP *= 2;
-    const bool split = l.nt < 2048;
-    const int KS = split ? 4 : 1, D = split ? 2 : 4;
-    // blocks of 128 features staged at a time: all, or what 40 KiB hold
-    const int longest = (l.kb + KS - 1) / KS;
-    const size_t per = (size_t)KS * RP * (256 * kParts<XT> + 4);
-    int kc = std::min<int>(longest, std::max<int>(D, (int)(40960 / per) / D * D));
-    const size_t lds = std::max<size_t>(per * kc, split ? 3 * 64 * sizeof(float4_t) : 0);
-    const dim3 b(kLayerThreads);
-    const unsigned gy = (c.M + kRowsM - 1) / kRowsM;
-    if (split)
-        hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, 4>), dim3(l.nt, gy), b, lds, s, l, c, RP, kc);
-    else
-        hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, 1>), dim3((l.nt + kLayerWaves - 1) / kLayerWaves, gy), b, lds, s, l,
-                           c, RP, kc);
-    return hipGetLastError();
+    if (l.nt < 2048) return RP <= 4 ? few_launch<XT, WS, GPT, 4, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 4, 4>(l, c, RP, s);
+    return RP <= 4 ? few_launch<XT, WS, GPT, 1, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 1, 4>(l, c, RP, s);
 }
 
 // Row tiles of 16 a workgroup of k_layer_many takes (2 or 4); 0: the rows are few,
