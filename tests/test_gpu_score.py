@@ -85,6 +85,9 @@ def _layer_check(y, x, arrays, out):
     (17, 300, 16500, 64, "bf16", "f16", "f32", True, True),
     (32, 130, 16400, 32, "f16", "f32", "f32", False, False),
     (64, 390, 17001, 32, "f32", "f32", "f16", True, True),
+    (3, 2050, 16500, 64, "f32", "f16", "f32", True, True),
+    (16, 2049, 16490, 128, "bf16", "f32", "bf16", False, True),
+    (5, 2100, 16400, 32, "f16", "bf16", "f32", True, False),
     (65, 1, 8200, 128, "f32", "f16", "f32", True, False),
     (1000, 257, 1100, 96, "f16", "bf16", "bf16", True, False),
     (777, 512, 1300, 128, "bf16", "bf16", "f32", False, True),
@@ -191,7 +194,7 @@ def test_layer_repeats_bit_for_bit():
     a = layer.logits(h)
     for _ in range(3):
         assert torch.equal(a, layer.logits(h))
-    # a row's result does not depend on the rows beside it
+    # within the few-row path a row's result does not depend on the rows beside it
     assert torch.equal(layer.logits(h[7:8]), a[7:8])
     layer, _ = _layer_arrays(16, 300, 17000, 32)
     h = torch.randn(70, 300, device="cuda")

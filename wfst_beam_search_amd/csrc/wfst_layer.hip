@@ -582,12 +582,18 @@ hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
     return RP <= 4 ? few_launch<XT, WS, GPT, 1, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 1, 4>(l, c, RP, s);
 }
 
-// Row tiles of 16 a workgroup of k_layer_many takes (2 or 4); 0: the rows are few,
-// or the workgroups would be too few to fill the card, and k_layer_few serves.
-int many_tiles(const Layer &l, int32_t rows)
+// Row tiles of 16 a workgroup of k_layer_many takes (1, 2 or 4); 0: k_layer_few
+// serves, because the workgroups would be too few to fill the card or the rows are
+// few. Two launches cost some 6 us: below 16384 weight tiles they pay past 16 rows
+// only (17000 x 1024, 16 rows: few 12 .. 23 us, many 14); above, from 3 rows of
+// bfloat16 or binary32 on and from 5 of binary16, whose staging is a copy (32003 x
+// 2050, few / many: 2 rows 18 / 18, 20 / 20, 13 / 18 us; 4 rows 22 / 19, 34 / 20, 15 / 19;
+// 8 rows 42 / 19, 44 / 20, 28 / 19).
+int many_tiles(const Layer &l, int32_t rows, int32_t x_dtype)
 {
-    if (rows <= kRowsM) return 0;
-    const int mt = rows <= 2 * kRowsM ? 2 : 4;
+    const bool large = (int64_t)l.nt * l.kb >= 16384;
+    if (rows < (!large ? kRowsM + 1 : x_dtype == kF16 ? 5 : 3)) return 0;
+    const int mt = rows <= kRowsM ? 1 : rows <= 2 * kRowsM ? 2 : 4;
     const int64_t groups = (int64_t)((l.nt + 7) / 8) * ((rows + mt * kRowsM - 1) / (mt * kRowsM));
     return groups >= 128 ? mt : 0;
 }
@@ -614,9 +620,10 @@ hipError_t layer_many(const Layer &l, const LayerCall &c, hipStream_t s)
 template <typename XT, int WS, int GPT>
 hipError_t layer_rows(const Layer &l, const LayerCall &c, hipStream_t s)
 {
-    const int mt = many_tiles(l, c.M);
+    const int mt = many_tiles(l, c.M, c.x_dtype);
     if (mt == 4) return layer_many<XT, WS, GPT, 4>(l, c, s);
     if (mt == 2) return layer_many<XT, WS, GPT, 2>(l, c, s);
+    if (mt == 1) return layer_many<XT, WS, GPT, 1>(l, c, s);
     return layer_few<XT, WS, GPT>(l, c, s);
 }
 
@@ -651,7 +658,7 @@ hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, v
 
 size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype)
 {
-    if (!many_tiles(l, rows)) return 0;
+    if (!many_tiles(l, rows, x_dtype)) return 0;
     const size_t blocks = (size_t)((rows + kRowsM - 1) / kRowsM) * l.kb;
     return operand_bytes(l, rows, x_dtype) + (x_dtype == kF16 ? 0 : blocks * kRowsM * 4);
 }
