@@ -512,6 +512,44 @@ def test_sample_far_rows():
     _sample_check(wb.sample(t, u, top_k=30), t.contiguous(), u, top_k=30)
 
 
+def test_sample_longest_rows():
+    V = (1 << 20) + 3
+    g = torch.Generator(device="cuda").manual_seed(9)
+    t = torch.randn(3, V, generator=g, device="cuda") * 3
+    u = torch.rand(3, generator=g, device="cuda")
+    for s in (dict(), dict(top_k=40, top_p=0.9), dict(top_p=0.8), dict(min_p=0.05)):
+        _sample_check(wb.sample(t, u, **s), t, u, **s)
+
+
+@pytest.mark.parametrize("V", [30, 3000])
+def test_sample_extreme_temperatures(V):
+    """Infinite (in a tensor only), subnormal, huge and NaN."""
+    t = torch.randn(7, V, device="cuda")
+    t[:, ::3] = -float("inf")
+    u = torch.rand(7, device="cuda")
+    T = torch.tensor([float("inf"), 1e-45, 1e-30, 3e38, float("nan"), 1e30, 1e-3], device="cuda")
+    for s in (dict(), dict(min_p=1.0), dict(min_p=0.5), dict(top_k=7), dict(top_p=0.613), dict(top_p=0.4, min_p=0.9)):
+        full = dict(s, temperature=T)
+        _sample_check(wb.sample(t, u, **full), t, u, **full)
+
+
+def test_more_rows_than_workgroups():
+    R = (1 << 20) + 5
+    t = torch.randn(R, 4, device="cuda")
+    u = torch.rand(R, device="cuda")
+    y = wb.log_softmax(t)
+    assert torch.allclose(y.double(), torch.log_softmax(t.double(), -1), rtol=0, atol=1e-5)
+    keep = t >= t.topk(2, -1).values[:, 1:]
+    w = torch.where(keep, torch.exp(t.double() - t.amax(-1, keepdim=True).double()), 0.0)
+    run = w.cumsum(-1)
+    want = (run > (u.double() * run[:, -1])[:, None]).int().argmax(-1)
+    assert torch.equal(wb.sample(t, u, top_k=2).tokens.long(), want)
+    w = torch.exp(t.double() - t.amax(-1, keepdim=True).double())
+    run = w.cumsum(-1)
+    want = (run > (u.double() * run[:, -1])[:, None]).int().argmax(-1)
+    assert torch.equal(wb.sample(t, u).tokens.long(), want)
+
+
 def test_sample_many_rows():
     t = (torch.randn(3000, 50, device="cuda") * 2).bfloat16()
     u = torch.rand(3000, device="cuda")
@@ -549,6 +587,16 @@ def test_sample_refuses():
 
 # ---------------------------------------------------------------- a run of them
 
+def test_gradients_are_refused():
+    layer, _ = _layer_arrays(20, 64, 10, 32)
+    h = torch.randn(3, 64, device="cuda", requires_grad=True)
+    for f in (lambda: layer.logits(h), lambda: wb.log_softmax(h), lambda: wb.sample(h, torch.rand(3, device="cuda"))):
+        with pytest.raises(ValueError, match="gradient"):
+            f()
+        with torch.no_grad():
+            f()
+
+
 def test_streams_and_empty_calls():
     layer, arrays = _layer_arrays(21, 96, 300, 32, bias=True)
     h = torch.randn(40, 96, device="cuda")
@@ -570,10 +618,12 @@ def test_streams_and_empty_calls():
     assert wb.sample(want[:0], u[:0]).tokens.shape == (0,)
 
 
-def test_captured_run_replays():
+@pytest.mark.parametrize("B,T,V", [(6, 3, 1111), (4, 5, 70003), (30, 1, 20011)])
+def test_captured_run_replays(B, T, V):
     """Hidden states to draws captured into one graph: every replay on new inputs
-    equals the eager run, with eager work between the replays."""
-    B, T, K, V = 6, 3, 160, 1111
+    equals the eager run, with eager work between the replays (at sizes where the
+    operators take one launch, and where they take two and three)."""
+    K = 160
     layer, _ = _layer_arrays(23, K, V, 32, zeros=True, bias=True)
     h = torch.randn(B, T, K, device="cuda").bfloat16()
     u = torch.rand(B, T, device="cuda")

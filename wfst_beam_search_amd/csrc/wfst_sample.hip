@@ -84,7 +84,8 @@ struct MassOf {
     {
         if (!(lim > 0.0)) return -INFINITY;
         const double y = m + t * log(lim / one);
-        return (float)(y - 1e-6 * (fabs(y) + fabs(m)));
+        const double low = y - 1e-6 * (fabs(y) + fabs(m)) - 1e-12 * t;      // (t: a mass is off by 2^-51 of itself)
+        return low > -INFINITY ? (float)low : -INFINITY;       // (also where an infinite T leaves a NaN)
     }
     __device__ __forceinline__ float read(float x) const { return pick ? (x == top ? 0.0f : -INFINITY) : x; }
     // 2^(t + unit), t = (x - m) a <= 0 (below -1000: as -1000): adding `base`

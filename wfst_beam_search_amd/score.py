@@ -6,8 +6,9 @@ library (``wfst_layer_*``, ``wfst_log_softmax``, ``wfst_sample`` of
 and streams. They are inference operators: no gradient passes through them.
 
 Every call is asynchronous on ``stream`` (a ``torch.cuda.Stream`` or a raw
-handle; default: the current stream of the operands' device) and may be captured
-into a HIP graph when its ``lengths`` is a device tensor. Tensors may have any
+handle; default: the current stream of the operands' device; new tensors then
+belong to that stream) and may be captured into a HIP graph when its ``lengths``
+is a device tensor. Tensors may have any
 leading dimensions whose rows lie a constant distance apart. ``lengths`` (int32
 [B], for tensors [B, T, ...]; a device tensor, or host values that are copied
 first) marks the rows t >= lengths[b] as empty: they are not read, and in ``out``
@@ -70,6 +71,8 @@ def _gpu(t, what, device=None):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a torch tensor on the GPU")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, which these operators do not have (detach it, or use no_grad)")
     if device is not None and t.device != device:
         raise ValueError(f"{what} must be on {device}")
     return t
@@ -113,12 +116,14 @@ def _stream(stream, device):
     return raw, other
 
 
-def _keep(other, *tensors):
-    """Memory made here on the current stream is used on ``other``: not to be reused before that."""
-    if other is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(other)
+def _new(shape, dtype, device, other):
+    """Memory for work on ``other`` (None: the current stream), from that stream's
+    own pool: what it held before may still be in use on the current one."""
+    import torch
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _lengths(lengths, shape, device, other):
@@ -137,18 +142,16 @@ def _lengths(lengths, shape, device, other):
             lengths = lengths.numpy()
         host = torch.from_numpy(np.array(lengths, dtype=np.int32).reshape(-1))
         lengths = host.to(device)               # (the copy has ended when this returns)
-        _keep(other, lengths)
+        if other is not None:
+            lengths.record_stream(other)
     if lengths.numel() != shape[0]:
         raise ValueError("lengths must have B entries")
     return lengths, int(shape[1])
 
 
 def _out(out, shape, dtype, device, other):
-    import torch
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        _keep(other, out)
-        return out
+        return _new(shape, dtype, device, other)
     _gpu(out, "out", device)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)}")
@@ -159,9 +162,7 @@ def _workspace(nbytes, device, other):
     import torch
     if nbytes <= 0:
         return None
-    work = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _keep(other, work)
-    return work
+    return _new(nbytes, torch.uint8, device, other)
 
 
 def _p(t):
@@ -354,8 +355,7 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
     raw, other = _stream(stream, device)
     lengths, T = _lengths(lengths, shape, device, other)
     if out is None:
-        buf = torch.empty((3, *shape), dtype=torch.int32, device=device)
-        _keep(other, buf)
+        buf = _new((3, *shape), torch.int32, device, other)
         res = SampleResult(buf[0], buf[1].view(torch.float32), buf[2])
     else:
         res = SampleResult(*out)
