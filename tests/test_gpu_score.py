@@ -265,7 +265,7 @@ def test_log_softmax(V, x, out):
         _norm_check(wb.log_softmax(t, dtype=out, scale=0.7, bias=bias), t, out, float(np.float32(0.7)), bias)
 
 
-@pytest.mark.parametrize("V", [7, 500, 5000, 40001])
+@pytest.mark.parametrize("V", [7, 500, 5000, 40001, 70001])
 def test_log_softmax_masks_and_specials(V):
     inf = float("inf")
     t = torch.randn(9, V) * 3
@@ -294,7 +294,7 @@ def test_log_softmax_masks_and_specials(V):
     _norm_check(y, t[6:8], "f32", 1.0, bias)
 
 
-@pytest.mark.parametrize("V", [6, 77, 500, 5003, 20001])
+@pytest.mark.parametrize("V", [6, 77, 500, 5003, 20001, 70001])
 @pytest.mark.parametrize("x", ["f32", "f16"])
 def test_log_softmax_strides_lengths_in_place(V, x):
     B, T = 4, 6
@@ -352,11 +352,11 @@ def test_log_softmax_refuses():
     assert lib.wfst_log_softmax(np.zeros(40, np.float32).ctypes.data, 0, 10, 4, 10, 1.0, None, None, 1, t.data_ptr(),
                                 0, 10, None, 0, None) == -1
     # a row in pieces needs its workspace
-    t = torch.randn(2, 9000, device="cuda")
+    t = torch.randn(2, 90000, device="cuda")
     n = np.zeros(1, np.int64)
-    assert lib.wfst_log_softmax_workspace(0, 2, 9000, 0, n.ctypes.data) == 0 and n[0] > 0
+    assert lib.wfst_log_softmax_workspace(0, 2, 90000, 0, n.ctypes.data) == 0 and n[0] > 0
     for w, size in ((None, 0), (t.data_ptr(), int(n[0])), (torch.empty(8, device="cuda").data_ptr(), 8)):
-        assert lib.wfst_log_softmax(t.data_ptr(), 0, 9000, 2, 9000, 1.0, None, None, 1, t.data_ptr(), 0, 9000, w, size,
+        assert lib.wfst_log_softmax(t.data_ptr(), 0, 90000, 2, 90000, 1.0, None, None, 1, t.data_ptr(), 0, 90000, w, size,
                                     None) == -1
 
 

@@ -572,13 +572,15 @@ hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
     return hipGetLastError();
 }
 
-// Fewer than 2048 tiles of features: K over the wavefronts, to have enough of them.
+// Few tiles of features: K over the wavefronts of a workgroup, to have enough of
+// them (one row, one / four wavefronts a tile: 1000 tiles x 4096 15 / 13 us, 1000 x 1024
+// 7.5 / 8.4, 2001 x 2050 13 / 16, 4096 x 4096 31 / 41).
 template <typename XT, int WS, int GPT>
 hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
 {
     int RP = 1;
     while (RP < std::min(c.M, kRowsM)) RP *= 2;
-    if (l.nt < 2048) return RP <= 4 ? few_launch<XT, WS, GPT, 4, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 4, 4>(l, c, RP, s);
+    if (l.nt < 1536) return RP <= 4 ? few_launch<XT, WS, GPT, 4, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 4, 4>(l, c, RP, s);
     return RP <= 4 ? few_launch<XT, WS, GPT, 1, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 1, 4>(l, c, RP, s);
 }
 

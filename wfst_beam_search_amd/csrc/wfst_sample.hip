@@ -1303,19 +1303,21 @@ __global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int un
     }
 }
 
-// Wavefronts a row: one where the rows are many (the fixed work of a row, its
-// scans and its logarithm, is then done once), more where few rows would leave
-// the card idle.
+// Wavefronts a row: one for short rows (the fixed work of a row, its scans and its
+// logarithm, is then done once), more for long ones or where few rows would leave
+// the card idle. 1 / 4 / 16 wavefronts, binary16, us: 500 labels, 4096 rows 12 / 25 / 84;
+// 5000 labels, 256 rows 12 / 11 / 11, 1024 rows 13 / 15 / 27, 16000 rows 104 / 153 / 375;
+// 32003 labels, 256 rows 50 / 19 / 17, 1024 rows 67 / 49 / 61, 2048 rows 94 / 81 / 115.
 template <typename XT>
 void draw_all(const SampleCall &c, int unit, hipStream_t s)
 {
     constexpr int kPackW = 64 * (16 / (int)sizeof(XT));
     const int64_t packs = (c.V + kPackW - 1) / kPackW;
-    const int64_t want = std::min<int64_t>(packs, 4096 / std::max<int64_t>(c.rows, 1));
     const auto grid = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxRowGrid)); };
-    if (want < 4) hipLaunchKernelGGL((k_draw_all<XT, 1>), grid((c.rows + 3) / 4), dim3(256), 0, s, c, unit);
-    else if (want < 16) hipLaunchKernelGGL((k_draw_all<XT, 4>), grid(c.rows), dim3(256), 0, s, c, unit);
-    else hipLaunchKernelGGL((k_draw_all<XT, 16>), grid(c.rows), dim3(1024), 0, s, c, unit);
+    if (packs >= 16 && c.rows <= 256) hipLaunchKernelGGL((k_draw_all<XT, 16>), grid(c.rows), dim3(1024), 0, s, c, unit);
+    else if (packs >= 32 || (packs >= 4 && c.rows <= 512))
+        hipLaunchKernelGGL((k_draw_all<XT, 4>), grid(c.rows), dim3(256), 0, s, c, unit);
+    else hipLaunchKernelGGL((k_draw_all<XT, 1>), grid((c.rows + 3) / 4), dim3(256), 0, s, c, unit);
 }
 
 template <typename XT>
