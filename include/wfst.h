@@ -686,7 +686,7 @@ typedef struct wfst_sample_config {
  *  out_kept      device int32 [rows] or null: the number of labels kept.
  * Labels with score -inf or NaN are never drawn nor kept; a row of nothing else
  * is empty. +inf scores leave only each other, with equal masses. Masses are
- * computed in binary64 and added as multiples of 2^-52 or of V * 2^-62 rounded up
+ * computed in binary64 and added as multiples of 2^-51 or of V * 2^-62 rounded up
  * to a power of two, whichever is larger: results do not depend on any order of
  * addition, and labels whose mass rounds to 0 are not drawn. V in [1, 2^24].
  * Outputs must not overlap each other or the inputs. workspace: device memory,
