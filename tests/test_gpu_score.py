@@ -695,3 +695,34 @@ def test_hidden_states_to_words(dtype):
         dec.decode_hidden(other, h, L)
     dec.close()
     dg.release()
+
+
+# ---------------------------------------------------------------- rows cut into chunks, joined by four wavefronts
+
+@pytest.mark.parametrize("V", [150001, 300001, 520011])
+def test_sample_chunks_of_every_wavefront_join(V):
+    """The best chunk (whose bound is the row's) with each wavefront of the join in turn, the other chunks'
+    lists longer or shorter than its own."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    span = 2048                                          # labels of a chunk of binary32 scores
+    chunks = -(-V // span)
+    t = torch.randn(8, V, generator=g, device="cuda")
+    for r in range(8):
+        c0 = (chunks - 1) * r // 7
+        t[r, c0 * span:c0 * span + (span if r % 2 else 40)] += 6.0
+    t[5, ::2] = -float("inf")
+    t[6, V // 2:] = t[6, V // 2:].round()                # long lists of equal scores behind the best chunk
+    u = torch.rand(8, generator=g, device="cuda")
+    for s in (dict(temperature=0.0), dict(top_k=1), dict(top_k=50), dict(top_k=50, top_p=0.9), dict(top_k=600),
+              dict(top_k=64, min_p=0.01)):
+        _say("chunks", V, s)
+        want = wb.sample(t, u, **s)
+        _sample_check(want, t, u, **s)
+        for r in range(0, 8, 3):
+            for a, b in zip(wb.sample(t[r:r + 1], u[r:r + 1], **s), want):
+                assert torch.equal(a, b[r:r + 1])
+    # every kind of row in one call
+    s = dict(temperature=torch.tensor([0.0, 1, 1, 0, 1, 1, 1, 0.5], device="cuda"),
+             top_k=torch.tensor([0, 50, 0, 9, 200, 3, 700, 50], dtype=torch.int32, device="cuda"),
+             top_p=torch.tensor([1.0, 0.9, 0.8, 1, 1, 1, 0.5, 1], device="cuda"))
+    _sample_check(wb.sample(t, u, **s), t, u, **s)

@@ -1172,6 +1172,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int un
     constexpr int kEach = kChunk / THREADS;
     __shared__ DrawShared<THREADS, E, false> s;
     __shared__ uint16_t n_listed[kMaxChunks];
+    __shared__ uint32_t longest[WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Exp2Poly poly;
     uint32_t round = 0, round_small = 0;
@@ -1190,6 +1191,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int un
         uint32_t bound = st.bound;
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) bound = max(bound, (uint32_t)__shfl_xor((int)bound, d, 64));
+        // s.a, s.b and s.sum: the row before has been read by all (the barrier above). Read here, s.sum and s.b are
+        // written again behind a barrier only (block_before, element_totals, draw_list); a row that needs no masses
+        // reaches its lists without one, so what it passes there, `longest` and n_listed, is read nowhere else.
         const uint64_t spilt = __ballot(st.listed > kChunkList);
         if (lane == 0) { s.a[wave] = __float_as_uint(top); s.b[wave] = bound; s.sum[wave] = spilt; }
         if (tid == 0) s.count = 0;
@@ -1253,11 +1257,11 @@ __global__ __launch_bounds__(kJoinThreads) void k_draw_join(SampleCall c, int un
             uint32_t most = st.listed;
 #pragma unroll
             for (int d = 32; d >= 1; d >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, d, 64));
-            if (lane == 0) s.b[wave] = most;
+            if (lane == 0) longest[wave] = most;
             n_listed[tid] = (uint16_t)st.listed;
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < WAVES; ++i) most = max(most, s.b[i]);
+            for (int i = 0; i < WAVES; ++i) most = max(most, longest[i]);
             const int places = most > 1 ? 32 - __clz((int)most - 1) : 0;
             const unsigned long long *list = lists + r * chunks * kChunkList;
             constexpr int kAhead = 4;                          // loads in flight (those past a list's end are dropped)
