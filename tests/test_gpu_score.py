@@ -726,3 +726,19 @@ def test_sample_chunks_of_every_wavefront_join(V):
              top_k=torch.tensor([0, 50, 0, 9, 200, 3, 700, 50], dtype=torch.int32, device="cuda"),
              top_p=torch.tensor([1.0, 0.9, 0.8, 1, 1, 1, 0.5, 1], device="cuda"))
     _sample_check(wb.sample(t, u, **s), t, u, **s)
+
+
+def test_integers_past_32_bits():
+    """No limit written as the largest integer keeps every label; sizes and lengths past 32 bits are not cut."""
+    import sys
+    t = torch.randn(6, 900, device="cuda")
+    u = torch.rand(6, device="cuda")
+    for k in (sys.maxsize, 2 ** 32 + 1, 2 ** 31):
+        _sample_check(wb.sample(t, u, top_k=k, top_p=0.9), t, u, top_p=0.9)
+    w = torch.zeros(4, 32, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        wb.OutputLayer(w, torch.ones(4, 1, device="cuda"), group_size=2 ** 32 + 32)
+    x = t.view(2, 3, 900)
+    out = torch.full_like(x, 9.0)
+    wb.log_softmax(x, lengths=np.array([2 ** 32 + 1, -2 ** 32 + 2]), out=out)
+    assert torch.equal(out[0], wb.log_softmax(x)[0]) and (out[1] == 9).all()

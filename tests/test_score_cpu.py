@@ -143,3 +143,91 @@ def test_reference_sample_by_hand():
     assert ref.sample_row(x, 0.99, min_p=0.4)[0::2] == (3, 3)
     assert ref.sample_row(np.full(3, -np.inf), 0.5) == (-1, -np.inf, 0)
     assert ref.sample_row(np.array([np.nan, 1.0, np.inf, np.inf]), 0.6)[0::2] == (3, 2)
+
+
+# ---- integers past 32 bits (meta tensors have such shapes without memory)
+
+@pytest.fixture
+def no_gpu_checks(monkeypatch):
+    """The binding up to the library call, on tensors without memory."""
+    monkeypatch.setattr(score, "_gpu", lambda t, what, device=None: t)
+    monkeypatch.setattr(score, "_stream", lambda stream, device: (0, None))
+
+
+def _meta(*shape, dtype=torch.float16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+class _Recorder:
+    """The library, but for the calls that would reach a device."""
+
+    def __init__(self, lib):
+        self.lib = lib
+        self.top_k = []
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name)
+
+    def wfst_sample(self, *args):
+        self.top_k.append(args[6]._obj.top_k)
+        return 0
+
+
+@pytest.mark.parametrize("given,passed", [
+    (0, 0), (1, 1), (7, 7), (999, 999), (1000, 1000), (1001, 1000), (2 ** 31, 1000), (2 ** 32 + 1, 1000),
+    (2 ** 63 - 1, 1000), (10 ** 30, 1000), (-1, -1), (-2 ** 31, -1), (-2 ** 32 + 5, -1)])
+def test_top_k_keeps_its_meaning_past_32_bits(lib, monkeypatch, no_gpu_checks, given, passed):
+    fake = _Recorder(lib)
+    monkeypatch.setattr(score, "load_library", lambda: fake)
+    wb.sample(_meta(2, 1000), _meta(2, dtype=torch.float32), top_k=given)
+    assert fake.top_k == [passed]
+
+
+def test_sizes_past_32_bits_are_refused(lib, no_gpu_checks):
+    wide, tall = _meta(1, 2 ** 32 + 5), _meta(2 ** 32 + 2, 1, 8)
+    with pytest.raises(ValueError, match="V .* 32 bits"):
+        wb.log_softmax(wide)
+    with pytest.raises(ValueError, match="V .* 32 bits"):
+        wb.sample(wide, _meta(1, dtype=torch.float32))
+    with pytest.raises(ValueError, match="T .* 32 bits"):
+        wb.log_softmax(_meta(2, 2 ** 32 + 4, 8), lengths=[1, 1])
+    w, s = _meta(4, 32, dtype=torch.uint8), _meta(4, 1)
+    with pytest.raises(ValueError, match="group_size .* 32 bits"):
+        wb.OutputLayer(w, s, group_size=2 ** 32 + 32)
+    with pytest.raises(ValueError, match="in_features .* 32 bits"):
+        wb.OutputLayer(_meta(4, 2 ** 31 + 32, dtype=torch.uint8), s, group_size=2 ** 32)
+    with pytest.raises(ValueError, match="out_features .* 32 bits"):
+        wb.OutputLayer(_meta(2 ** 32 + 4, 32, dtype=torch.uint8), _meta(2 ** 32 + 4, 1), group_size=64)
+    layer = object.__new__(wb.OutputLayer)
+    layer.handle, layer.device, layer.in_features, layer.out_features, layer._bytes = 1, tall.device, 8, 4, {}
+    try:
+        with pytest.raises(ValueError, match="rows .* 32 bits"):
+            layer.logits(tall)
+    finally:
+        layer.handle = None
+
+
+@pytest.mark.parametrize("given", [[2 ** 32 + 5, -2 ** 32 + 5, 3], np.array([2 ** 32 + 5, -2 ** 32 + 5, 3]),
+                                   torch.tensor([2 ** 32 + 5, -2 ** 32 + 5, 3])])
+def test_host_lengths_past_32_bits(given):
+    got, T = score._lengths(given, (3, 7), torch.device("cpu"), None)
+    assert T == 7 and got.dtype == torch.int32 and got.tolist() == [2 ** 31 - 1, -1, 3]
+
+
+def test_host_lengths_of_other_types():
+    for given in ([3, 0, 7], np.array([3, 0, 7], np.uint8), torch.tensor([3, 0, 7], dtype=torch.int16), (3.0, 0.0, 7.0)):
+        assert score._lengths(given, (3, 7), torch.device("cpu"), None)[0].tolist() == [3, 0, 7]
+    assert score._lengths([], (0, 7), torch.device("cpu"), None)[0].numel() == 0
+    with pytest.raises((ValueError, OverflowError)):
+        score._lengths([float("nan"), 1, 2], (3, 7), torch.device("cpu"), None)
+
+
+def test_hidden_lengths_are_checked_as_given():
+    class Layer:
+        out_features = 5
+
+    dec = object.__new__(wb.Decoder)
+    dec.handle, dec.graph = None, type("G", (), {"vocab": 5})
+    for bad in (np.array([2 ** 32 + 1, 0]), [-2 ** 32 + 1, 0], [8, 0]):
+        with pytest.raises(ValueError, match="lengths"):
+            dec._log_probs(Layer, torch.zeros(2, 7, 3), bad, 1.0, None, None)

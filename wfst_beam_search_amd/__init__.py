@@ -355,9 +355,10 @@ class Decoder:
             raise ValueError("hidden must be [B, T, K]")
         if layer.out_features != self.graph.vocab:
             raise ValueError("the layer's out_features differ from the graph's vocabulary")
-        lens = np.asarray(lengths, dtype=np.int32).reshape(-1)
+        lens = np.asarray(lengths).reshape(-1)          # (checked before they become 32 bits)
         if lens.size and (lens.min() < 0 or lens.max() > hidden.shape[1]):
             raise ValueError("lengths must lie in [0, T]")
+        lens = lens.astype(np.int32)
         return layer.log_probs(hidden, dtype=self.lp_dtype, scale=scale, bias=bias, lengths=lens, stream=stream)
 
     @staticmethod

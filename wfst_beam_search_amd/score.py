@@ -67,6 +67,17 @@ def _named(dtype):
     return names[dtype]
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _int32(v, what):
+    """v as an int that the library's 32 bits hold (ctypes would cut off the bits above them)."""
+    v = int(v)
+    if not -_INT32_MAX <= v <= _INT32_MAX:
+        raise ValueError(f"{what} ({v}) does not fit 32 bits")
+    return v
+
+
 def _gpu(t, what, device=None):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -140,13 +151,15 @@ def _lengths(lengths, shape, device, other):
     else:
         if isinstance(lengths, torch.Tensor):
             lengths = lengths.numpy()
-        host = torch.from_numpy(np.array(lengths, dtype=np.int32).reshape(-1))
-        lengths = host.to(device)               # (the copy has ended when this returns)
+        host = np.array(lengths).reshape(-1)
+        if host.dtype != np.int32:              # (wider numbers to the nearest 32-bit one: none passes T)
+            host = np.array([min(max(int(v), -1), _INT32_MAX) for v in host.tolist()], dtype=np.int32)
+        lengths = torch.from_numpy(host).to(device)     # (the copy has ended when this returns)
         if other is not None:
             lengths.record_stream(other)
     if lengths.numel() != shape[0]:
         raise ValueError("lengths must have B entries")
-    return lengths, int(shape[1])
+    return lengths, _int32(shape[1], "T")
 
 
 def _out(out, shape, dtype, device, other):
@@ -191,9 +204,9 @@ class OutputLayer:
         _gpu(scales, "scales", device)
         if weights.dtype != torch.uint8 or weights.dim() != 2 or not weights.is_contiguous():
             raise TypeError("weights must be a packed uint8 tensor [N, ceil(K / 2)]")
-        N, half = (int(v) for v in weights.shape)
-        K = 2 * half if in_features is None else int(in_features)
-        group_size = int(group_size)
+        N, half = _int32(weights.shape[0], "out_features"), int(weights.shape[1])
+        K = _int32(2 * half if in_features is None else in_features, "in_features")
+        group_size = _int32(group_size, "group_size")
         if (K + 1) // 2 != half:
             raise ValueError("weights must have ceil(in_features / 2) columns")
         if group_size < 1:
@@ -227,6 +240,7 @@ class OutputLayer:
         _gpu(hidden, "hidden", self.device)
         code = _code(hidden, "hidden")
         rows, step = _rows(hidden, "hidden")
+        rows = _int32(rows, "rows")
         if hidden.shape[-1] != self.in_features:
             raise ValueError(f"hidden must be [..., {self.in_features}]")
         raw, other = _stream(stream, self.device)
@@ -287,7 +301,7 @@ def log_softmax(x, dtype: str | None = None, scale: float = 1.0, bias=None, leng
     device = x.device
     code = _code(x, "x")
     rows, step = _rows(x, "x")
-    V = int(x.shape[-1])
+    V = _int32(x.shape[-1], "V")
     want = x.dtype if dtype is None else _named(dtype)
     if bias is not None:
         _gpu(bias, "bias", device)
@@ -344,6 +358,7 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
     device = scores.device
     code = _code(scores, "scores")
     rows, step = _rows(scores, "scores")
+    V = _int32(scores.shape[-1], "V")
     shape = scores.shape[:-1]
     _gpu(u, "u", device)
     if u.dtype != torch.float32 or u.shape != shape or not u.is_contiguous():
@@ -362,8 +377,8 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
         for o, dt in zip(res, (torch.int32, torch.float32, torch.int32)):
             if o is None or not _out(o, shape, dt, device, other).is_contiguous():
                 raise ValueError("out must be three packed tensors (int32, float32, int32)")
-    cfg = _SampleConfig(float(t), int(k), float(p), float(mp), _p(ts), _p(ks), _p(ps), _p(mps))
-    V = int(scores.shape[-1])
+    k = max(-1, min(int(k), V))                 # (V and more: all)
+    cfg = _SampleConfig(float(t), k, float(p), float(mp), _p(ts), _p(ks), _p(ps), _p(mps))
     need = _sample_bytes(code, rows, V)
     work = _workspace(need, device, other)
     _check(lib.wfst_sample(scores.data_ptr(), code, step, rows, V, u.data_ptr(), ctypes.byref(cfg), _p(lengths), T,
