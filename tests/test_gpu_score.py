@@ -742,3 +742,24 @@ def test_integers_past_32_bits():
     out = torch.full_like(x, 9.0)
     wb.log_softmax(x, lengths=np.array([2 ** 32 + 1, -2 ** 32 + 2]), out=out)
     assert torch.equal(out[0], wb.log_softmax(x)[0]) and (out[1] == 9).all()
+
+
+def test_forward_mode_duals_are_refused():
+    import torch.autograd.forward_ad as fw
+    layer, _ = _layer_arrays(27, 64, 10, 32)
+    h, u, b = torch.randn(3, 64, device="cuda"), torch.rand(3, device="cuda"), torch.randn(64, device="cuda")
+    with fw.dual_level():
+        d, db = fw.make_dual(h, torch.ones_like(h)), fw.make_dual(b, torch.ones_like(b))
+        du, out = fw.make_dual(u, torch.ones_like(u)), fw.make_dual(torch.empty_like(h), h)
+        for f in (lambda: layer.logits(d), lambda: layer.log_probs(d[1:]), lambda: wb.log_softmax(d),
+                  lambda: wb.log_softmax(h, bias=db), lambda: wb.log_softmax(h, out=out), lambda: wb.sample(d, u),
+                  lambda: wb.sample(h, du), lambda: wb.sample(h, u, temperature=du)):
+            with pytest.raises(ValueError, match="tangent"):
+                f()
+        assert torch.equal(wb.log_softmax(d.detach()), wb.log_softmax(h))      # the primal alone
+        assert torch.equal(layer.logits(d.detach()), layer.logits(h))
+        with torch.inference_mode():
+            wb.log_softmax(h)
+    with pytest.raises(ValueError, match="tangent"):
+        torch.func.jvp(lambda t: wb.log_softmax(t), (h,), (torch.ones_like(h),))
+    assert torch.equal(wb.log_softmax(h), wb.log_softmax(h.clone()))

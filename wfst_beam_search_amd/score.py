@@ -3,7 +3,8 @@ log-softmax that makes ``log_prob`` of its logits, and the draw of tokens from
 scores. Thin bindings like the rest of the package: the work runs in the HIP
 library (``wfst_layer_*``, ``wfst_log_softmax``, ``wfst_sample`` of
 ``include/wfst.h``, which states the formulas); PyTorch supplies device memory
-and streams. They are inference operators: no gradient passes through them.
+and streams. They are inference operators: no gradient passes through them, and a
+tensor that needs one (backward, or a forward-mode dual) is refused.
 
 Every call is asynchronous on ``stream`` (a ``torch.cuda.Stream`` or a raw
 handle; default: the current stream of the operands' device; new tensors then
@@ -84,6 +85,9 @@ def _gpu(t, what, device=None):
         raise TypeError(f"{what} must be a torch tensor on the GPU")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{what} requires a gradient, which these operators do not have (detach it, or use no_grad)")
+    fw = torch.autograd.forward_ad
+    if fw._current_level >= 0 and torch._C._is_fwd_grad_enabled() and fw.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{what} carries a forward-mode tangent, which these operators do not have (detach it)")
     if device is not None and t.device != device:
         raise ValueError(f"{what} must be on {device}")
     return t
