@@ -763,3 +763,51 @@ def test_forward_mode_duals_are_refused():
     with pytest.raises(ValueError, match="tangent"):
         torch.func.jvp(lambda t: wb.log_softmax(t), (h,), (torch.ones_like(h),))
     assert torch.equal(wb.log_softmax(h), wb.log_softmax(h.clone()))
+
+
+# ---------------------------------------------------------------- output layer: small scales, small and mixed hidden states
+
+def _layer_bound(layer, arrays, h, out="f32", held=0.0):
+    """|y - exact| <= half a step of the output + (K / 32 + 40) E S + held sum |w| (the module's bound; each
+    addition of two subnormal numbers is exact, each product's rounding among them at most 2^-150; held: how far
+    a hidden state may be off by its block's largest)."""
+    y = layer.logits(h, dtype=out)
+    want, size = ref.layer(_np(h), *arrays)
+    n = arrays[4] / 32 + 40
+    tol = _half(out) * np.abs(want) * 1.001 + n * E * size + n * 2.0 ** -149
+    tol = tol + held * ref.layer(np.ones((1, arrays[4])), *arrays)[1]
+    err = np.abs(_np(y) - want)
+    bad = err > tol
+    assert not bad.any(), (np.argwhere(bad)[:4], _np(y)[bad][:4], want[bad][:4], (err / tol).max())
+
+
+def _scaled_layer(seed, K, N, group, factor, scale):
+    """Scales of about `factor`, rounded to their type."""
+    rng = np.random.default_rng(seed)
+    w = rng.integers(0, 256, (N, (K + 1) // 2), dtype=np.uint8)
+    s = torch.from_numpy(((0.5 + rng.random((N, -(-K // group)))) * factor).astype(np.float32)).to(DT[scale])
+    layer = wb.OutputLayer(torch.from_numpy(w).cuda(), s.cuda(), in_features=K, group_size=group)
+    return layer, (w, s.double().numpy(), None, None, K, group)
+
+
+@pytest.mark.parametrize("M,K,N,group", [(1, 256, 20, 32), (4, 300, 40, 128), (16, 513, 33, 64),      # few rows, K split
+                                         (2, 140, 24600, 32),                                         # few rows, K whole
+                                         (20, 260, 16500, 64), (70, 390, 8200, 128)])                 # operands
+@pytest.mark.parametrize("x,scale,factor,size", [("f32", "f32", 1e-7, 1e-32), ("f32", "f16", 3e-5, 1e-32),
+                                                 ("bf16", "f32", 2e-7, 1e-32), ("bf16", "bf16", 1e-8, 1e-32),
+                                                 ("f32", "bf16", 1e5, 1e33), ("bf16", "f32", 3e4, 3e33)])
+def test_layer_scale_and_block_factor_do_not_meet_alone(M, K, N, group, x, scale, factor, size):
+    """A block's power of two times a group's scale may leave the binary32 range, or its normal part, where the
+    result does not: a row's accuracy depends neither on that nor on the number of rows."""
+    _say("small scales", M, K, N, group, x, scale, factor, size)
+    layer, arrays = _scaled_layer(M + K, K, N, group, factor, scale)
+    h = (torch.from_numpy(np.random.default_rng(K).normal(size=(M, K)).astype(np.float32)) * size).to(DT[x])
+    if factor > 1:                          # one huge value a row; the columns whose weight there is 0 stay small
+        h *= 1e-5
+        h[:, K // 2] = 2e38
+        q = ref.unpack(arrays[0], K)[:, K // 2] == 8
+        assert q.any() or N < 200
+        y = _np(layer.logits(h.cuda()))
+        assert not np.isnan(y).any() and (not q.any() or np.isfinite(y[:, q]).all())
+        return
+    _layer_bound(layer, arrays, h.cuda())

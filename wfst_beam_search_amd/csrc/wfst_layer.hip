@@ -258,12 +258,7 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
                 sq[i] = load_tile_scale<WS, GPT>(l, nx * kTileN + col);
                 const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
                 const int u = slice * kc + t + i - c0;
-                float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-                if (kScaled<XT>) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) f[q] = xf[u * RP + min(frow + q, RP - 1)];
-                }
-                float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f}, tile = sum;
                 ZeroPair z = zero_pair(ts.z & 255u);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -277,10 +272,17 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
                         const float s = scale_of<WS, GPT>(ts, j * GPT / 4, bf16s);
 #pragma unroll
                         for (int q4 = 0; q4 < 4; ++q4) {
-                            acc[q4] = fmaf(sum[q4], kScaled<XT> ? s * f[q4] : s, acc[q4]);
+                            if (!kScaled<XT>) acc[q4] = fmaf(sum[q4], s, acc[q4]);
+                            else if (j < 4 / GPT) tile[q4] = sum[q4] * s;
+                            else tile[q4] = fmaf(sum[q4], s, tile[q4]);
                             sum[q4] = 0.0f;
                         }
                     }
+                }
+                // (the block's factor comes last: its product with a small scale alone may be subnormal)
+                if (kScaled<XT>) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) acc[q4] = fmaf(tile[q4], xf[u * RP + min(frow + q4, RP - 1)], acc[q4]);
                 }
             }
         }
