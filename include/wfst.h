@@ -623,9 +623,11 @@ int wfst_layer_release(wfst_layer_t layer);   /* null is a no-op */
 /*
  * out[r, :] = the layer's y for hidden state x[r, :], rows in [0, 2^20 - 16].
  * q - zeros is exact, products and a group's sums are binary32 sums of products
- * of exact values (a binary32 x enters as a sum of two binary16 values, off by at
- * most 2^-24 of itself or 2^-38 of the largest finite |x| among its 128
- * neighbours); infinities and NaN in x go where the formula takes them.
+ * of exact values, with two exceptions, both next to the largest finite |x| among
+ * a row's 128 features that begin at a multiple of 128: a bfloat16 x more than
+ * 2^30 times smaller than it may be off by 2^-39 of it; a binary32 x enters as two
+ * binary16 values, off by at most 2^-23 of x or 2^-50 of that largest. Infinities
+ * and NaN in x go where the formula takes them.
  * out must not overlap x. workspace: device memory, 16-byte aligned, of at least
  * wfst_layer_workspace's bytes (null when those are 0), in use until the stream
  * has passed the call. Errors: WFST_EINVAL, WFST_EDEVICE.

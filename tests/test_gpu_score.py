@@ -811,3 +811,31 @@ def test_layer_scale_and_block_factor_do_not_meet_alone(M, K, N, group, x, scale
         assert not np.isnan(y).any() and (not q.any() or np.isfinite(y[:, q]).all())
         return
     _layer_bound(layer, arrays, h.cuda())
+
+
+@pytest.mark.parametrize("M,K,N,group", [(1, 256, 64, 32), (3, 300, 40, 128), (16, 513, 33, 64), (2, 140, 24600, 32),
+                                         (20, 260, 16500, 64), (70, 390, 8200, 128), (33, 512, 16400, 32)])
+def test_layer_binary32_beside_large_values(M, K, N, group):
+    """Small binary32 values keep their digits beside a large one in their block: the columns whose weight at the
+    large one is 0 see them alone (S counts no more than that). Two binary16 parts, the second scaled by 2^11, hold
+    a value within 2^-23 of itself or 2^-50 of its block's largest."""
+    rng = np.random.default_rng(M * K)
+    w = rng.integers(0, 256, (N, (K + 1) // 2), dtype=np.uint8)
+    big = np.arange(7, K, 128)
+    w[::2, big // 2] = w[::2, big // 2] & 15 | 8 << 4                    # feature 7 of each block (odd: the high half)
+    s = torch.from_numpy(((0.5 + rng.random((N, -(-K // group)))) / np.sqrt(K)).astype(np.float32))
+    layer = wb.OutputLayer(torch.from_numpy(w).cuda(), s.cuda(), in_features=K, group_size=group)
+    h = rng.normal(size=(M, K)).astype(np.float32) * 0.01
+    h[:, big] = rng.normal(size=(M, big.size)) * 1e7
+    _layer_bound(layer, (w, s.double().numpy(), None, None, K, group), torch.from_numpy(h).cuda(),
+                 held=2.0 ** -50 * float(np.abs(h).max()))
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 128, 40), (5, 300, 40), (40, 300, 16500)])
+def test_layer_subnormal_hidden_states(M, K, N):
+    """Blocks of subnormal binary32 (and bfloat16) values, large scales: the result is normal."""
+    for x in ("f32", "bf16"):
+        layer, arrays = _scaled_layer(3, K, N, 64, 1e8, "f32")
+        h = (torch.from_numpy(np.random.default_rng(K).normal(size=(M, K)).astype(np.float32)) * 2e-40).to(DT[x])
+        h[:, ::3] *= 1e-2
+        _layer_bound(layer, arrays, h.cuda())

@@ -19,10 +19,13 @@ namespace {
 //
 // x enters the matrix unit as binary16. bfloat16 and binary32 rows are scaled
 // by a power of two per 128 features so that the block's largest finite value
-// lies in [2^14, 2^15): a bfloat16 value then fits binary16 exactly or, 2^29
-// below the block's largest, loses less than 2^-39 of that; a binary32 value is
-// cut into a sum of two binary16 values (off by at most 2^-24 of itself, or
-// 2^-39 of the block's largest).
+// lies in [2^14, 2^15): a bfloat16 value then fits binary16 exactly or, 2^30
+// below the block's largest, loses less than 2^-39 of that. A binary32 value is
+// cut into hi + lo / 2^11, two binary16 values, and lo meets weights divided by
+// 2^11 (exact, and both sums stay one): off by at most 2^-23 of itself, or 2^-50
+// of the block's largest. Without the 2^11 lo would end at binary16's smallest
+// number, 2^-39 of the block's largest: 16 bits of 0.01 beside 1e5. Exact values
+// would take a third part, a product more of two.
 
 constexpr int kLayerWaves = 4;
 constexpr int kLayerThreads = kLayerWaves * kWaveSize;
@@ -65,7 +68,7 @@ __device__ __forceinline__ float finite_max(const float (&v)[8], float mx)
     return mx;
 }
 
-// The binary16 operand (and for binary32 its remainder) of eight values, scaled by `inv`, a power of two.
+// The binary16 operand (and for binary32 its remainder, times 2^11) of eight values, scaled by `inv`, a power of two.
 template <typename XT>
 __device__ __forceinline__ void to_half(const float (&v)[8], float inv, half8_t &hi, half8_t &lo)
 {
@@ -75,7 +78,7 @@ __device__ __forceinline__ void to_half(const float (&v)[8], float inv, half8_t 
         hi[j] = (_Float16)s;
         if (kParts<XT> == 2) {
             const float d = s - (float)hi[j];
-            lo[j] = (_Float16)(fabsf(s) < INFINITY ? d : 0.0f);      // (an infinity or NaN is in hi alone)
+            lo[j] = (_Float16)(fabsf(s) < INFINITY ? d * 2048.0f : 0.0f);      // (an infinity or NaN is in hi alone)
         }
     }
 }
@@ -140,6 +143,12 @@ __device__ __forceinline__ half8_t unpack_word(uint32_t w, uint32_t magic, const
     q.h[1] = __builtin_elementwise_fma(q.h[1], r16, z.sixteenth);
     q.h[3] = __builtin_elementwise_fma(q.h[3], r16, z.sixteenth);
     return q.v;
+}
+
+// The weights that meet a binary32 value's second part.
+__device__ __forceinline__ half8_t part_weights(const half8_t &q, int part)
+{
+    return part ? q * (_Float16)(1.0f / 2048.0f) : q;
 }
 
 // 1024 in both halves, in a vector register that the compiler does not fold: a
@@ -266,8 +275,8 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
                     const half8_t q = unpack_word(w[j], magic, z);
 #pragma unroll
                     for (int p = 0; p < P; ++p)
-                        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[p * part + (u * 16 + j * 4 + quad) * RP + arow], q,
-                                                                     sum, 0, 0, 0);
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[p * part + (u * 16 + j * 4 + quad) * RP + arow],
+                                                                     part_weights(q, p), sum, 0, 0, 0);
                     if ((j + 1) % (4 / GPT) == 0) {
                         const float s = scale_of<WS, GPT>(ts, j * GPT / 4, bf16s);
 #pragma unroll
@@ -461,9 +470,13 @@ __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const 
                     q[n] = unpack_word(w, magic, z[n]);
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
+                for (int p = 0; p < P; ++p) {
+                    if (p) {
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
+                        for (int n = 0; n < NT; ++n) q[n] = part_weights(q[n], p);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
                         const half8_t a = a0[m * kBlk + (p * 4 + j) * 64];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
