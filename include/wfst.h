@@ -688,9 +688,13 @@ typedef struct wfst_sample_config {
  *  out_kept      device int32 [rows] or null: the number of labels kept.
  * Labels with score -inf or NaN are never drawn nor kept; a row of nothing else
  * is empty. +inf scores leave only each other, with equal masses. Masses are
- * computed in binary64 and added as multiples of 2^-51 or of V * 2^-62 rounded up
- * to a power of two, whichever is larger: results do not depend on any order of
- * addition, and labels whose mass rounds to 0 are not drawn. V in [1, 2^24].
+ * computed in binary64 and added as multiples of 2^-unit, so results do not depend
+ * on any order of addition; labels whose mass rounds to 0 are not drawn. unit is
+ * min(51, 62 - ceil(log2 V)): a sum of masses is off by at most V * 2^-(unit + 1)
+ * of the largest one, 2^-29 at 131072 labels, 2^-23 at 2^20. Past 2^20 labels unit
+ * follows from the row's own masses, and sums are off by at most 2^-23 of its
+ * total. A draw or a top_p cut whose border lies nearer than that may fall on the
+ * other side of it. V in [1, 2^24].
  * Outputs must not overlap each other or the inputs. workspace: device memory,
  * 16-byte aligned, of at least wfst_sample_workspace's bytes (null when those are
  * 0), in use until the stream has passed the call.

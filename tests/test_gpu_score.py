@@ -839,3 +839,93 @@ def test_layer_subnormal_hidden_states(M, K, N):
         h = (torch.from_numpy(np.random.default_rng(K).normal(size=(M, K)).astype(np.float32)) * 2e-40).to(DT[x])
         h[:, ::3] *= 1e-2
         _layer_bound(layer, arrays, h.cuda())
+
+
+# ---------------------------------------------------------------- draw: rows with a long, light tail
+
+def _mass_error(V):
+    """Bound of a sum's error: V masses rounded to multiples of 2^-unit, unit = min(51, 62 - ceil(log2 V)), as a share
+    of the largest; past 2^20 labels V * (labels of one of at least 256 threads) * 2^-63 of the total."""
+    bits = max(0, (V - 1).bit_length())
+    return V * 2.0 ** -(min(51, 62 - bits) + 1) if V <= 1 << 20 else V * (V / 256 + 32) * 2.0 ** -63
+
+
+def _tail_check(R, V, tail, x, s, us):
+    """Rows of one label of score 0 and V - 1 of score `tail`: index i has the running mass 1 + i w."""
+    t = torch.full((R, V), tail, device="cuda", dtype=DT[x])
+    t[:, 0] = 0
+    u = torch.tensor([us[i % len(us)] for i in range(R)], device="cuda")
+    r = wb.sample(t, u, **s)
+    w = float(np.exp(np.float64(float(t[0, 1]))))
+    C = 1 + (V - 1) * w
+    err = _mass_error(V) * C + 2.0 ** -48
+    n = V
+    if s.get("top_p", 1.0) < 1:
+        n = max(1, int(np.ceil((float(np.float32(s["top_p"])) * C - 1) / w)) + 1)
+    kept = r.kept.cpu().numpy()
+    room = 0 if n == V else 2 * err / w + 1
+    assert (np.abs(kept - n) <= room).all(), (kept, n, room)
+    for i in range(min(R, 4 * len(us))):
+        total = 1 + (int(kept[i]) - 1) * w
+        goal = float(u[i].double()) * total
+        want = 0 if goal < 1 else int((goal - 1) / w) + 1
+        tok = int(r.tokens[i])
+        assert abs(tok - want) <= 2 * err / w + 1 or abs(goal - 1) <= 2 * err, (i, tok, want)
+        lp = (float(t[i, tok]) if tok else 0.0) - np.log(total)
+        # (total is off by err at most; a binary32 result)
+        assert abs(float(r.log_probs[i]) - lp) <= err * 1.001 + 2.0 ** -24 * abs(lp), (i, float(r.log_probs[i]), lp)
+
+
+US = [0.0, 0.25, 0.6, 0.75, 1.0 - 2.0 ** -24, 0.9999]
+
+
+@pytest.mark.parametrize("V,R,tail,x", [
+    (131072, 1, -31.5, "f32"), (131072, 33, -31.5, "f32"), (131072, 2, -20.0, "bf16"), (131072, 40, -12.25, "bf16"),
+    (1 << 20, 3, -28.0, "f16"), ((1 << 20) + 3, 2, -28.125, "f32"), ((1 << 20) + 3, 258, -28.125, "f16"),
+    ((1 << 21) + 5, 3, -27.75, "bf16"), (1 << 24, 2, -27.296875, "f32"), (1 << 24, 3, -17.0, "f16"),
+    ((1 << 24) - 1, 2, -14.0, "bf16")])
+def test_sample_light_tails(V, R, tail, x):
+    for s in (dict(), dict(min_p=1e-30), dict(top_p=0.9), dict(top_p=1.0 - 2.0 ** -13)):
+        _say("tails", V, R, tail, x, s)
+        _tail_check(R, V, tail, x, s, US)
+
+
+@pytest.mark.parametrize("V", [(1 << 20) + 77, (1 << 22) + 1, 1 << 24])
+@pytest.mark.parametrize("sigma", [0.01, 3.0])
+def test_sample_longest_rows_against_running_sums(V, sigma):
+    """The token's running mass brackets u times the total, within the sums' error."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    t = torch.randn(3, V, generator=g, device="cuda") * sigma
+    t[1, ::2] = -float("inf")
+    t[2, V // 3] = 40.0 * sigma
+    u = torch.rand(3, generator=g, device="cuda")
+    m = torch.exp(t.double() - t.amax(-1, keepdim=True).double())
+    run = m.cumsum(-1)
+    for s in (dict(), dict(top_k=V // 2), dict(top_p=0.99), dict(temperature=0.0)):
+        _say("longest", V, sigma, s)
+        r = wb.sample(t, u, **s)
+        if "temperature" in s:
+            assert torch.equal(r.tokens.long(), t.argmax(-1))
+            continue
+        for i in range(3):
+            mi, total = m[i], run[i, -1]
+            if s:
+                order = torch.sort(t[i], descending=True, stable=True).indices
+                sorted_run = mi[order].cumsum(0)
+                n = min(V // 2, int((t[i] > -float("inf")).sum()))
+                if "top_p" in s:
+                    goal = float(np.float32(0.99)) * total
+                    err = (_mass_error(V) + 2.0 ** -45) * total
+                    lo, hi = (int((sorted_run < goal + d).sum()) + 1 for d in (-err, err))
+                    assert lo <= int(r.kept[i]) <= hi, (lo, int(r.kept[i]), hi)
+                    n = int(r.kept[i])
+                assert int(r.kept[i]) == n
+                mi = torch.zeros_like(mi).scatter_(0, order[:n], mi[order[:n]])
+            c = mi.cumsum(0)
+            total = float(c[-1])
+            goal, tok = float(u[i].double()) * total, int(r.tokens[i])
+            err = (_mass_error(V) + 2.0 ** -45) * total * 2
+            assert float(mi[tok]) > 0
+            assert float(c[tok]) > goal - err and float(c[tok] - mi[tok]) <= goal + err
+            lp = np.log(float(mi[tok])) - np.log(total)
+            assert abs(float(r.log_probs[i]) - lp) <= err / total + 2.0 ** -24 * abs(lp) + 1e-12

@@ -15,9 +15,13 @@ namespace wfst {
 // compare: top_k and top_p each cut at one value of it, `last`, found digit by
 // digit (8 bits at a time) from histograms of counts or masses. Masses are
 // binary64 powers rounded to multiples of 2^-unit and added as integers, so no
-// sum depends on the order in which threads add, sums of any two groupings
-// agree, and a draw falls on the exact sums' side of a border except within
-// about 2^-45 of it.
+// sum depends on the order in which threads add, and sums of any two groupings
+// agree. V roundings leave a sum off by at most V 2^-(unit+1) of the largest
+// mass: 2^-41 up to 2048 labels (unit 51), 2^-29 at 131072 (45), 2^-23 at 2^20 (42),
+// for a row all of whose masses are rounded the same way; a draw or a cut next to a
+// border by less than that may fall on its other side. Past 2^20 labels, where V
+// masses of 1 would leave fewer bits still, a row's unit comes from a bound on its
+// own total (row_unit).
 
 namespace {
 
@@ -168,6 +172,32 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane)
 }
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) { return lane_u64(wave_scan_u64(v), 63); }
+
+// The unit of a row of more than kUnitLabels labels, by the WAVES wavefronts of a
+// workgroup: its total is at most `each` (the labels a thread reads) times the sum
+// of the threads' largest masses, and 2^unit times that stays below 2^63. A row
+// with few large masses then gets nearly all bits, and a level one loses no more
+// than the bound exceeds its total: sums are off by at most V each 2^-63 of the
+// total, 2^-23 for 2^24 labels on 256 threads. (By V alone 2^-15.)
+constexpr int kUnitLabels = 1 << 20;
+
+template <int WAVES>
+__device__ __forceinline__ int row_unit(float own, float top, float T, bool greedy, int each, int least, const Exp2Poly &poly,
+                                        unsigned long long *sum)
+{
+    constexpr int kUnit = 50;                        // 1024 masses stay below 2^62
+    const MassOf mass(top, T, 0.0f, kUnit, greedy);
+    const uint64_t w = wave_sum_u64(MassOf::fixed(mass(mass.read(own), poly)) + 1);       // (+ 1: rounded up)
+    if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = w;
+    __syncthreads();
+    uint64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) all += sum[i];
+    __syncthreads();                                 // (sum may be written again)
+    const double bound = (double)all * (double)each;      // < 2^e: the total is below 2^(e - kUnit)
+    const int e = (int)((uint32_t)__double2hiint(bound) >> 20) - 1022;
+    return min(51, max(least, 63 + kUnit - e));
+}
 
 // f(v, scores v .. v + VEC - 1) for the lane's packs of labels v0 .. v1 - 1 of a row
 // of V, a wavefront taking 64 * VEC labels at once: AHEAD packs are loaded before
@@ -327,6 +357,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
 #pragma unroll
             for (int j = 0; j < VEC; ++j) top = fmaxf(top, y[j]);        // (NaN leaves it)
         });
+        const float own = top;
         top = wave_max_f(top);
         if (WAVES > 1) {
             if (lane == 0) red[wave] = top;
@@ -335,7 +366,11 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void k_draw_all(Samp
             for (int w = 0; w < WAVES; ++w) top = fmaxf(top, red[w]);
         }
         const bool greedy = !(T > 0.0f);
-        const MassOf mass(top, T, greedy ? 0.0f : minp, unit, greedy);
+        int bits = unit;
+        if constexpr (WAVES > 1) {
+            if (c.V > kUnitLabels) bits = row_unit<WAVES>(own, top, T, greedy, packs * VEC, unit, poly, s.sum);
+        }
+        const MassOf mass(top, T, greedy ? 0.0f : minp, bits, greedy);
         // Two forms: the tests of the general one, as selects, take half as long again as the sum itself.
         // Without them -inf and NaN have the mass 2^-1000, which rounds to 0. With min_p most labels fail a test
         // of their score and need no mass.
@@ -727,6 +762,9 @@ __device__ __forceinline__ void draw_one(const SampleCall &c, int64_t r, const R
         return;
     }
 
+    if constexpr (WAVES == 16) {
+        if (V > kUnitLabels) unit = row_unit<WAVES>(own, top, row.T, false, seg / 64, unit, poly, s.sum);
+    }
     const MassOf mass(top, row.T, row.minp, unit, false);
     const float high = mass.read(top);                 // the largest score as it is read
     const uint32_t kmax = score_key(high);
