@@ -579,7 +579,8 @@ int wfst_decoder_kernel_times(wfst_decoder_t d, double *out, int32_t n);
  *
  * lengths (device int32 [rows / T], or null): row r = b * T + t holds data iff
  * t < lengths[b]; the other rows are not read and their outputs left as they
- * were. With null every row holds data and T is ignored.
+ * were. With null every row holds data and T is ignored. No output and no
+ * workspace may overlap it.
  */
 
 typedef struct wfst_layer_s *wfst_layer_t;

@@ -929,3 +929,37 @@ def test_sample_longest_rows_against_running_sums(V, sigma):
             assert float(c[tok]) > goal - err and float(c[tok] - mi[tok]) <= goal + err
             lp = np.log(float(mi[tok])) - np.log(total)
             assert abs(float(r.log_probs[i]) - lp) <= err / total + 2.0 ** -24 * abs(lp) + 1e-12
+
+
+def test_outputs_over_lengths_are_refused():
+    """A row's workgroup would read what another one writes."""
+    B, V = 6, 64
+    L = torch.ones(B, dtype=torch.int32, device="cuda")
+    x = torch.randn(B, 1, V, device="cuda")
+    u = torch.rand(B, 1, device="cuda")
+    ok = lambda d: torch.zeros(B, 1, dtype=d, device="cuda")          # noqa: E731
+    over = L.view(B, 1)
+    for out in ((over, ok(torch.float32), ok(torch.int32)), (ok(torch.int32), over.view(torch.float32), ok(torch.int32)),
+                (ok(torch.int32), ok(torch.float32), over)):
+        with pytest.raises(wb.WfstError, match="overlap lengths"):
+            wb.sample(x, u, lengths=L, out=out)
+    buf = torch.ones(B * V + B, dtype=torch.int32, device="cuda")
+    for L in (buf[:B], buf[B * V - 3:B * V - 3 + B]):
+        with pytest.raises(wb.WfstError, match="overlap lengths"):
+            wb.log_softmax(x, lengths=L, out=buf[:B * V].view(torch.float32).view(B, 1, V))
+        layer, _ = _layer_arrays(31, 32, V, 32)
+        with pytest.raises(wb.WfstError, match="overlap lengths"):
+            layer.logits(x[:, :, :32].contiguous(), lengths=L, out=buf[:B * V].view(torch.float32).view(B, 1, V))
+    assert (buf == 1).all()
+    wb.log_softmax(x, lengths=buf[B * V:], out=buf[:B * V].view(torch.float32).view(B, 1, V))     # beside it
+    # workspaces
+    lib = wb.load_library()
+    t, out = torch.randn(2, 90000, device="cuda"), torch.empty(2, 90000, device="cuda")
+    n = np.zeros(1, np.int64)
+    assert lib.wfst_log_softmax_workspace(0, 2, 90000, 0, n.ctypes.data) == 0 and n[0] > 0
+    work = torch.ones(int(n[0]) // 4 + 90000, dtype=torch.int32, device="cuda")
+    for bias, L, word in ((None, work[4:6], b"lengths"), (work[8:], None, b"bias")):
+        assert lib.wfst_log_softmax(t.data_ptr(), 0, 90000, 2, 90000, 1.0, None if bias is None else bias.data_ptr(),
+                                    None if L is None else L.data_ptr(), 1, out.data_ptr(), 0, 90000, work.data_ptr(),
+                                    int(n[0]), None) == -1
+        assert word in lib.wfst_last_error()

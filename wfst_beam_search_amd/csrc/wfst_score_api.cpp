@@ -128,6 +128,14 @@ int check_lengths(const int32_t *lengths, int64_t rows, int32_t T, int device)
     return api_check_buffer(lengths, (size_t)(rows / T) * 4, device, "lengths");
 }
 
+// A range that a call writes (workspaces among them) must leave its lengths alone:
+// other workgroups still read them.
+int check_off_lengths(const void *p, int64_t bytes, const int32_t *lengths, int64_t rows, int32_t T, const char *what)
+{
+    if (!lengths || !p || !bytes || !ranges_meet(p, bytes, lengths, rows / T * 4)) return WFST_OK;
+    return api_fail(WFST_EINVAL, std::string(what) + " must not overlap lengths");
+}
+
 int check_workspace(const void *w, int64_t bytes, size_t need, int device, const void *x, int64_t xb, const void *out,
                     int64_t ob)
 {
@@ -266,7 +274,10 @@ extern "C" int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dt
         TRY(check_lengths(lengths, rows, T, layer->device));
         TRY(check_stream(stream, layer->device));
         if (ranges_meet(x, xb, out, ob)) return api_fail(WFST_EINVAL, "out must not overlap x");
-        TRY(check_workspace(workspace, workspace_bytes, layer_workspace(l, rows, x_dtype), layer->device, x, xb, out, ob));
+        const size_t need = layer_workspace(l, rows, x_dtype);
+        TRY(check_workspace(workspace, workspace_bytes, need, layer->device, x, xb, out, ob));
+        TRY(check_off_lengths(out, ob, lengths, rows, T, "out"));
+        TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
         const LayerCall c{x, out, x_stride, out_stride, rows, x_dtype, out_dtype, {lengths, T}, workspace};
         HIP_TRY(launch_layer(l, c, (hipStream_t)stream));
         return WFST_OK;
@@ -308,8 +319,12 @@ extern "C" int wfst_log_softmax(const void *x, int32_t x_dtype, int64_t x_stride
             return api_fail(WFST_EINVAL, "out must be x itself (same type and stride) or not overlap it");
         if (bias && ranges_meet(bias, (int64_t)V * 4, out, ob))
             return api_fail(WFST_EINVAL, "out must not overlap bias");
-        TRY(check_workspace(workspace, workspace_bytes, norm_workspace(rows, V, x_dtype, out_dtype), device, x, xb, out,
-                            ob));
+        const size_t need = norm_workspace(rows, V, x_dtype, out_dtype);
+        TRY(check_workspace(workspace, workspace_bytes, need, device, x, xb, out, ob));
+        if (need && bias && ranges_meet(workspace, (int64_t)need, bias, (int64_t)V * 4))
+            return api_fail(WFST_EINVAL, "workspace must not overlap bias");
+        TRY(check_off_lengths(out, ob, lengths, rows, T, "out"));
+        TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
         const NormCall c{x, out, bias, x_stride, out_stride, rows, V, x_dtype, out_dtype, scale, {lengths, T}, workspace};
         HIP_TRY(launch_log_softmax(c, (hipStream_t)stream));
         return WFST_OK;
@@ -393,6 +408,9 @@ extern "C" int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int
             for (const auto &a : row_args)
                 if (a.p && ranges_meet(workspace, (int64_t)need, a.p, rb))
                     return api_fail(WFST_EINVAL, std::string("workspace overlaps ") + a.name);
+        for (const auto &o : row_args)
+            if (o.out) TRY(check_off_lengths(o.p, rb, lengths, rows, T, o.name));
+        TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
         SampleCall c{};
         c.x = x;
         c.x_stride = x_stride;
