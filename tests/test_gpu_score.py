@@ -963,3 +963,91 @@ def test_outputs_over_lengths_are_refused():
                                     None if L is None else L.data_ptr(), 1, out.data_ptr(), 0, 90000, work.data_ptr(),
                                     int(n[0]), None) == -1
         assert word in lib.wfst_last_error()
+
+
+# ---------------------------------------------------------------- 64-row products whose operands load straight into LDS
+
+def _many(M, N):
+    """Enough workgroups for 64 rows by 128 features each."""
+    assert M > 32 and -(-N // 128) * -(-M // 64) >= 128, (M, N)
+
+
+@pytest.mark.parametrize("M,K,N,group,x,scale,out,zeros,bias", [
+    # one block of features (one step, half of it clamped), part of one
+    (64, 100, 16400, 128, "f16", "f16", "f32", True, True),
+    (65, 128, 8300, 128, "bf16", "f32", "f16", False, True),
+    (200, 7, 4200, 128, "f16", "f32", "f32", True, False),
+    # odd numbers of blocks, the last one part of a block
+    (70, 385, 8200, 128, "f16", "f32", "f32", True, True),
+    (65, 301, 8333, 256, "bf16", "bf16", "bf16", True, False),
+    (129, 1153, 5600, 384, "f16", "bf16", "f32", False, True),
+    (513, 2049, 2000, 128, "bf16", "f16", "f32", True, True),
+    (1000, 2049, 1100, 128, "f16", "f16", "f16", True, False),
+    # even numbers, whole and not
+    (200, 256, 4100, 128, "f16", "f16", "f32", False, False),
+    (2000, 500, 500, 128, "bf16", "f32", "f32", True, True),
+    (2000, 1024, 500, 1024, "f16", "f32", "bf16", False, True),
+    (100, 3840, 8209, 128, "f16", "bf16", "f32", True, True),
+])
+def test_layer_direct_loads(M, K, N, group, x, scale, out, zeros, bias):
+    _say("direct", M, K, N, group, x, scale, out)
+    _many(M, N)
+    assert group % 128 == 0 and x != "f32"
+    layer, arrays = _layer_arrays(M + K + N, K, N, group, scale, zeros, bias)
+    h = torch.from_numpy(np.random.default_rng(K).normal(size=(M, K + 3)).astype(np.float32)).to(DT[x]).cuda()[:, 1:K + 1]
+    y = layer.logits(h, dtype=out)
+    _layer_check(y, h.contiguous(), arrays, out)
+    for _ in range(3):
+        assert torch.equal(layer.logits(h, dtype=out), y)
+
+
+@pytest.mark.parametrize("x", ["f16", "bf16"])
+@pytest.mark.parametrize("K", [100, 385, 1280])
+def test_layer_direct_loads_lengths(x, K):
+    """A padded batch: rows behind the last frame hold NaN and are not read, their outputs stay."""
+    B, T, N = 7, 90, 1700
+    layer, arrays = _layer_arrays(K, K, N, 128, zeros=True, bias=True)
+    _many(B * T, N)
+    h = torch.randn(B, T, K, device="cuda").to(DT[x])
+    L = torch.tensor([90, 0, 1, 64, 63, 17, 89], dtype=torch.int32, device="cuda")
+    act = torch.arange(T, device="cuda")[None] < L[:, None]
+    h[~act] = float("nan")
+    out = torch.full((B, T, N), 5.0, device="cuda")
+    layer.logits(h, lengths=L, out=out)
+    assert (out[~act] == 5).all()
+    _layer_check(out[act], h[act], arrays, "f32")
+
+
+@pytest.mark.parametrize("x", ["f16", "bf16", "f32"])
+def test_workspaces_on_side_streams(x):
+    """Layer, log-softmax and draw, all with a workspace, on two streams at once and in turn with work on the current one."""
+    K, V, R = 200, 70003, 20
+    layer, _ = _layer_arrays(33, K, V, 128, zeros=True, bias=True)
+    for rows, code in ((R, "layer"), (R, "norm"), (R, "draw")):
+        n = np.zeros(1, np.int64)
+        lib = wb.load_library()
+        dt = {"f32": 0, "f16": 1, "bf16": 2}[x]
+        rc = {"layer": lambda: lib.wfst_layer_workspace(layer.handle, dt, rows, n.ctypes.data),
+              "norm": lambda: lib.wfst_log_softmax_workspace(0, rows, V, 1, n.ctypes.data),
+              "draw": lambda: lib.wfst_sample_workspace(1, rows, V, n.ctypes.data)}[code]()
+        assert rc == 0 and n[0] > 0, code
+    hs = [torch.randn(R, K, device="cuda").to(DT[x]) for _ in range(2)]
+    u = torch.rand(R, device="cuda")
+
+    def step(h, stream=None):
+        lp = layer.log_probs(h, dtype="f16", stream=stream)
+        return lp, wb.sample(lp, u, top_k=40, top_p=0.9, stream=stream), wb.sample(lp, u, stream=stream)
+
+    want = [step(h) for h in hs]
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for turn in range(4):
+        got = [step(h, s) for h, s in zip(hs, side)]
+        here = step(hs[turn % 2])
+        junk = [torch.full((R, V), 3.0, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        del junk
+        for a, b in zip(got + [here], want + [want[turn % 2]]):
+            assert torch.equal(a[0], b[0])
+            for p, q in zip(a[1:], b[1:]):
+                assert all(torch.equal(i, j) for i, j in zip(p, q))
