@@ -231,3 +231,12 @@ def test_hidden_lengths_are_checked_as_given():
     for bad in (np.array([2 ** 32 + 1, 0]), [-2 ** 32 + 1, 0], [8, 0]):
         with pytest.raises(ValueError, match="lengths"):
             dec._log_probs(Layer, torch.zeros(2, 7, 3), bad, 1.0, None, None)
+
+
+def test_build_jobs_from_any_environment(monkeypatch):
+    from wfst_beam_search_amd import build as hip_build
+    for given, jobs in (("", 4), ("auto", 4), ("0", 1), ("2", 2), ("16", 4), (" 3 ", 3), ("-1", 4)):
+        monkeypatch.setenv("MAX_JOBS", given)
+        assert hip_build._jobs() == jobs
+    monkeypatch.delenv("MAX_JOBS")
+    assert hip_build._jobs() == 4

@@ -41,13 +41,18 @@ def _run(cmd, verbose: bool) -> None:
     subprocess.check_call(cmd)
 
 
+def _jobs() -> int:
+    """Compilers at once: MAX_JOBS where it is a number, at most 4."""
+    given = os.environ.get("MAX_JOBS", "").strip()
+    return max(1, min(4, int(given))) if given.isdigit() else 4
+
+
 def _compile(out: str, sources, verbose: bool) -> None:
     """Each source to an object of its own, several at once, then one shared library."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    jobs = max(1, min(4, int(os.environ.get("MAX_JOBS", "4"))))
     with tempfile.TemporaryDirectory(prefix="wfst_build_") as tmpdir:
         objs = [os.path.join(tmpdir, f"{i}.o") for i in range(len(sources))]
-        with ThreadPoolExecutor(jobs) as pool:
+        with ThreadPoolExecutor(_jobs()) as pool:
             list(pool.map(lambda so: _run([hipcc, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I",
                                            os.path.join(HERE, "csrc"), "-c", "-o", so[1], so[0]], verbose),
                           zip(sources, objs)))
