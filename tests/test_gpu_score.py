@@ -1051,3 +1051,19 @@ def test_workspaces_on_side_streams(x):
             assert torch.equal(a[0], b[0])
             for p, q in zip(a[1:], b[1:]):
                 assert all(torch.equal(i, j) for i, j in zip(p, q))
+
+
+def test_overwriting_a_saved_tensor_stops_its_backward():
+    layer, _ = _layer_arrays(35, 8, 64, 32)
+    h, u = torch.randn(3, 8, device="cuda"), torch.rand(3, device="cuda")
+    tok = torch.empty(3, dtype=torch.int32, device="cuda")
+    for write in (lambda t: wb.log_softmax(t, out=t), lambda t: layer.logits(h, out=t), lambda t: layer.log_probs(h, out=t)):
+        x = torch.randn(3, 64, device="cuda", requires_grad=True)
+        y = x.exp()
+        write(y.detach())
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.sum().backward()
+    saved = torch.rand(3, device="cuda", requires_grad=True).exp()
+    wb.sample(h, u, out=(tok, saved.detach(), tok.clone()))
+    with pytest.raises(RuntimeError, match="inplace"):
+        saved.sum().backward()

@@ -240,3 +240,15 @@ def test_build_jobs_from_any_environment(monkeypatch):
         assert hip_build._jobs() == jobs
     monkeypatch.delenv("MAX_JOBS")
     assert hip_build._jobs() == 4
+
+
+def test_writing_to_out_is_known_to_autograd(no_gpu_checks):
+    """out may share its memory with a tensor that a backward pass has saved."""
+    x = torch.randn(2, 3, requires_grad=True)
+    y = x.exp()                                     # saved for its own gradient
+    out = score._out(y.detach(), (2, 3), torch.float32, x.device, None)
+    assert out._version == 1
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    with torch.inference_mode():
+        assert score._out(torch.zeros(2, 3), (2, 3), torch.float32, x.device, None).shape == (2, 3)

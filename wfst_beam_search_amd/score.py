@@ -167,11 +167,13 @@ def _lengths(lengths, shape, device, other):
 
 
 def _out(out, shape, dtype, device, other):
+    import torch
     if out is None:
         return _new(shape, dtype, device, other)
     _gpu(out, "out", device)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)}")
+    torch.autograd.graph.increment_version(out)     # (a backward pass that saved it says so instead of using it)
     return out
 
 
