@@ -243,7 +243,7 @@ hipError_t norm_launch(const NormCall &c, hipStream_t s)
     constexpr int VEC = pack_len<XT, OT>();
     constexpr int kLane = kWaveSize * VEC;      // elements of one pack a lane
     const auto grid = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, kMaxRowGrid)); };
-    const int pieces = norm_pieces(c.rows, c.V, c.x_dtype, c.out_dtype);
+    const int pieces = norm_pieces(c.V, c.x_dtype, c.out_dtype);
     if (pieces > 0) {
         const dim3 g = grid(c.rows * pieces), b(kPieceWaves * kWaveSize);
         hipLaunchKernelGGL((k_norm_piece<XT, OT, false>), g, b, 0, s, c, pieces);
@@ -273,7 +273,7 @@ hipError_t norm_ot(const NormCall &c, hipStream_t s)
 // Pieces a row is cut into, 0 for rows that 16 wavefronts hold: whole rows are
 // faster there however few they are (1, 64, 256 rows of 32768 binary32 labels, whole /
 // in pieces: 9 / 14, 9 / 14, 15 / 21 us).
-int norm_pieces(int64_t, int32_t V, int32_t x_dtype, int32_t out_dtype)
+int norm_pieces(int32_t V, int32_t x_dtype, int32_t out_dtype)
 {
     const int vec = 16 / (int)std::max(dtype_size(x_dtype), dtype_size(out_dtype));
     const int span = kPieceWaves * kWaveSize * vec * kPieceNV;
@@ -283,7 +283,7 @@ int norm_pieces(int64_t, int32_t V, int32_t x_dtype, int32_t out_dtype)
 
 size_t norm_workspace(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype)
 {
-    return (size_t)rows * (size_t)norm_pieces(rows, V, x_dtype, out_dtype) * sizeof(NormStat);
+    return (size_t)rows * (size_t)norm_pieces(V, x_dtype, out_dtype) * sizeof(NormStat);
 }
 
 hipError_t launch_log_softmax(const NormCall &c, hipStream_t s)

@@ -610,7 +610,6 @@ __device__ __forceinline__ bool draw_list(const SampleCall &c, int64_t r, const 
     for (int rule = 0; rule < 3; ++rule) {
         if (rule == 0 ? !row.cut_k : rule == 1 ? !row.cut_p : false) continue;
         if (rule == 2) {
-            // (by selects: the compiler has been seen to lose stores to such arrays under divergent branches)
             if (mass.lim > 0.0) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) {

@@ -1,6 +1,7 @@
 // Shared by the host entry points (wfst_score_api.cpp) and the gfx950 kernels
-// (wfst_score.hip) of the operators around the search: the output layer with
-// 4-bit weights, the log-softmax and the draw of tokens. Not part of the ABI.
+// (wfst_layer.hip, wfst_norm.hip, wfst_sample.hip) of the operators around the
+// search: the output layer with 4-bit weights, the log-softmax and the draw of
+// tokens. Not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -85,7 +86,7 @@ struct NormCall {
     void *workspace;            // norm_workspace bytes
 };
 
-int norm_pieces(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype);
+int norm_pieces(int32_t V, int32_t x_dtype, int32_t out_dtype);
 size_t norm_workspace(int64_t rows, int32_t V, int32_t x_dtype, int32_t out_dtype);
 hipError_t launch_log_softmax(const NormCall &c, hipStream_t s);
 

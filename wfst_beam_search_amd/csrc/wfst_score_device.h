@@ -59,14 +59,6 @@ __device__ __forceinline__ float wave_sum_f(float v)
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum_t(T v)
-{
-#pragma unroll
-    for (int d = kWaveSize / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d, kWaveSize);
-    return v;
-}
-
 }  // namespace
 
 }  // namespace wfst
