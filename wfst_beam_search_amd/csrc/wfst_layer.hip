@@ -21,11 +21,14 @@ namespace {
 // by a power of two per 128 features so that the block's largest finite value
 // lies in [2^14, 2^15): a bfloat16 value then fits binary16 exactly or, 2^30
 // below the block's largest, loses less than 2^-39 of that. A binary32 value is
-// cut into hi + lo / 2^11, two binary16 values, and lo meets weights divided by
-// 2^11 (exact, and both sums stay one): off by at most 2^-23 of itself, or 2^-50
-// of the block's largest. Without the 2^11 lo would end at binary16's smallest
-// number, 2^-39 of the block's largest: 16 bits of 0.01 beside 1e5. Exact values
-// would take a third part, a product more of two.
+// cut into hi + lo / 2^11, two binary16 values: off by at most 2^-23 of itself, or
+// 2^-50 of the block's largest. Without the 2^11 lo would end at binary16's smallest
+// number, 2^-39 of the block's largest: 16 bits of 0.01 beside 1e5. lo meets
+// weights divided by 2^11 (exact), so the sum stays one, or (few rows, one scale a
+// tile) has a sum of its own: one row x 131072 x 4096 of binary32, groups of 128, divided
+// weights / own sum 75 / 68 us, groups of 64 79 / 78, groups of 32 88 / 99; for many
+// rows the sums would pass the registers. Exact values would take a third part, half
+// as many products again.
 
 constexpr int kLayerWaves = 4;
 constexpr int kLayerThreads = kLayerWaves * kWaveSize;
@@ -145,12 +148,6 @@ __device__ __forceinline__ half8_t unpack_word(uint32_t w, uint32_t magic, const
     return q.v;
 }
 
-// The weights that meet a binary32 value's second part.
-__device__ __forceinline__ half8_t part_weights(const half8_t &q, int part)
-{
-    return part ? q * (_Float16)(1.0f / 2048.0f) : q;
-}
-
 // 1024 in both halves, in a vector register that the compiler does not fold: a
 // mask and this then combine in one instruction.
 __device__ __forceinline__ uint32_t magic_1024()
@@ -187,6 +184,7 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
 {
     constexpr int P = kParts<XT>;
     constexpr int D = kTilesAhead<KS, SPL>;
+    constexpr bool kLow = P == 2 && GPT == 1;                           // second parts have a sum of their own
     extern __shared__ __align__(16) char smem[];
     half8_t *xs = (half8_t *)smem;                                      // [P][KS * kc * 16][RP]
     const int part = KS * kc * 16 * RP;
@@ -267,24 +265,26 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
                 sq[i] = load_tile_scale<WS, GPT>(l, nx * kTileN + col);
                 const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
                 const int u = slice * kc + t + i - c0;
-                float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f}, tile = sum;
+                float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f}, low = sum, tile = sum;       // (low: of the second parts)
                 ZeroPair z = zero_pair(ts.z & 255u);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (j && j % (4 / GPT) == 0) z = zero_pair((ts.z >> (8 * (j * GPT / 4))) & 255u);
                     const half8_t q = unpack_word(w[j], magic, z);
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[p * part + (u * 16 + j * 4 + quad) * RP + arow],
-                                                                     part_weights(q, p), sum, 0, 0, 0);
+const int at = (u * 16 + j * 4 + quad) * RP + arow;
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[at], q, sum, 0, 0, 0);
+                    if constexpr (kLow) low = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[part + at], q, low, 0, 0, 0);
+                    else if constexpr (P == 2)
+                        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[part + at], q * (_Float16)(1.0f / 2048.0f), sum, 0, 0, 0);
                     if ((j + 1) % (4 / GPT) == 0) {
                         const float s = scale_of<WS, GPT>(ts, j * GPT / 4, bf16s);
 #pragma unroll
                         for (int q4 = 0; q4 < 4; ++q4) {
+                            if (kLow) sum[q4] = fmaf(low[q4], 1.0f / 2048.0f, sum[q4]);
                             if (!kScaled<XT>) acc[q4] = fmaf(sum[q4], s, acc[q4]);
                             else if (j < 4 / GPT) tile[q4] = sum[q4] * s;
                             else tile[q4] = fmaf(sum[q4], s, tile[q4]);
-                            sum[q4] = 0.0f;
+                            sum[q4] = low[q4] = 0.0f;
                         }
                     }
                 }
@@ -473,7 +473,7 @@ __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const 
                 for (int p = 0; p < P; ++p) {
                     if (p) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) q[n] = part_weights(q[n], p);
+                        for (int n = 0; n < NT; ++n) q[n] *= (_Float16)(1.0f / 2048.0f);       // (as the second part is held)
                     }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
