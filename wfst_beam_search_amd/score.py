@@ -43,6 +43,8 @@ class _SampleConfig(ctypes.Structure):
 
 _codes = None          # torch dtype -> element type code
 _names = None          # "f32" ... -> torch dtype
+_fw = None             # torch.autograd.forward_ad
+_bump = None           # torch.autograd.graph.increment_version
 
 
 def _types():
@@ -80,13 +82,15 @@ def _int32(v, what):
 
 
 def _gpu(t, what, device=None):
+    global _fw
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a torch tensor on the GPU")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{what} requires a gradient, which these operators do not have (detach it, or use no_grad)")
-    fw = torch.autograd.forward_ad
-    if fw._current_level >= 0 and torch._C._is_fwd_grad_enabled() and fw.unpack_dual(t).tangent is not None:
+    if _fw is None:
+        _fw = torch.autograd.forward_ad
+    if _fw._current_level >= 0 and torch._C._is_fwd_grad_enabled() and _fw.unpack_dual(t).tangent is not None:
         raise ValueError(f"{what} carries a forward-mode tangent, which these operators do not have (detach it)")
     if device is not None and t.device != device:
         raise ValueError(f"{what} must be on {device}")
@@ -143,9 +147,9 @@ def _new(shape, dtype, device, other):
 
 def _lengths(lengths, shape, device, other):
     """(device int32 tensor or None, T) for a batch of rows of the given leading shape."""
-    import torch
     if lengths is None:
         return None, 1
+    import torch
     if len(shape) != 2:
         raise ValueError("lengths need a tensor [B, T, ...]")
     if isinstance(lengths, torch.Tensor) and lengths.is_cuda:
@@ -166,21 +170,34 @@ def _lengths(lengths, shape, device, other):
     return lengths, _int32(shape[1], "T")
 
 
+def _written(outs):
+    """Tensors that the call overwrites: a backward pass that saved one says so instead of using it."""
+    global _bump
+    if _bump is None:
+        import torch
+        _bump = torch.autograd.graph.increment_version
+    _bump(outs)
+
+
+def _checked(out, shape, dtype, device):
+    _gpu(out, "out", device)
+    if out.dtype != dtype or out.shape != shape:
+        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)}")
+    return out
+
+
 def _out(out, shape, dtype, device, other):
-    import torch
     if out is None:
         return _new(shape, dtype, device, other)
-    _gpu(out, "out", device)
-    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)}")
-    torch.autograd.graph.increment_version(out)     # (a backward pass that saved it says so instead of using it)
+    _checked(out, shape, dtype, device)
+    _written((out,))
     return out
 
 
 def _workspace(nbytes, device, other):
-    import torch
     if nbytes <= 0:
         return None
+    import torch
     return _new(nbytes, torch.uint8, device, other)
 
 
@@ -381,8 +398,9 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
     else:
         res = SampleResult(*out)
         for o, dt in zip(res, (torch.int32, torch.float32, torch.int32)):
-            if o is None or not _out(o, shape, dt, device, other).is_contiguous():
+            if o is None or not _checked(o, shape, dt, device).is_contiguous():
                 raise ValueError("out must be three packed tensors (int32, float32, int32)")
+        _written(res)
     k = max(-1, min(int(k), V))                 # (V and more: all)
     cfg = _SampleConfig(float(t), k, float(p), float(mp), _p(ts), _p(ks), _p(ps), _p(mps))
     need = _sample_bytes(code, rows, V)
