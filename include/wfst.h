@@ -629,7 +629,8 @@ int wfst_layer_release(wfst_layer_t layer);   /* null is a no-op */
  * 2^30 times smaller than it may be off by 2^-39 of it; a binary32 x enters as two
  * binary16 values, off by at most 2^-23 of x or 2^-50 of that largest. Infinities
  * and NaN in x go where the formula takes them.
- * out must not overlap x. workspace: device memory, 16-byte aligned, of at least
+ * out must not overlap x (nor reach between its rows: ranges from a tensor's first
+ * to its last element count). workspace: device memory, 16-byte aligned, of at least
  * wfst_layer_workspace's bytes (null when those are 0), in use until the stream
  * has passed the call. Errors: WFST_EINVAL, WFST_EDEVICE.
  */
@@ -644,7 +645,8 @@ int wfst_layer_workspace(wfst_layer_t layer, int32_t x_dtype, int32_t rows, int6
  * blank penalty, -inf for a label that may not be emitted). V in [1, 2^24]; bias
  * is a device float [V] or null. Statistics are binary32. A row whose entries
  * are all -inf stays -inf; a row with a NaN or +inf becomes NaN. out may be x
- * itself (same element type and stride), otherwise it must not overlap x.
+ * itself (same element type and stride), otherwise it must not overlap x (ranges from
+ * first to last element count).
  * workspace: device memory, 16-byte aligned, of at least wfst_log_softmax_workspace's bytes (null
  * when those are 0), in use until the stream has passed the call.
  * Errors: WFST_EINVAL, WFST_EDEVICE.

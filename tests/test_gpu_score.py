@@ -1067,3 +1067,26 @@ def test_overwriting_a_saved_tensor_stops_its_backward():
     wb.sample(h, u, out=(tok, saved.detach(), tok.clone()))
     with pytest.raises(RuntimeError, match="inplace"):
         saved.sum().backward()
+
+
+def test_sample_masks_and_specials_of_longest_rows():
+    """Past 2^20 labels, where a row's unit comes from its own masses: empty, masked, infinite, NaN and greedy rows."""
+    V, inf = (1 << 20) + 9, float("inf")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    t = torch.randn(9, V, generator=g, device="cuda") * 4
+    t[0] = -inf
+    t[1] = float("nan")
+    t[2] = -inf
+    t[2, V - 1] = 1.0
+    t[3, 1], t[3, V - 2], t[3, 700000] = inf, inf, inf
+    t[4, ::3] = float("nan")
+    t[5] = torch.finfo(torch.float32).min
+    t[6, 1000:] = -inf
+    t[7, 5] = 3e38
+    u = torch.rand(9, generator=g, device="cuda")
+    T = torch.tensor([1.0, 1, 1, 1, 0.7, inf, 2, 1, 0], device="cuda")
+    for s in (dict(), dict(temperature=T), dict(temperature=0.0), dict(min_p=0.3), dict(top_k=30, top_p=0.9),
+              dict(top_k=torch.tensor([0, 3, 0, 2, 90, 0, 2000, 0, 7], dtype=torch.int32, device="cuda"), temperature=T,
+                   top_p=torch.tensor([1, 0.5, 0.5, 1, 0.8, 1, 0.9, 0.5, 0.1], device="cuda"))):
+        _say("longest specials", {k: type(v).__name__ for k, v in s.items()})
+        _sample_check(wb.sample(t, u, **s), t, u, **s)

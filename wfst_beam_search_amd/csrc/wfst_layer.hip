@@ -173,10 +173,10 @@ __device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, fl
 // features and walks all of K. KS = 4: the four wavefronts of a workgroup own
 // the same 16 features and a quarter of K each, joined in LDS at the end.
 // Weights stream D tiles ahead of their use. SPL = 1 (at most 4 rows, whose staging
-// takes one run of 8 features a thread) leaves registers for 8 wavefronts a SIMD:
-// one row x 131072 x 4096 takes 59 us with 3 tiles ahead (62, 61, 71 with 4, 2, 6),
-// where the general staging's registers leave 5 and it takes 74; 278 MB at 4.7 TB/s,
-// 92 % of what a large copy moves on this card.
+// takes one run of 8 features a thread) leaves registers for 4 wavefronts a SIMD (118
+// of bfloat16): one row x 131072 x 4096 takes 59 us with 3 tiles ahead (62, 61, 71
+// with 4, 2, 6), where the general staging's (174) leave 2 and it takes 74; 278 MB at
+// 4.7 TB/s, 92 % of what a large copy moves on this card.
 template <int KS, int SPL> constexpr int kTilesAhead = KS == 1 ? (SPL == 1 ? 3 : 4) : 2;
 
 template <typename XT, int WS, int GPT, int KS, int SPL>
@@ -362,10 +362,10 @@ __global__ __launch_bounds__(256) void k_layer_operands(Layer l, LayerCall c, ha
 // read from LDS between two weight tiles. Operands of the next step are loaded
 // into registers during a step and stored into the other LDS buffer after it, or
 // (64 rows, one part, one scale a tile) loaded into that buffer directly, which
-// frees the matrix instructions of the stores: 4096 x 131072 x 4096 binary16 8.3 -> 6.4
-// ms (690 TFLOP/s), bfloat16 9.4 -> 8.8; with two parts, smaller groups or fewer rows
-// the wait for the loads costs more (binary32 13.1 -> 13.5, groups of 32 1.49 -> 1.54 at
-// 32003 x 2050, 32 rows 82 -> 88 us).
+// frees the matrix instructions of the stores: 4096 x 131072 x 4096 binary16 8.3 -> 6.5
+// ms (670 TFLOP/s), bfloat16 9.4 -> 8.6; with two parts, smaller groups or fewer rows
+// the wait for the loads costs more (binary32 3 % of its 12.8 ms, groups of 32 3 %, 32
+// rows 7 %).
 template <typename XT, int WS, int GPT, int MT>
 __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf)
 {
@@ -610,8 +610,12 @@ hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
 }
 
 // Few tiles of features: K over the wavefronts of a workgroup, to have enough of
-// them (one row, one / four wavefronts a tile: 1000 tiles x 4096 15 / 13 us, 1000 x 1024
-// 7.5 / 8.4, 2001 x 2050 13 / 16, 4096 x 4096 31 / 41).
+// them. One row of bfloat16, one / four wavefronts a tile, us, K = 512, 1024, 2050, 4096:
+//  250 tiles 4.5 / 4.0, 5.7 / 4.5, 9.3 / 6.8, 13.4 / 7.9
+// 1000 tiles 4.6 / 5.0, 5.9 / 5.9, 9.5 / 9.0, 15.3 / 12.5
+// 1500 tiles 5.1 / 6.4, 6.8 / 7.6, 11.4 / 12.9, 18.5 / 18.0
+// 2001 tiles 5.2 / 7.4, 6.9 / 8.9, 12.5 / 15.8, 19.2 / 21.1
+// The border lies lower the smaller K is; one for all K gives up 1.3 us at 1500 x 512.
 template <typename XT, int WS, int GPT>
 hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
 {
@@ -627,7 +631,11 @@ hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
 // only (17000 x 1024, 16 rows: few 12 .. 23 us, many 14); above, from 3 rows of
 // bfloat16 or binary32 on and from 5 of binary16, whose staging is a copy (32003 x
 // 2050, few / many: 2 rows 18 / 18, 20 / 20, 13 / 18 us; 4 rows 22 / 19, 34 / 20, 15 / 19;
-// 8 rows 42 / 19, 44 / 20, 28 / 19).
+// 8 rows 42 / 19, 44 / 20, 28 / 19). By workgroups, bfloat16, few / many: 4 (64 x 500 x
+// 512) 5 / 14, 40 (64 x 5000 x 1024) 14 / 18, 63 (64 x 8000 x 2048) 33 / 26, 64 (1024 x
+// 500 x 512) 14 / 15, 80 (128 x 5000 x 1024) 25 / 19, 94 (64 x 12000 x 1024) 29 / 18, 160
+// (256 x 5000 x 1024) 46 / 19: 128 keeps every size where few is faster, and between
+// 60 and 128 some where many would be.
 int many_tiles(const Layer &l, int32_t rows, int32_t x_dtype)
 {
     const bool large = (int64_t)l.nt * l.kb >= 16384;

@@ -1393,6 +1393,11 @@ hipError_t sample_xt(const SampleCall &c, hipStream_t s)
 // one row 34 / 19 us without cuts, 24 / 21 with top_k 50, 60 / 28 with top_p 0.9 (67 /
 // 85 where the nucleus outgrows the lists); 32 rows 34 / 20, 24 / 24, 61 / 36; 64 rows
 // 35 / 25, 24 / 30, 60 / 44; 32003 binary32 labels, one row 14 / 19, 18 / 19, 29 / 26.
+// Next to the border, 70003 binary32 labels, whole / in chunks: one row 26 / 12 without
+// cuts, 21 / 18 with top_k 50, 41 / 25 with top_p 0.9, 19 / 20 with min_p 0.05, 18 / 15
+// greedy; 32 rows 27 / 16, 22 / 22, 44 / 31, 20 / 25, 18 / 17. By shape alone, so that the
+// workspace does not depend on settings that live on the device: rows with min_p alone
+// (131072 bfloat16, 32 rows 22 / 28) and nuclei that outgrow the lists pay for it.
 int sample_chunks(int64_t rows, int32_t V, int32_t x_dtype)
 {
     const int chunk = kChunkThreads * kChunkPacks * (16 / (int)dtype_size(x_dtype));
