@@ -371,7 +371,7 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
     """Draw one token of each row of ``scores`` [..., V] (logits or
     log-probabilities) with the uniform random numbers ``u`` (float32 [...], in
     [0, 1)). The rules apply in this order, ties to the lowest index: temperature
-    (0: the largest score), top_k largest (0: all), the fewest of these whose mass
+    (0: the largest score), top_k largest (0, or V and more: all), the fewest of these whose mass
     reaches top_p of theirs, of these the ones with at least min_p of the largest
     one's mass. Each setting is a number or a tensor [...] on the GPU (float32;
     top_k int32). ``out``: tensors (tokens, log_probs, kept) to write to."""
