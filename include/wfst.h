@@ -569,8 +569,8 @@ int wfst_decoder_kernel_times(wfst_decoder_t d, double *out, int32_t n);
  * asynchronous: it is ordered on the caller's HIP stream (null: the null stream
  * of the operands' device) and returns without waiting for it, so operands must
  * stay valid until the stream has passed it. None allocates device memory or
- * synchronises (but wfst_layer_create / _release), so they may be captured into
- * a HIP graph, which then reads and writes the same buffers at every replay.
+ * synchronises (but wfst_layer_create / _release and wfst_adapters_create /
+ * _release), so they may be captured into a HIP graph, which then reads and writes the same buffers at every replay.
  * Calls on different streams run at once (a workspace serves one call at a time). Element types
  * are WFST_LP_F32, _F16 and _BF16; a result is rounded to its type once, to
  * nearest even. Tensors are rows `stride` elements apart (stride >= the row's
@@ -638,6 +638,59 @@ int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_
                       const int32_t *lengths, int32_t T, void *out, int32_t out_dtype, int64_t out_stride,
                       void *workspace, int64_t workspace_bytes, void *stream);
 int wfst_layer_workspace(wfst_layer_t layer, int32_t x_dtype, int32_t rows, int64_t *bytes);
+
+typedef struct wfst_adapters_s *wfst_adapters_t;
+
+/*
+ * Low-rank adapters beside layers of one size (out_features N, in_features K):
+ * `slots` places in [1, 2^16], each empty or holding two matrices down [r, K] and
+ * up [N, r] of element type `dtype`, of a rank r of its own up to `rank` (in [1,
+ * 128]), and a scale.
+ */
+typedef struct wfst_adapters_desc {
+    int32_t in_features;
+    int32_t out_features;
+    int32_t slots;
+    int32_t rank;
+    int32_t dtype;
+} wfst_adapters_desc;
+
+/*
+ * Memory for the slots on `device` (slots * (K + N) * rank elements, rank rounded up
+ * to 16, K to 32, N to 16), all empty. Ordered on `stream`, which it synchronises.
+ * Release with wfst_adapters_release, which waits for the device; graphs that
+ * captured the adapters must not be replayed after it.
+ * Errors: WFST_EINVAL, WFST_ENOMEM, WFST_EDEVICE.
+ */
+int wfst_adapters_create(const wfst_adapters_desc *d, int device, void *stream, wfst_adapters_t *out);
+int wfst_adapters_release(wfst_adapters_t adapters);   /* null is a no-op */
+
+/*
+ * Fill a slot with a copy of down (rows down_stride elements apart) and up (rows
+ * up_stride apart), or empty it (rank 0; the matrices are then ignored).
+ * Asynchronous on `stream`: calls that use the slot have to be ordered before or
+ * after it by the caller; other slots are left alone. A captured call reads what
+ * the slots hold at its replay. scale is finite. Errors: WFST_EINVAL, WFST_EDEVICE.
+ */
+int wfst_adapters_load(wfst_adapters_t adapters, int32_t slot, int32_t rank, const void *down, int64_t down_stride,
+                       const void *up, int64_t up_stride, float scale, void *stream);
+
+/*
+ * wfst_layer_logits with an adapter for each row:
+ *   out[r, n] = y[r, n] + sum_j up[n, j] * h[r, j],   h[r, j] = scale * sum_k down[j, k] * x[r, k]
+ * of slot ids[r / rows_per_id] (device int32 [rows / rows_per_id]); an id outside
+ * [0, slots) or of an empty slot is none: such rows hold the layer's y. x, down and
+ * up count with all their bits; h and the sums are binary32, and out is rounded once.
+ * Rows take nothing from each other's adapters, infinities and NaN included. out and
+ * the workspace (wfst_layer_adapted_workspace's bytes) must not overlap ids; all
+ * else is as for wfst_layer_logits.
+ */
+int wfst_layer_adapted_logits(wfst_layer_t layer, wfst_adapters_t adapters, const int32_t *ids, int32_t rows_per_id,
+                              const void *x, int32_t x_dtype, int64_t x_stride, int32_t rows, const int32_t *lengths,
+                              int32_t T, void *out, int32_t out_dtype, int64_t out_stride, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+int wfst_layer_adapted_workspace(wfst_layer_t layer, wfst_adapters_t adapters, int32_t x_dtype, int32_t rows,
+                                 int64_t *bytes);
 
 /*
  * out[r, :] = log_softmax(scale * x[r, :] + bias): the search's log_prob rows
@@ -707,6 +760,53 @@ int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, 
                 const wfst_sample_config *cfg, const int32_t *lengths, int32_t T, int32_t *out_tokens,
                 float *out_log_probs, int32_t *out_kept, void *workspace, int64_t workspace_bytes, void *stream);
 int wfst_sample_workspace(int32_t x_dtype, int64_t rows, int32_t V, int64_t *bytes);
+
+/*
+ * Outputs of wfst_token_scores, device arrays (null: not wanted; log_probs and
+ * ranks are given together where tokens_per_row > 0, top_tokens and top_log_probs
+ * where top_n > 0):
+ *  log_probs      float [rows, tokens_per_row]
+ *  ranks          int32 [rows, tokens_per_row]
+ *  entropies      float [rows]
+ *  top_tokens     int32 [rows, top_n]
+ *  top_log_probs  float [rows, top_n]
+ */
+typedef struct wfst_token_scores_out {
+    void *log_probs;
+    void *ranks;
+    void *entropies;
+    void *top_tokens;
+    void *top_log_probs;
+} wfst_token_scores_out;
+
+/*
+ * Scores of given tokens under softmax(x[r, :] / T), over all V labels (no label
+ * is cut, unlike a draw's):
+ *  log_probs  (x[tok] - max) / T - log sum exp((x - max) / T) of each given token
+ *             (tokens: device int32 [rows, tokens_per_row], 0 to 256 of them a row;
+ *             one outside [0, V) has log-probability -inf and rank -1).
+ *  ranks      labels before the token: those with a larger score, or with the same
+ *             one and a lower index (0: the largest). NaN counts as -inf here.
+ *  entropies  - sum p log p.
+ *  top_tokens, top_log_probs  the top_n (0 to 64) largest scores in this order, ties
+ *             to the lowest index. Labels with score -inf or NaN are not listed;
+ *             places left over hold -1 and -inf.
+ * T: `temperature`, >= 0 and finite, or temperatures[r] (device float [rows]; a
+ * value that is not > 0 is 0, +inf the largest finite number). 0 leaves all mass to
+ * the largest score: log-probability 0 there, -inf elsewhere, entropy 0. Order
+ * never depends on T. A row of -inf alone has log-probabilities -inf and entropy 0;
+ * in a row with a NaN or +inf every log-probability and the entropy are NaN.
+ * Statistics are binary32. V in [1, 2^24]. Outputs must not overlap each other or
+ * an input. workspace: device memory, 16-byte aligned, of at least
+ * wfst_token_scores_workspace's bytes (null when those are 0), in use until the
+ * stream has passed the call. Errors: WFST_EINVAL, WFST_EDEVICE.
+ */
+int wfst_token_scores(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V, const int32_t *tokens,
+                      int32_t tokens_per_row, int32_t top_n, float temperature, const float *temperatures,
+                      const int32_t *lengths, int32_t T, const wfst_token_scores_out *out, void *workspace,
+                      int64_t workspace_bytes, void *stream);
+int wfst_token_scores_workspace(int32_t x_dtype, int64_t rows, int32_t V, int32_t tokens_per_row, int32_t top_n,
+                                int64_t *bytes);
 
 #ifdef __cplusplus
 }

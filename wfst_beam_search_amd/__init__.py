@@ -18,7 +18,8 @@ from types import SimpleNamespace
 import numpy as np
 
 __all__ = ["Graph", "Decoder", "DecodeResult", "WfstError", "library_path", "load_library", "decode_noalloc",
-           "EXPORTED_SYMBOLS", "LP_F32", "LP_F16", "OutputLayer", "log_softmax", "sample", "SampleResult"]
+           "EXPORTED_SYMBOLS", "LP_F32", "LP_F16", "OutputLayer", "Adapters", "log_softmax", "sample", "SampleResult",
+           "token_scores", "TokenScores"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libwfst_mi355x.so")
@@ -30,7 +31,10 @@ EXPORTED_SYMBOLS = ("wfst_last_error", "wfst_graph_upload", "wfst_graph_release"
                     "wfst_decoder_kernel_times", "wfst_create_stream", "wfst_advance_chunk",
                     "wfst_finalize_stream", "wfst_finalize_streams", "wfst_create_streams", "wfst_release_stream", "wfst_lattice_records",
                     "wfst_blank_skip", "wfst_decode_noalloc", "wfst_layer_create", "wfst_layer_release",
-                    "wfst_layer_logits", "wfst_layer_workspace", "wfst_log_softmax", "wfst_log_softmax_workspace", "wfst_sample", "wfst_sample_workspace")
+                    "wfst_layer_logits", "wfst_layer_workspace", "wfst_log_softmax", "wfst_log_softmax_workspace", "wfst_sample", "wfst_sample_workspace",
+                    "wfst_token_scores", "wfst_token_scores_workspace", "wfst_adapters_create",
+                    "wfst_adapters_release", "wfst_adapters_load", "wfst_layer_adapted_logits",
+                    "wfst_layer_adapted_workspace")
 KERNELS = ("clear", "init", "lpmax", "max", "expand", "finalize", "eps_expand", "eps_resolve",
            "eps_apply", "backtrack", "stream_begin", "stream_end", "reclass", "lat_resolve", "lat_init",
            "lat_back", "gc_begin", "gc_mark", "gc_scan", "gc_compact", "gc_commit", "gc_roots", "gc_clear",
@@ -133,6 +137,13 @@ def load_library():
         lib.wfst_log_softmax_workspace.argtypes = [i32, i64, i32, i32, vp]
         lib.wfst_sample.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, i32, vp, vp, vp, vp, i64, vp]
         lib.wfst_sample_workspace.argtypes = [i32, i64, i32, vp]
+        lib.wfst_token_scores.argtypes = [vp, i32, i64, i64, i32, vp, i32, i32, f32, vp, vp, i32, vp, vp, i64, vp]
+        lib.wfst_token_scores_workspace.argtypes = [i32, i64, i32, i32, i32, vp]
+        lib.wfst_adapters_create.argtypes = [vp, ctypes.c_int, vp, ctypes.POINTER(vp)]
+        lib.wfst_adapters_release.argtypes = [vp]
+        lib.wfst_adapters_load.argtypes = [vp, i32, i32, vp, i64, vp, i64, f32, vp]
+        lib.wfst_layer_adapted_logits.argtypes = [vp, vp, vp, i32, vp, i32, i64, i32, vp, i32, vp, i32, i64, vp, i64, vp]
+        lib.wfst_layer_adapted_workspace.argtypes = [vp, vp, i32, i32, vp]
         for name in EXPORTED_SYMBOLS:
             if name != "wfst_last_error":
                 getattr(lib, name).restype = ctypes.c_int
@@ -335,22 +346,25 @@ class Decoder:
         return self._result(out, wcap, acap)
 
     def decode_hidden(self, layer, hidden, lengths, scale: float = 1.0, bias=None, stream=None,
-                      words_cap: int | None = None, arcs_cap: int | None = None) -> DecodeResult:
+                      words_cap: int | None = None, arcs_cap: int | None = None, adapters=None,
+                      ids=None) -> DecodeResult:
         """Decode a model's last hidden states [B, T, K]: ``layer`` (an OutputLayer
         with the graph's vocabulary) and log_softmax(scale * logits + bias) make the
         log-posteriors of the ``lengths[b]`` frames of each lane, in the decoder's
-        dtype, and decode searches them."""
-        lp = self._log_probs(layer, hidden, lengths, scale, bias, stream)
+        dtype, and decode searches them. ``adapters`` and ``ids`` (one a lane) as in
+        OutputLayer.logits."""
+        lp = self._log_probs(layer, hidden, lengths, scale, bias, stream, adapters, ids)
         return self.decode(lp, lengths, stream=self._raw(stream), words_cap=words_cap, arcs_cap=arcs_cap)
 
     def advance_hidden(self, channels, layer, hidden, lengths, scale: float = 1.0, bias=None,
-                       want_partial: bool = False, stream=None, words_cap: int = 4096, arcs_cap: int = 4096):
+                       want_partial: bool = False, stream=None, words_cap: int = 4096, arcs_cap: int = 4096,
+                       adapters=None, ids=None):
         """advance_chunk from hidden states [C, T, K], as decode_hidden makes their log-posteriors."""
-        lp = self._log_probs(layer, hidden, lengths, scale, bias, stream)
+        lp = self._log_probs(layer, hidden, lengths, scale, bias, stream, adapters, ids)
         return self.advance_chunk(channels, lp, lengths, want_partial=want_partial, stream=self._raw(stream),
                                   words_cap=words_cap, arcs_cap=arcs_cap)
 
-    def _log_probs(self, layer, hidden, lengths, scale, bias, stream):
+    def _log_probs(self, layer, hidden, lengths, scale, bias, stream, adapters=None, ids=None):
         if hidden.dim() != 3:
             raise ValueError("hidden must be [B, T, K]")
         if layer.out_features != self.graph.vocab:
@@ -359,7 +373,8 @@ class Decoder:
         if lens.size and (lens.min() < 0 or lens.max() > hidden.shape[1]):
             raise ValueError("lengths must lie in [0, T]")
         lens = lens.astype(np.int32)
-        return layer.log_probs(hidden, dtype=self.lp_dtype, scale=scale, bias=bias, lengths=lens, stream=stream)
+        more = {} if adapters is None and ids is None else {"adapters": adapters, "ids": ids}
+        return layer.log_probs(hidden, dtype=self.lp_dtype, scale=scale, bias=bias, lengths=lens, stream=stream, **more)
 
     @staticmethod
     def _raw(stream):
@@ -501,4 +516,5 @@ class Decoder:
             pass
 
 
-from .score import OutputLayer, SampleResult, log_softmax, sample  # noqa: E402  (needs the names above)
+from .score import (Adapters, OutputLayer, SampleResult, TokenScores, log_softmax,  # noqa: E402  (needs the names above)
+                    sample, token_scores)

@@ -14,6 +14,7 @@ LIB = os.path.join(HERE, "libwfst_mi355x.so")
 SOURCES = [os.path.join(HERE, "csrc", "wfst_kernels.hip"), os.path.join(HERE, "csrc", "wfst_noalloc.hip"),
            os.path.join(HERE, "csrc", "wfst_api.cpp"), os.path.join(HERE, "csrc", "wfst_layer.hip"),
            os.path.join(HERE, "csrc", "wfst_norm.hip"), os.path.join(HERE, "csrc", "wfst_sample.hip"),
+           os.path.join(HERE, "csrc", "wfst_adapters.hip"), os.path.join(HERE, "csrc", "wfst_tokens.hip"),
            os.path.join(HERE, "csrc", "wfst_score_api.cpp")]
 
 FLAGS = [

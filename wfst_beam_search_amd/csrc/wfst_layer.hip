@@ -47,20 +47,6 @@ __device__ __forceinline__ int block_exponent(float mx)
 template <typename XT> constexpr int kParts = sizeof(XT) == 4 ? 2 : 1;
 template <typename XT> constexpr bool kScaled = !__is_same(XT, _Float16);
 
-// x[k .. k+7] of a row of K features (0 past them, and for a row that is not there).
-template <typename XT>
-__device__ __forceinline__ void load_x(const XT *row, bool there, int k, int K, float (&v)[8])
-{
-    if (there && k + 8 <= K) {
-        const Pack<XT, 8> p = *(const Pack<XT, 8> *)(row + k);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (float)p.v[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = there && k + j < K ? (float)row[k + j] : 0.0f;
-    }
-}
-
 __device__ __forceinline__ float finite_max(const float (&v)[8], float mx)
 {
 #pragma unroll
@@ -165,6 +151,64 @@ __device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, fl
     else ((__bf16 *)c.out)[i] = (__bf16)y;
 }
 
+// Four of a slot's up elements as binary32.
+__device__ __forceinline__ float4_t load_up(const Adapters &a, size_t i)
+{
+    float4_t u;
+    if (a.dtype == kF32) {
+        u = ((const float4_t *)a.up)[i];
+    } else if (a.dtype == kF16) {
+        const Pack<_Float16, 4> p = ((const Pack<_Float16, 4> *)a.up)[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = (float)p.v[j];
+    } else {
+        const Pack<__bf16, 4> p = ((const Pack<__bf16, 4> *)a.up)[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = (float)p.v[j];
+    }
+    return u;
+}
+
+// Adds what the adapters of 16 rows from m0 on give to NT feature tiles from nt0 on:
+// for each slot among the rows the product of h with its up, which only its own rows
+// take (an infinity in one request's adapter stays in its rows). Of `parts`
+// wavefronts with the same sums, number `part` takes every parts-th slot.
+template <int NT>
+__device__ __forceinline__ void add_adapters(const LayerCall &c, int64_t m0, int nt0, int part, int parts,
+                                             float4_t (&acc)[NT])
+{
+    const AdaptCall &ad = c.ad;
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const int64_t m = m0 + col;
+    const int id = m < c.M && row_active(c.rows, m) ? row_adapter(ad, m) : -1;
+    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
+    for (int turn = 0; todo; ++turn) {
+        const int slot = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+        const uint32_t mine = (uint32_t)__ballot(id == slot) & 0xFFFFu;
+        todo &= ~mine;
+        if (turn % parts != part) continue;
+        const int nb = (ad.a.ranks[slot] + 15) / 16;
+        const float *h = ad.h + m * (ad.a.rb * 16) + quad * 4;
+        float4_t d[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) d[n] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int jb = 0; jb < nb; ++jb) {
+            const float4_t hv = *(const float4_t *)(h + jb * 16);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const size_t t = ((size_t)slot * ad.a.nt + min(nt0 + n, ad.a.nt - 1)) * ad.a.rb + jb;
+                const float4_t u = load_up(ad.a, t * kWaveSize + lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(hv[k], u[k], d[n], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = mine >> (quad * 4 + i) & 1 ? acc[n][i] + d[n][i] : acc[n][i];
+    }
+}
+
 // Up to 16 rows of x at a time (blockIdx.y: which 16), which the workgroup itself turns into
 // binary16 in LDS, kc blocks of 128 features per slice at a time, laid out as the
 // matrix instruction reads it: [32 features][8 features][row][8]. Only RP rows
@@ -179,7 +223,7 @@ __device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, fl
 // 4.7 TB/s, 92 % of what a large copy moves on this card.
 template <int KS, int SPL> constexpr int kTilesAhead = KS == 1 ? (SPL == 1 ? 3 : 4) : 2;
 
-template <typename XT, int WS, int GPT, int KS, int SPL>
+template <typename XT, int WS, int GPT, int KS, int SPL, bool AD>
 __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall c, int RP, int kc)
 {
     constexpr int P = kParts<XT>;
@@ -296,6 +340,11 @@ const int at = (u * 16 + j * 4 + quad) * RP + arow;
             }
         }
     }
+    if constexpr (AD) {
+        float4_t sums[1] = {acc};
+        add_adapters<1>(c, m0, nt, slice, KS, sums);
+        acc = sums[0];
+    }
     if (KS > 1) {
         __syncthreads();
         if (wave) joint[(wave - 1) * kWaveSize + lane] = acc;
@@ -366,7 +415,7 @@ __global__ __launch_bounds__(256) void k_layer_operands(Layer l, LayerCall c, ha
 // ms (670 TFLOP/s), bfloat16 9.4 -> 8.6; with two parts, smaller groups or fewer rows
 // the wait for the loads costs more (binary32 3 % of its 12.8 ms, groups of 32 3 %, 32
 // rows 7 %).
-template <typename XT, int WS, int GPT, int MT>
+template <typename XT, int WS, int GPT, int MT, bool AD>
 __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf)
 {
     constexpr int P = kParts<XT>;
@@ -514,6 +563,10 @@ __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const 
         if (step + 1 < steps) put(slot ^ 1);
         __syncthreads();
     }
+    if constexpr (AD) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) add_adapters<NT>(c, ((int64_t)mblk * MT + m) * kRowsM, nt0, half, 2, acc[m]);
+    }
     if (half) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -595,7 +648,7 @@ __global__ __launch_bounds__(256) void k_layer_pack(Layer l, LayerSource src, ui
         for (size_t i = t0; i < (size_t)l.N; i += nthreads) bias[i] = src.bias[i];
 }
 
-template <typename XT, int WS, int GPT, int KS, int SPL>
+template <typename XT, int WS, int GPT, int KS, int SPL, bool AD>
 hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
 {
     constexpr int D = kTilesAhead<KS, SPL>;
@@ -605,7 +658,7 @@ hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
     const int kc = std::min<int>(longest, std::max<int>(D, (int)(40960 / per) / D * D));
     const size_t lds = std::max<size_t>(per * kc, KS > 1 ? (KS - 1) * 64 * sizeof(float4_t) : 0);
     const dim3 g(KS > 1 ? l.nt : (l.nt + kLayerWaves - 1) / kLayerWaves, (c.M + kRowsM - 1) / kRowsM);
-    hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, KS, SPL>), g, dim3(kLayerThreads), lds, s, l, c, RP, kc);
+    hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, KS, SPL, AD>), g, dim3(kLayerThreads), lds, s, l, c, RP, kc);
     return hipGetLastError();
 }
 
@@ -616,13 +669,14 @@ hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
 // 1500 tiles 5.1 / 6.4, 6.8 / 7.6, 11.4 / 12.9, 18.5 / 18.0
 // 2001 tiles 5.2 / 7.4, 6.9 / 8.9, 12.5 / 15.8, 19.2 / 21.1
 // The border lies lower the smaller K is; one for all K gives up 1.3 us at 1500 x 512.
-template <typename XT, int WS, int GPT>
+template <typename XT, int WS, int GPT, bool AD>
 hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
 {
     int RP = 1;
     while (RP < std::min(c.M, kRowsM)) RP *= 2;
-    if (l.nt < 1536) return RP <= 4 ? few_launch<XT, WS, GPT, 4, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 4, 4>(l, c, RP, s);
-    return RP <= 4 ? few_launch<XT, WS, GPT, 1, 1>(l, c, RP, s) : few_launch<XT, WS, GPT, 1, 4>(l, c, RP, s);
+    if (l.nt < 1536)
+        return RP <= 4 ? few_launch<XT, WS, GPT, 4, 1, AD>(l, c, RP, s) : few_launch<XT, WS, GPT, 4, 4, AD>(l, c, RP, s);
+    return RP <= 4 ? few_launch<XT, WS, GPT, 1, 1, AD>(l, c, RP, s) : few_launch<XT, WS, GPT, 1, 4, AD>(l, c, RP, s);
 }
 
 // Row tiles of 16 a workgroup of k_layer_many takes (1, 2 or 4); 0: k_layer_few
@@ -651,7 +705,7 @@ size_t operand_bytes(const Layer &l, int32_t rows, int32_t x_dtype)
     return blocks * kBlockHalves * 2 * (x_dtype == kF32 ? 2 : 1);
 }
 
-template <typename XT, int WS, int GPT, int MT>
+template <typename XT, int WS, int GPT, int MT, bool AD>
 hipError_t layer_many(const Layer &l, const LayerCall &c, hipStream_t s)
 {
     const int64_t blocks = (int64_t)((c.M + kRowsM - 1) / kRowsM) * l.kb;
@@ -660,18 +714,24 @@ hipError_t layer_many(const Layer &l, const LayerCall &c, hipStream_t s)
     hipLaunchKernelGGL(k_layer_operands<XT>, dim3((unsigned)((blocks + 3) / 4)), dim3(256), 0, s, l, c, xa, xf);
     const size_t lds = 2 * 2 * MT * (kParts<XT> * kBlockHalves * 2 + 64);
     const dim3 g((l.nt + 7) / 8, (c.M + MT * kRowsM - 1) / (MT * kRowsM));
-    hipLaunchKernelGGL((k_layer_many<XT, WS, GPT, MT>), g, dim3(512), lds, s, l, c, (const half8_t *)xa, (const float *)xf);
+    hipLaunchKernelGGL((k_layer_many<XT, WS, GPT, MT, AD>), g, dim3(512), lds, s, l, c, (const half8_t *)xa, (const float *)xf);
     return hipGetLastError();
+}
+
+template <typename XT, int WS, int GPT, bool AD>
+hipError_t layer_rows_ad(const Layer &l, const LayerCall &c, hipStream_t s)
+{
+    const int mt = many_tiles(l, c.M, c.x_dtype);
+    if (mt == 4) return layer_many<XT, WS, GPT, 4, AD>(l, c, s);
+    if (mt == 2) return layer_many<XT, WS, GPT, 2, AD>(l, c, s);
+    if (mt == 1) return layer_many<XT, WS, GPT, 1, AD>(l, c, s);
+    return layer_few<XT, WS, GPT, AD>(l, c, s);
 }
 
 template <typename XT, int WS, int GPT>
 hipError_t layer_rows(const Layer &l, const LayerCall &c, hipStream_t s)
 {
-    const int mt = many_tiles(l, c.M, c.x_dtype);
-    if (mt == 4) return layer_many<XT, WS, GPT, 4>(l, c, s);
-    if (mt == 2) return layer_many<XT, WS, GPT, 2>(l, c, s);
-    if (mt == 1) return layer_many<XT, WS, GPT, 1>(l, c, s);
-    return layer_few<XT, WS, GPT>(l, c, s);
+    return c.ad.ids ? layer_rows_ad<XT, WS, GPT, true>(l, c, s) : layer_rows_ad<XT, WS, GPT, false>(l, c, s);
 }
 
 template <typename XT>
@@ -712,6 +772,10 @@ size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype)
 
 hipError_t launch_layer(const Layer &l, const LayerCall &c, hipStream_t s)
 {
+    if (c.ad.ids) {
+        const hipError_t e = launch_adapt_shrink(c, l.K, s);
+        if (e != hipSuccess) return e;
+    }
     if (c.x_dtype == kF32) return layer_xt<float>(l, c, s);
     if (c.x_dtype == kF16) return layer_xt<_Float16>(l, c, s);
     return layer_xt<__bf16>(l, c, s);

@@ -1,7 +1,8 @@
 // Shared by the host entry points (wfst_score_api.cpp) and the gfx950 kernels
-// (wfst_layer.hip, wfst_norm.hip, wfst_sample.hip) of the operators around the
-// search: the output layer with 4-bit weights, the log-softmax and the draw of
-// tokens. Not part of the ABI.
+// (wfst_layer.hip, wfst_adapters.hip, wfst_norm.hip, wfst_sample.hip, wfst_tokens.hip)
+// of the operators around the search: the output layer with 4-bit weights and the
+// low-rank adapters beside it, the log-softmax, the draw of tokens and the scores of
+// given tokens. Not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -57,6 +58,37 @@ struct LayerSource {
     const float *bias;          // [N] or null
 };
 
+// Low-rank adapters of one layer, slots of them, each down [rank, K] and up [N, rank]
+// of an own rank (0: none) and scale. A slot's down is [rb * 16][kp], features past K
+// 0; its up holds for feature tile nt (16 of them) and 16 ranks jb 4 elements for each
+// of 64 lanes, [nt][rb][64][4]: lane l has feature l % 16 and ranks 16 jb + 4 (l / 16)
+// .. + 3, 0 past the slot's rank.
+struct Adapters {
+    void *down, *up;
+    float *scales;              // [slots]
+    int32_t *ranks;             // [slots]
+    int32_t K, N, slots, rank;  // rank: the largest
+    int32_t rb, kp, nt, dtype;
+};
+
+struct AdapterSource {
+    const void *down, *up;
+    int64_t down_stride, up_stride;
+    int32_t rank;
+    float scale;
+};
+
+// Row r of a call takes the adapter ids[r / per_id], none where that is no slot.
+struct AdaptCall {
+    Adapters a;
+    const int32_t *ids;         // null: no adapters
+    int32_t per_id;
+    float *h;                   // [rows up to a multiple of 16][rb * 16], in the workspace
+};
+
+hipError_t launch_adapters_clear(const Adapters &a, hipStream_t s);
+hipError_t launch_adapter_load(const Adapters &a, int32_t slot, const AdapterSource &src, hipStream_t s);
+
 struct LayerCall {
     const void *x;
     void *out;
@@ -65,7 +97,11 @@ struct LayerCall {
     int32_t x_dtype, out_dtype;
     RowSet rows;
     void *workspace;            // layer_workspace bytes
+    AdaptCall ad;
 };
+
+// h[r, j] = scale * sum_k down[j, k] x[r, k] of each row's adapter.
+hipError_t launch_adapt_shrink(const LayerCall &c, int32_t K, hipStream_t s);
 
 size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype);
 hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, void *scales, uint8_t *zeros,
@@ -112,5 +148,31 @@ int sample_chunks(int64_t rows, int32_t V, int32_t x_dtype);
 size_t sample_workspace(int64_t rows, int32_t V, int32_t x_dtype);
 
 hipError_t launch_sample(const SampleCall &c, hipStream_t s);
+
+// ---- scores of given tokens
+
+constexpr int kMaxTokens = 256; // given tokens of one row
+constexpr int kMaxTop = 64;     // alternatives of one row
+
+struct TokenCall {
+    const void *x;
+    int64_t x_stride, rows;
+    int32_t V, x_dtype;
+    const int32_t *tokens;      // [rows, C]
+    int32_t C, top_n;
+    float temperature;
+    const float *temperatures;  // one a row, or null
+    float *log_probs;           // [rows, C]
+    int32_t *ranks;             // [rows, C]
+    float *entropies;           // [rows] or null
+    int32_t *top_tokens;        // [rows, top_n]
+    float *top_log_probs;       // [rows, top_n]
+    RowSet set;
+    void *workspace;            // token_workspace bytes
+};
+
+size_t token_workspace(int64_t rows, int32_t V, int32_t C, int32_t top_n, int32_t x_dtype);
+
+hipError_t launch_token_scores(const TokenCall &c, hipStream_t s);
 
 }  // namespace wfst

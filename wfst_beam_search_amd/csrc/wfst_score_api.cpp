@@ -1,5 +1,5 @@
-// C ABI of the operators around the search: argument checks, the output layer's
-// handle and the launches. Every call is asynchronous on the caller's stream
+// C ABI of the operators around the search: argument checks, the handles of the output
+// layer and its adapters, and the launches. Every call is asynchronous on the caller's stream
 // unless its declaration says otherwise, keeps the calling thread's current
 // device, and lets no exception out.
 #include <hip/hip_runtime.h>
@@ -21,10 +21,17 @@ struct wfst_layer_s {
     Layer l{};
 };
 
+struct wfst_adapters_s {
+    int device = -1;
+    void *block = nullptr;       // one allocation: down, up, scales, ranks
+    Adapters a{};
+};
+
 namespace {
 
 int hip_fail(hipError_t e, const char *what)
 {
+    (void)hipGetLastError();     // (a later call's launch must not report this one's error)
     return api_fail(e == hipErrorOutOfMemory ? WFST_ENOMEM : WFST_EDEVICE,
                     std::string(what) + ": " + hipGetErrorString(e));
 }
@@ -249,37 +256,199 @@ extern "C" int wfst_layer_workspace(wfst_layer_t layer, int32_t x_dtype, int32_t
     });
 }
 
+namespace {
+
+// Where the adapters' products lie in a call's workspace, behind the layer's own.
+size_t adapt_offset(const Layer &l, int32_t rows, int32_t x_dtype)
+{
+    return (layer_workspace(l, rows, x_dtype) + 255) / 256 * 256;
+}
+
+size_t adapt_workspace(const Layer &l, const Adapters &a, int32_t rows, int32_t x_dtype)
+{
+    return adapt_offset(l, rows, x_dtype) + ((size_t)rows + 15) / 16 * 16 * a.rb * 16 * sizeof(float);
+}
+
+int check_same_layer(const Layer &l, int device, wfst_adapters_t ad)
+{
+    if (ad->a.K != l.K || ad->a.N != l.N) return api_fail(WFST_EINVAL, "the adapters are of a layer of another size");
+    if (ad->device != device) return api_fail(WFST_EINVAL, "the adapters are on another device than the layer");
+    return WFST_OK;
+}
+
+// The layer's logits, with adapters where ad is given.
+int layer_logits(wfst_layer_t layer, wfst_adapters_t ad, const int32_t *ids, int32_t rows_per_id, const void *x,
+                 int32_t x_dtype, int64_t x_stride, int32_t rows, const int32_t *lengths, int32_t T, void *out,
+                 int32_t out_dtype, int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!layer) return api_fail(WFST_EINVAL, "layer is null");
+    const Layer &l = layer->l;
+    if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return api_fail(WFST_EINVAL, "not an element type");
+    if (rows < 0 || rows > (1 << 20) - 16) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^20 - 16]");
+    if (ad) TRY(check_same_layer(l, layer->device, ad));
+    if (rows == 0) return WFST_OK;
+    if (!x || !out || (ad && !ids)) return api_fail(WFST_EINVAL, "a pointer is null");
+    if (ad && (rows_per_id < 1 || rows % rows_per_id))
+        return api_fail(WFST_EINVAL, "rows must be a multiple of rows_per_id >= 1");
+    if (rows > 1 && (x_stride < l.K || out_stride < l.N))
+        return api_fail(WFST_EINVAL, "a row stride is smaller than its row");
+    const size_t xe = dtype_size(x_dtype), oe = dtype_size(out_dtype);
+    const int64_t xb = span_bytes(rows, l.K, x_stride, xe), ob = span_bytes(rows, l.N, out_stride, oe);
+    if (xb < 0 || ob < 0) return api_fail(WFST_EINVAL, "a tensor is too large");
+    DeviceScope scope;
+    HIP_TRY(scope.enter(layer->device));
+    TRY(check_aligned(x, xe, "x"));
+    TRY(check_aligned(out, oe, "out"));
+    TRY(api_check_buffer(x, (size_t)xb, layer->device, "x"));
+    TRY(api_check_buffer(out, (size_t)ob, layer->device, "out"));
+    TRY(check_lengths(lengths, rows, T, layer->device));
+    TRY(check_stream(stream, layer->device));
+    if (ranges_meet(x, xb, out, ob)) return api_fail(WFST_EINVAL, "out must not overlap x");
+    const size_t need = ad ? adapt_workspace(l, ad->a, rows, x_dtype) : layer_workspace(l, rows, x_dtype);
+    TRY(check_workspace(workspace, workspace_bytes, need, layer->device, x, xb, out, ob));
+    TRY(check_off_lengths(out, ob, lengths, rows, T, "out"));
+    TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
+    LayerCall c{x, out, x_stride, out_stride, rows, x_dtype, out_dtype, {lengths, T}, workspace, {}};
+    if (ad) {
+        const int64_t ib = (int64_t)(rows / rows_per_id) * 4;
+        TRY(check_aligned(ids, 4, "ids"));
+        TRY(api_check_buffer(ids, (size_t)ib, layer->device, "ids"));
+        if (ranges_meet(ids, ib, out, ob) || ranges_meet(ids, ib, workspace, (int64_t)need))
+            return api_fail(WFST_EINVAL, "out and workspace must not overlap ids");
+        c.ad = {ad->a, ids, rows_per_id, (float *)((char *)workspace + adapt_offset(l, rows, x_dtype))};
+    }
+    HIP_TRY(launch_layer(l, c, (hipStream_t)stream));
+    return WFST_OK;
+}
+
+}  // namespace
+
 extern "C" int wfst_layer_logits(wfst_layer_t layer, const void *x, int32_t x_dtype, int64_t x_stride, int32_t rows,
                                  const int32_t *lengths, int32_t T, void *out, int32_t out_dtype, int64_t out_stride,
                                  void *workspace, int64_t workspace_bytes, void *stream)
 {
     return guarded([&]() -> int {
-        if (!layer) return api_fail(WFST_EINVAL, "layer is null");
-        const Layer &l = layer->l;
-        if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return api_fail(WFST_EINVAL, "not an element type");
+        return layer_logits(layer, nullptr, nullptr, 1, x, x_dtype, x_stride, rows, lengths, T, out, out_dtype,
+                            out_stride, workspace, workspace_bytes, stream);
+    });
+}
+
+extern "C" int wfst_layer_adapted_logits(wfst_layer_t layer, wfst_adapters_t adapters, const int32_t *ids,
+                                         int32_t rows_per_id, const void *x, int32_t x_dtype, int64_t x_stride,
+                                         int32_t rows, const int32_t *lengths, int32_t T, void *out, int32_t out_dtype,
+                                         int64_t out_stride, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return guarded([&]() -> int {
+        if (!adapters) return api_fail(WFST_EINVAL, "adapters is null");
+        return layer_logits(layer, adapters, ids, rows_per_id, x, x_dtype, x_stride, rows, lengths, T, out, out_dtype,
+                            out_stride, workspace, workspace_bytes, stream);
+    });
+}
+
+extern "C" int wfst_layer_adapted_workspace(wfst_layer_t layer, wfst_adapters_t adapters, int32_t x_dtype,
+                                            int32_t rows, int64_t *bytes)
+{
+    return guarded([&]() -> int {
+        if (!layer || !adapters || !bytes) return api_fail(WFST_EINVAL, "a pointer is null");
+        if (!dtype_ok(x_dtype)) return api_fail(WFST_EINVAL, "not an element type");
         if (rows < 0 || rows > (1 << 20) - 16) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^20 - 16]");
-        if (rows == 0) return WFST_OK;
-        if (!x || !out) return api_fail(WFST_EINVAL, "a pointer is null");
-        if (rows > 1 && (x_stride < l.K || out_stride < l.N))
-            return api_fail(WFST_EINVAL, "a row stride is smaller than its row");
-        const size_t xe = dtype_size(x_dtype), oe = dtype_size(out_dtype);
-        const int64_t xb = span_bytes(rows, l.K, x_stride, xe), ob = span_bytes(rows, l.N, out_stride, oe);
-        if (xb < 0 || ob < 0) return api_fail(WFST_EINVAL, "a tensor is too large");
+        TRY(check_same_layer(layer->l, layer->device, adapters));
+        *bytes = (int64_t)adapt_workspace(layer->l, adapters->a, rows, x_dtype);
+        return WFST_OK;
+    });
+}
+
+extern "C" int wfst_adapters_create(const wfst_adapters_desc *d, int device, void *stream, wfst_adapters_t *out)
+{
+    return guarded([&]() -> int {
+        if (!d || !out) return api_fail(WFST_EINVAL, "a pointer is null");
+        *out = nullptr;
+        if (d->in_features < 1 || d->in_features > (1 << 24))
+            return api_fail(WFST_EINVAL, "in_features must lie in [1, 2^24]");
+        if (d->out_features < 1 || d->out_features > (1 << 24))
+            return api_fail(WFST_EINVAL, "out_features must lie in [1, 2^24]");
+        if (d->slots < 1 || d->slots > (1 << 16)) return api_fail(WFST_EINVAL, "slots must lie in [1, 2^16]");
+        if (d->rank < 1 || d->rank > 128) return api_fail(WFST_EINVAL, "rank must lie in [1, 128]");
+        if (!dtype_ok(d->dtype)) return api_fail(WFST_EINVAL, "dtype is not an element type");
+        int ndev = 0;
+        if (hipGetDeviceCount(&ndev) != hipSuccess) ndev = 0;
+        if (device < 0 || device >= ndev) return api_fail(WFST_EINVAL, "no such device");
         DeviceScope scope;
-        HIP_TRY(scope.enter(layer->device));
-        TRY(check_aligned(x, xe, "x"));
-        TRY(check_aligned(out, oe, "out"));
-        TRY(api_check_buffer(x, (size_t)xb, layer->device, "x"));
-        TRY(api_check_buffer(out, (size_t)ob, layer->device, "out"));
-        TRY(check_lengths(lengths, rows, T, layer->device));
-        TRY(check_stream(stream, layer->device));
-        if (ranges_meet(x, xb, out, ob)) return api_fail(WFST_EINVAL, "out must not overlap x");
-        const size_t need = layer_workspace(l, rows, x_dtype);
-        TRY(check_workspace(workspace, workspace_bytes, need, layer->device, x, xb, out, ob));
-        TRY(check_off_lengths(out, ob, lengths, rows, T, "out"));
-        TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
-        const LayerCall c{x, out, x_stride, out_stride, rows, x_dtype, out_dtype, {lengths, T}, workspace};
-        HIP_TRY(launch_layer(l, c, (hipStream_t)stream));
+        HIP_TRY(scope.enter(device));
+        TRY(check_stream(stream, device));
+        Adapters a{};
+        a.K = d->in_features;
+        a.N = d->out_features;
+        a.slots = d->slots;
+        a.rank = d->rank;
+        a.rb = (d->rank + 15) / 16;
+        a.kp = (d->in_features + 31) / 32 * 32;
+        a.nt = (d->out_features + kTileN - 1) / kTileN;
+        a.dtype = d->dtype;
+        const auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+        const size_t es = dtype_size(a.dtype), n = (size_t)a.slots * a.rb * 16;
+        const size_t db = up(n * a.kp * es), ub = up(n * a.nt * kTileN * es), sb = up((size_t)a.slots * 4);
+        wfst_adapters_s *h = new wfst_adapters_s;
+        hipError_t e = hipMalloc(&h->block, db + ub + 2 * sb);
+        if (e != hipSuccess) {
+            delete h;
+            return hip_fail(e, "hipMalloc");
+        }
+        char *p = (char *)h->block;
+        a.down = p;
+        a.up = p + db;
+        a.scales = (float *)(p + db + ub);
+        a.ranks = (int32_t *)(p + db + ub + sb);
+        h->device = device;
+        h->a = a;
+        e = launch_adapters_clear(a, (hipStream_t)stream);
+        if (e == hipSuccess) e = hipStreamSynchronize((hipStream_t)stream);
+        if (e != hipSuccess) {
+            (void)hipFree(h->block);
+            delete h;
+            return hip_fail(e, "wfst_adapters_create");
+        }
+        *out = h;
+        return WFST_OK;
+    });
+}
+
+extern "C" int wfst_adapters_release(wfst_adapters_t adapters)
+{
+    return guarded([&]() -> int {
+        if (!adapters) return WFST_OK;
+        DeviceScope scope;
+        HIP_TRY(scope.enter(adapters->device));
+        const hipError_t e = hipFree(adapters->block);
+        delete adapters;
+        if (e != hipSuccess) return hip_fail(e, "hipFree");
+        return WFST_OK;
+    });
+}
+
+extern "C" int wfst_adapters_load(wfst_adapters_t adapters, int32_t slot, int32_t rank, const void *down,
+                                  int64_t down_stride, const void *up, int64_t up_stride, float scale, void *stream)
+{
+    return guarded([&]() -> int {
+        if (!adapters) return api_fail(WFST_EINVAL, "adapters is null");
+        const Adapters &a = adapters->a;
+        if (slot < 0 || slot >= a.slots) return api_fail(WFST_EINVAL, "slot must lie in [0, slots)");
+        if (rank < 0 || rank > a.rank) return api_fail(WFST_EINVAL, "rank must lie in [0, the adapters' rank]");
+        if (!std::isfinite(scale)) return api_fail(WFST_EINVAL, "scale must be finite");
+        if (rank && (!down || !up)) return api_fail(WFST_EINVAL, "a pointer is null");
+        if ((rank > 1 && down_stride < a.K) || (rank && a.N > 1 && up_stride < rank))
+            return api_fail(WFST_EINVAL, "a row stride is smaller than its row");
+        const size_t es = dtype_size(a.dtype);
+        const int64_t db = span_bytes(rank, a.K, down_stride, es), ub = span_bytes(rank ? a.N : 0, rank, up_stride, es);
+        if (db < 0 || ub < 0) return api_fail(WFST_EINVAL, "a tensor is too large");
+        DeviceScope scope;
+        HIP_TRY(scope.enter(adapters->device));
+        TRY(check_aligned(down, es, "down"));
+        TRY(check_aligned(up, es, "up"));
+        TRY(api_check_buffer(down, (size_t)db, adapters->device, "down"));
+        TRY(api_check_buffer(up, (size_t)ub, adapters->device, "up"));
+        TRY(check_stream(stream, adapters->device));
+        HIP_TRY(launch_adapter_load(a, slot, {down, up, down_stride, up_stride, rank, scale}, (hipStream_t)stream));
         return WFST_OK;
     });
 }
@@ -432,6 +601,112 @@ extern "C" int wfst_sample(const void *x, int32_t x_dtype, int64_t x_stride, int
         c.set = {lengths, T};
         c.workspace = workspace;
         HIP_TRY(launch_sample(c, (hipStream_t)stream));
+        return WFST_OK;
+    });
+}
+
+namespace {
+
+int check_token_sizes(int32_t x_dtype, int64_t rows, int32_t V, int32_t C, int32_t top_n)
+{
+    if (!dtype_ok(x_dtype)) return api_fail(WFST_EINVAL, "not an element type");
+    if (rows < 0 || rows > ((int64_t)1 << 40)) return api_fail(WFST_EINVAL, "rows must lie in [0, 2^40]");
+    if (V < 1 || V > (1 << 24)) return api_fail(WFST_EINVAL, "V must lie in [1, 2^24]");
+    if (C < 0 || C > kMaxTokens) return api_fail(WFST_EINVAL, "tokens_per_row must lie in [0, 256]");
+    if (top_n < 0 || top_n > kMaxTop) return api_fail(WFST_EINVAL, "top_n must lie in [0, 64]");
+    return WFST_OK;
+}
+
+}  // namespace
+
+extern "C" int wfst_token_scores_workspace(int32_t x_dtype, int64_t rows, int32_t V, int32_t tokens_per_row,
+                                           int32_t top_n, int64_t *bytes)
+{
+    return guarded([&]() -> int {
+        TRY(check_token_sizes(x_dtype, rows, V, tokens_per_row, top_n));
+        if (!bytes) return api_fail(WFST_EINVAL, "a pointer is null");
+        *bytes = (int64_t)token_workspace(rows, V, tokens_per_row, top_n, x_dtype);
+        return WFST_OK;
+    });
+}
+
+extern "C" int wfst_token_scores(const void *x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t V,
+                                 const int32_t *tokens, int32_t tokens_per_row, int32_t top_n, float temperature,
+                                 const float *temperatures, const int32_t *lengths, int32_t T,
+                                 const wfst_token_scores_out *out, void *workspace, int64_t workspace_bytes,
+                                 void *stream)
+{
+    return guarded([&]() -> int {
+        const int32_t C = tokens_per_row;
+        if (!out) return api_fail(WFST_EINVAL, "out is null");
+        TRY(check_token_sizes(x_dtype, rows, V, C, top_n));
+        if (!temperatures && !(temperature >= 0.0f && std::isfinite(temperature)))
+            return api_fail(WFST_EINVAL, "temperature must be finite and not negative");
+        if (rows == 0) return WFST_OK;
+        if (!x || (C && (!tokens || !out->log_probs || !out->ranks)) ||
+            (top_n && (!out->top_tokens || !out->top_log_probs)))
+            return api_fail(WFST_EINVAL, "a pointer is null");
+        if (rows > 1 && x_stride < V) return api_fail(WFST_EINVAL, "a row stride is smaller than its row");
+        const size_t xe = dtype_size(x_dtype);
+        const int64_t xb = span_bytes(rows, V, x_stride, xe);
+        if (xb < 0) return api_fail(WFST_EINVAL, "a tensor is too large");
+        const int device = device_of(x, "scores");
+        if (device < 0) return device;
+        DeviceScope scope;
+        HIP_TRY(scope.enter(device));
+        TRY(check_aligned(x, xe, "scores"));
+        TRY(api_check_buffer(x, (size_t)xb, device, "scores"));
+        const int64_t cb = rows * C * 4, nb = rows * top_n * 4;
+        const struct { const void *p; int64_t bytes; const char *name; bool out; } args[] = {
+            {C ? tokens : nullptr, cb, "tokens", false}, {temperatures, rows * 4, "temperatures", false},
+            {C ? out->log_probs : nullptr, cb, "log_probs", true}, {C ? out->ranks : nullptr, cb, "ranks", true},
+            {out->entropies, rows * 4, "entropies", true},
+            {top_n ? out->top_tokens : nullptr, nb, "top_tokens", true},
+            {top_n ? out->top_log_probs : nullptr, nb, "top_log_probs", true}};
+        bool any = false;
+        for (const auto &a : args) {
+            if (!a.p) continue;
+            any |= a.out;
+            TRY(check_aligned(a.p, 4, a.name));
+            TRY(api_check_buffer(a.p, (size_t)a.bytes, device, a.name));
+        }
+        if (!any) return api_fail(WFST_EINVAL, "no output is wanted");
+        for (const auto &o : args) {
+            if (!o.out || !o.p) continue;
+            if (ranges_meet(o.p, o.bytes, x, xb)) return api_fail(WFST_EINVAL, "an output overlaps the scores");
+            for (const auto &a : args)
+                if (a.p && &a != &o && ranges_meet(o.p, o.bytes, a.p, a.bytes))
+                    return api_fail(WFST_EINVAL, std::string(o.name) + " overlaps " + a.name);
+        }
+        TRY(check_lengths(lengths, rows, T, device));
+        TRY(check_stream(stream, device));
+        const size_t need = token_workspace(rows, V, C, top_n, x_dtype);
+        TRY(check_workspace(workspace, workspace_bytes, need, device, x, xb, nullptr, 0));
+        for (const auto &a : args) {
+            if (need && a.p && ranges_meet(workspace, (int64_t)need, a.p, a.bytes))
+                return api_fail(WFST_EINVAL, std::string("workspace overlaps ") + a.name);
+            if (a.out) TRY(check_off_lengths(a.p, a.bytes, lengths, rows, T, a.name));
+        }
+        TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
+        TokenCall c{};
+        c.x = x;
+        c.x_stride = x_stride;
+        c.rows = rows;
+        c.V = V;
+        c.x_dtype = x_dtype;
+        c.tokens = tokens;
+        c.C = C;
+        c.top_n = top_n;
+        c.temperature = temperature;
+        c.temperatures = temperatures;
+        c.log_probs = (float *)out->log_probs;
+        c.ranks = (int32_t *)out->ranks;
+        c.entropies = (float *)out->entropies;
+        c.top_tokens = (int32_t *)out->top_tokens;
+        c.top_log_probs = (float *)out->top_log_probs;
+        c.set = {lengths, T};
+        c.workspace = workspace;
+        HIP_TRY(launch_token_scores(c, (hipStream_t)stream));
         return WFST_OK;
     });
 }

@@ -18,6 +18,13 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 
+// The adapter slot of row r of a call, -1: none.
+__device__ __forceinline__ int row_adapter(const AdaptCall &ad, int64_t r)
+{
+    const int s = ad.ids[r / ad.per_id];
+    return s >= 0 && s < ad.a.slots && ad.a.ranks[s] > 0 ? s : -1;
+}
+
 // N consecutive elements at any element alignment, as one load or store.
 template <typename T, int N> struct __attribute__((packed, aligned(sizeof(T)))) Pack { T v[N]; };
 
@@ -26,6 +33,20 @@ __device__ __forceinline__ bool row_active(const RowSet &s, int64_t r)
     if (!s.lengths) return true;
     const int64_t b = r / s.T;
     return (int32_t)(r - b * s.T) < s.lengths[b];
+}
+
+// x[k .. k+7] of a row of K features (0 past them, and for a row that is not there).
+template <typename XT>
+__device__ __forceinline__ void load_x(const XT *row, bool there, int k, int K, float (&v)[8])
+{
+    if (there && k + 8 <= K) {
+        const Pack<XT, 8> p = *(const Pack<XT, 8> *)(row + k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (float)p.v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = there && k + j < K ? (float)row[k + j] : 0.0f;
+    }
 }
 
 // Reductions over a wavefront by data-parallel moves (all 64 lanes active): four

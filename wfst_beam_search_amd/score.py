@@ -1,7 +1,8 @@
-"""Operators around the search: the output layer with 4-bit weights, the
-log-softmax that makes ``log_prob`` of its logits, and the draw of tokens from
-scores. Thin bindings like the rest of the package: the work runs in the HIP
-library (``wfst_layer_*``, ``wfst_log_softmax``, ``wfst_sample`` of
+"""Operators around the search: the output layer with 4-bit weights and low-rank
+adapters beside it, the log-softmax that makes ``log_prob`` of its logits, the draw
+of tokens from scores and the scores of given tokens. Thin bindings like the rest
+of the package: the work runs in the HIP library (``wfst_layer_*``,
+``wfst_adapters_*``, ``wfst_log_softmax``, ``wfst_sample``, ``wfst_token_scores`` of
 ``include/wfst.h``, which states the formulas); PyTorch supplies device memory
 and streams. They are inference operators: no gradient passes through them, and a
 tensor that needs one (backward, or a forward-mode dual) is refused.
@@ -35,10 +36,20 @@ class _LayerDesc(ctypes.Structure):
                 ("zeros", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
+class _AdaptersDesc(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("slots", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 class _SampleConfig(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
                 ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
                 ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
+
+
+class _TokenScoresOut(ctypes.Structure):
+    _fields_ = [("log_probs", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("entropies", ctypes.c_void_p),
+                ("top_tokens", ctypes.c_void_p), ("top_log_probs", ctypes.c_void_p)]
 
 
 _codes = None          # torch dtype -> element type code
@@ -252,12 +263,17 @@ class OutputLayer:
         _check(lib.wfst_layer_create(ctypes.byref(desc), device.index, raw, ctypes.byref(h)))
         self.handle = h
         self._logits = lib.wfst_layer_logits
-        self._bytes = {}                        # (element type, rows) -> workspace bytes
+        self._adapted = lib.wfst_layer_adapted_logits
+        self._bytes = {}                        # (element type, rows, rank blocks) -> workspace bytes
         self.device = device
         self.in_features, self.out_features = K, N
 
-    def logits(self, hidden, dtype: str = "f32", lengths=None, out=None, stream=None):
-        """Logits [..., N] of hidden states [..., K], in ``dtype`` ("f32", "f16", "bf16")."""
+    def logits(self, hidden, dtype: str = "f32", lengths=None, out=None, stream=None, adapters=None, ids=None):
+        """Logits [..., N] of hidden states [..., K], in ``dtype`` ("f32", "f16", "bf16").
+        With ``adapters`` (an Adapters of this layer's size) the row of each hidden state
+        gets what the adapter in slot ``ids`` gives: int32, of the leading dimensions'
+        shape or its first ones' ([B] for [B, T, K]: one a lane), -1 or an empty slot for
+        none; a tensor on the GPU, or host values that are copied first."""
         if self.handle is None:
             raise ValueError("the layer was released")
         _gpu(hidden, "hidden", self.device)
@@ -269,36 +285,148 @@ class OutputLayer:
         raw, other = _stream(stream, self.device)
         lead = hidden.shape[:-1]
         lengths, T = _lengths(lengths, lead, self.device, other)
+        if adapters is not None:
+            adapters._check_layer(self)
+            ids, per = _ids(ids, lead, adapters.slots, self.device, other)
+        elif ids is not None:
+            raise ValueError("ids need adapters")
         out = _out(out, (*lead, self.out_features), _named(dtype), self.device, other)
         _, ostep = _rows(out, "out")
-        need = self._bytes.get((code, rows))
+        key = (code, rows, 0 if adapters is None else -(-adapters.rank // 16))
+        need = self._bytes.get(key)
         if need is None:
             n = ctypes.c_int64(0)
-            _check(load_library().wfst_layer_workspace(self.handle, code, rows, ctypes.byref(n)))
+            if adapters is None:
+                _check(load_library().wfst_layer_workspace(self.handle, code, rows, ctypes.byref(n)))
+            else:
+                _check(load_library().wfst_layer_adapted_workspace(self.handle, adapters.handle, code, rows,
+                                                                   ctypes.byref(n)))
             if len(self._bytes) > 256:
                 self._bytes.clear()
-            need = self._bytes[code, rows] = n.value
+            need = self._bytes[key] = n.value
         work = _workspace(need, self.device, other)
-        _check(self._logits(self.handle, hidden.data_ptr(), code, step, rows, _p(lengths), T, out.data_ptr(),
-                            DTYPES[dtype], ostep, _p(work), need, raw))
+        if adapters is None:
+            _check(self._logits(self.handle, hidden.data_ptr(), code, step, rows, _p(lengths), T, out.data_ptr(),
+                                DTYPES[dtype], ostep, _p(work), need, raw))
+        else:
+            _check(self._adapted(self.handle, adapters.handle, _p(ids), per, hidden.data_ptr(), code, step, rows,
+                                 _p(lengths), T, out.data_ptr(), DTYPES[dtype], ostep, _p(work), need, raw))
         return out
 
     def log_probs(self, hidden, dtype: str = "f32", scale: float = 1.0, bias=None, lengths=None, out=None,
-                  stream=None):
+                  stream=None, adapters=None, ids=None):
         """log_softmax(scale * logits + bias) of hidden states, in ``dtype``: the
         search's ``log_prob`` for hidden states [B, T, K]. The logits in between are binary32."""
         _, other = _stream(stream, self.device)
         if lengths is not None:
             lengths, _ = _lengths(lengths, hidden.shape[:-1], self.device, other)
         direct = dtype == "f32"
-        logits = self.logits(hidden, "f32", lengths=lengths, out=out if direct else None, stream=stream)
+        logits = self.logits(hidden, "f32", lengths=lengths, out=out if direct else None, stream=stream,
+                             adapters=adapters, ids=ids)
         return log_softmax(logits, dtype=dtype, scale=scale, bias=bias, lengths=lengths,
                            out=logits if direct else out, stream=stream)
+
+    def token_scores(self, hidden, tokens=None, top_n: int = 0, temperature=1.0, lengths=None, out=None, stream=None,
+                     adapters=None, ids=None) -> "TokenScores":
+        """token_scores of hidden states' logits (binary32 in between), with adapters as in ``logits``."""
+        _, other = _stream(stream, self.device)
+        if lengths is not None:
+            lengths, _ = _lengths(lengths, hidden.shape[:-1], self.device, other)
+        logits = self.logits(hidden, "f32", lengths=lengths, stream=stream, adapters=adapters, ids=ids)
+        return token_scores(logits, tokens, top_n=top_n, temperature=temperature, lengths=lengths, out=out,
+                            stream=stream)
 
     def release(self):
         if self.handle is not None:
             h, self.handle = self.handle, None
             load_library().wfst_layer_release(h)
+
+    def __del__(self):
+        try:
+            self.release()
+        except Exception:
+            pass
+
+
+def _ids(ids, lead, slots, device, other):
+    """(device int32 tensor, rows that share an id) for rows of the given leading shape."""
+    import torch
+    if ids is None:
+        raise ValueError("adapters need ids")
+    if isinstance(ids, torch.Tensor) and ids.is_cuda:
+        if ids.dtype != torch.int32 or not ids.is_contiguous():
+            raise TypeError("ids on the GPU must be a packed int32 tensor")
+        _gpu(ids, "ids", device)
+    else:
+        host = ids.numpy() if isinstance(ids, torch.Tensor) else np.array(ids)
+        if host.size and (host.dtype.kind not in "iu" or int(host.max()) >= slots):
+            raise ValueError(f"ids must be integers below {slots}, the adapters' slots")
+        host = np.array(np.maximum(host, -1), dtype=np.int32)
+        ids = torch.from_numpy(host).to(device)         # (the copy has ended when this returns)
+        if other is not None:
+            ids.record_stream(other)
+    if ids.shape != lead[:ids.dim()]:
+        raise ValueError(f"ids must have the leading dimensions of hidden, {tuple(lead)}, or the first ones of them")
+    per = 1
+    for size in lead[ids.dim():]:
+        per *= int(size)
+    return ids, _int32(per, "rows of an id")
+
+
+class Adapters:
+    """Low-rank adapters beside an output layer (or others of its size): ``slots``
+    places, each empty or holding down [r, K] and up [N, r] in ``dtype`` ("f32", "f16",
+    "bf16"), r up to ``rank`` (at most 128), and a scale. ``OutputLayer.logits`` adds
+    scale * up @ (down @ x) of each row's slot to the layer's logits."""
+
+    def __init__(self, layer: OutputLayer, slots: int, rank: int, dtype: str = "bf16", stream=None):
+        self.handle = None
+        lib = load_library()
+        self._dtype = _named(dtype)
+        self.slots, self.rank = _int32(slots, "slots"), _int32(rank, "rank")
+        self.in_features, self.out_features, self.device = layer.in_features, layer.out_features, layer.device
+        raw, _ = _stream(stream, self.device)
+        desc = _AdaptersDesc(self.in_features, self.out_features, self.slots, self.rank, DTYPES[dtype])
+        h = ctypes.c_void_p()
+        _check(lib.wfst_adapters_create(ctypes.byref(desc), self.device.index, raw, ctypes.byref(h)))
+        self.handle = h
+
+    def _check_layer(self, layer):
+        if self.handle is None:
+            raise ValueError("the adapters were released")
+        if (self.in_features, self.out_features) != (layer.in_features, layer.out_features):
+            raise ValueError("the adapters are of a layer of another size")
+        if self.device != layer.device:
+            raise ValueError(f"the adapters must be on {layer.device}")
+
+    def load(self, slot: int, down, up, scale: float = 1.0, stream=None):
+        """Fill ``slot`` with a copy of ``down`` [r, K] and ``up`` [N, r]. Ordered on ``stream`` like
+        every call; the other slots may be in use meanwhile."""
+        if self.handle is None:
+            raise ValueError("the adapters were released")
+        for t, name in ((down, "down"), (up, "up")):
+            _gpu(t, name, self.device)
+            if t.dtype != self._dtype or t.dim() != 2:
+                raise TypeError(f"{name} must be a {self._dtype} matrix")
+        r = _int32(down.shape[0], "rank")
+        if r < 1 or down.shape[1] != self.in_features or tuple(up.shape) != (self.out_features, r):
+            raise ValueError(f"down must be [r, {self.in_features}] and up [{self.out_features}, r]")
+        dstep, ustep = _rows(down, "down")[1], _rows(up, "up")[1]
+        raw, other = _stream(stream, self.device)
+        _check(load_library().wfst_adapters_load(self.handle, _int32(slot, "slot"), r, down.data_ptr(), dstep,
+                                                 up.data_ptr(), ustep, float(scale), raw))
+
+    def unload(self, slot: int, stream=None):
+        """Empty ``slot``: its id is then none."""
+        if self.handle is None:
+            raise ValueError("the adapters were released")
+        raw, _ = _stream(stream, self.device)
+        _check(load_library().wfst_adapters_load(self.handle, _int32(slot, "slot"), 0, None, 0, None, 0, 0.0, raw))
+
+    def release(self):
+        if self.handle is not None:
+            h, self.handle = self.handle, None
+            load_library().wfst_adapters_release(h)
 
     def __del__(self):
         try:
@@ -407,4 +535,89 @@ def sample(scores, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, lengths=No
     work = _workspace(need, device, other)
     _check(lib.wfst_sample(scores.data_ptr(), code, step, rows, V, u.data_ptr(), ctypes.byref(cfg), _p(lengths), T,
                            _p(res.tokens), _p(res.log_probs), _p(res.kept), _p(work), need, raw))
+    return res
+
+
+class TokenScores(NamedTuple):
+    log_probs: object        # float32 [...] or [..., C]: of each given token (None: no tokens)
+    ranks: object            # int32, the same shape: labels before it, -1 for a token that is no label
+    entropies: object        # float32 [...]
+    top_tokens: object       # int32 [..., top_n]: the largest scores, -1 where there are no more (None: top_n 0)
+    top_log_probs: object    # float32 [..., top_n]
+
+
+@functools.lru_cache(maxsize=256)
+def _token_bytes(code, rows, V, C, n):
+    need = ctypes.c_int64(0)
+    _check(load_library().wfst_token_scores_workspace(code, rows, V, C, n, ctypes.byref(need)))
+    return need.value
+
+
+_MAX_TOP = 64
+
+
+def token_scores(scores, tokens=None, top_n: int = 0, temperature=1.0, lengths=None, out=None,
+                 stream=None) -> TokenScores:
+    """Log-probability and rank of given ``tokens`` (int32 [...] or [..., C], up to
+    256 a row) under softmax(scores / temperature) over all of ``scores`` [..., V]
+    (logits or log-probabilities), the distribution's entropy, and the ``top_n`` (up to
+    64) best labels with their log-probabilities, ties to the lowest index.
+    ``temperature`` is a number or a float32 tensor [...] on the GPU (0: all mass to the
+    largest score). ``out``: tensors of the result to write to, in its order (None, or
+    left out at the end, where the result has none)."""
+    import torch
+    lib = load_library()
+    _gpu(scores, "scores")
+    device = scores.device
+    code = _code(scores, "scores")
+    rows, step = _rows(scores, "scores")
+    V = _int32(scores.shape[-1], "V")
+    shape = scores.shape[:-1]
+    n = int(top_n)
+    if not 0 <= n <= _MAX_TOP:
+        raise ValueError(f"top_n must lie in [0, {_MAX_TOP}]")
+    C, tshape = 0, None
+    if tokens is not None:
+        _gpu(tokens, "tokens", device)
+        tshape = tokens.shape
+        if tokens.dtype != torch.int32 or not tokens.is_contiguous():
+            raise TypeError("tokens must be a packed int32 tensor")
+        if tshape == shape:
+            C = 1
+        elif tshape[:-1] == shape and len(tshape) == len(shape) + 1:
+            C = _int32(tshape[-1], "tokens per row")
+        else:
+            raise ValueError(f"tokens must have the shape {tuple(shape)} or {(*shape, 'C')}")
+    t, ts = _setting(temperature, torch.float32, shape, device, "temperature")
+    raw, other = _stream(stream, device)
+    lengths, T = _lengths(lengths, shape, device, other)
+    if out is None:
+        # (one allocation: log-probabilities and ranks, the alternatives, entropies)
+        i, f = torch.int32, torch.float32
+        per = 2 * C + 2 * n + 1
+        buf = _new(rows * per, i, device, other)
+        cut = [rows * k for k in (C, 2 * C, 2 * C + n, 2 * C + 2 * n)]
+        res = TokenScores(None if tokens is None else buf[:cut[0]].view(f).view(tshape),
+                          None if tokens is None else buf[cut[0]:cut[1]].view(tshape),
+                          buf[cut[3]:].view(f).view(shape),
+                          buf[cut[1]:cut[2]].view(*shape, n) if n else None,
+                          buf[cut[2]:cut[3]].view(f).view(*shape, n) if n else None)
+    else:
+        out = tuple(out)
+        if len(out) > 5:
+            raise ValueError("out must be the result's tensors")
+        res = TokenScores(*out, *(None,) * (5 - len(out)))
+        want = ((tshape, torch.float32), (tshape, torch.int32), (shape, torch.float32),
+                ((*shape, n) if n else None, torch.int32), ((*shape, n) if n else None, torch.float32))
+        for o, (w, dt), name in zip(res, want, res._fields):
+            if (o is None) != (w is None):
+                raise ValueError(f"out must {'not ' if w is None else ''}hold {name}")
+            if o is not None and not _checked(o, torch.Size(w), dt, device).is_contiguous():
+                raise ValueError("out must be packed tensors")
+        _written(tuple(o for o in res if o is not None))
+    need = _token_bytes(code, rows, V, C, n)
+    work = _workspace(need, device, other)
+    dst = _TokenScoresOut(*(_p(o) for o in res))
+    _check(lib.wfst_token_scores(scores.data_ptr(), code, step, rows, V, _p(tokens), C, n, float(t), _p(ts),
+                                 _p(lengths), T, ctypes.byref(dst), _p(work), need, raw))
     return res
