@@ -17,9 +17,11 @@ namespace {
 
 typedef unsigned long long u64;
 
+
 constexpr int kTokenWaves = 4;                 // wavefronts of a row (or of a piece of one)
 constexpr int kTokenThreads = kTokenWaves * kWaveSize;
 constexpr int kMaxPieces = 64;                 // pieces of one row
+constexpr int kTokenGrid = 4096;               // workgroups of a launch: each takes several rows where there are more
 
 // Order of labels as integers: larger scores first, then lower indexes; 0: none
 // (-inf, NaN). One zero.
@@ -37,13 +39,19 @@ __device__ __forceinline__ int count(bool b) { return __popcll(__ballot(b)); }
 
 // What a row's temperature makes of its distances. Where z - m could pass binary32's
 // range, half of it is taken times 2 / T. T below 2^-125 counts as that for the sums.
+constexpr float kLog2e = 1.44269504088896341f;
+
 struct Heat { float t, scale; };
 
 __device__ __forceinline__ Heat row_heat(const TokenCall &c, int64_t r)
 {
-    float t = c.temperatures ? c.temperatures[r] : c.temperature;
-    t = t > 0.0f ? fminf(t, 3.402823466e38f) : 0.0f;
-    return {t, 1.44269504088896341f / fmaxf(t, 0x1p-125f)};
+    float t = c.temperature, scale = c.scale;
+    if (c.temperatures) {
+        t = c.temperatures[r];
+        t = t > 0.0f ? fminf(t, 3.402823466e38f) : 0.0f;
+        scale = kLog2e / fmaxf(t, 0x1p-125f);
+    }
+    return {t, scale};
 }
 
 struct Base { float half, mh, scale; };        // y = (z half - mh) scale
@@ -51,10 +59,17 @@ struct Base { float half, mh, scale; };        // y = (z half - mh) scale
 __device__ __forceinline__ Base base_of(float m, const Heat &h)
 {
     const float half = m > 0x1p100f ? 0.5f : 1.0f;
-    return {half, m * half, h.scale / half};
+    return {half, m * half, m > 0x1p100f ? 2.0f * h.scale : h.scale};
 }
 
 __device__ __forceinline__ float below(float z, const Base &b) { return fmaf(z, b.half, -b.mh) * b.scale; }
+
+// The next smaller number, for a number above -inf.
+__device__ __forceinline__ float next_below(float a)
+{
+    const uint32_t u = __float_as_uint(a);
+    return __uint_as_float(u << 1 == 0 ? 0x80000001u : u & 0x80000000u ? u + 1 : u - 1);
+}
 
 // Statistics of a set of z: the largest, how many equal it, and over the others the
 // sums of e = 2^y and of e y. +inf as the largest says that the set has a NaN or +inf.
@@ -84,6 +99,14 @@ __device__ __forceinline__ TokenStat stat_join(const TokenStat &a, const TokenSt
     return r;
 }
 
+// log(1 + x) for x >= 0: the logarithm of the rounded u = 1 + x and, times 1 / u, what
+// the rounding lost (x itself where u is 1).
+__device__ __forceinline__ float log1p_of(float x)
+{
+    const float u = 1.0f + x;
+    return fmaf(x - (u - 1.0f), __builtin_amdgcn_rcpf(u), 0.693147180559945309f * __builtin_amdgcn_logf(u));
+}
+
 // What a row's results need of its statistics.
 struct TokenRow { float m, half, t, lz, entropy; };
 
@@ -93,8 +116,8 @@ __device__ __forceinline__ TokenRow row_result(const TokenStat &s, const Heat &h
     if (s.m == INFINITY) {
         r.lz = r.entropy = NAN;
     } else if (s.m > -INFINITY && h.t > 0.0f) {
-        r.lz = log1pf((s.ones - 1.0f) + s.sum);
-        r.entropy = r.lz - 0.693147180559945309f * (s.ysum / (s.ones + s.sum));
+        r.lz = log1p_of((s.ones - 1.0f) + s.sum);
+        r.entropy = fmaf(-0.693147180559945309f * s.ysum, __builtin_amdgcn_rcpf(s.ones + s.sum), r.lz);
     }
     return r;
 }
@@ -104,7 +127,8 @@ __device__ __forceinline__ float log_prob(const TokenRow &r, float z, int rank)
     if (r.lz != r.lz) return NAN;
     if (!(z > -INFINITY)) return -INFINITY;
     if (r.t == 0.0f) return rank == 0 ? 0.0f : -INFINITY;
-    return fmaf(z, r.half, -r.m * r.half) / r.t / r.half - r.lz;
+    const float d = fmaf(z, r.half, -r.m * r.half);
+    return (r.t == 1.0f ? d : d / r.t) * (r.half == 1.0f ? 1.0f : 2.0f) - r.lz;
 }
 
 // The n-th largest (at least) of the keys that WORDS words of each lane hold (0:
@@ -131,10 +155,10 @@ template <int WAVES> struct TokenShared {
     int32_t at[WAVES > 1 ? WAVES * kWaveSize : 1];      // where it stands first
     float red[4 * WAVES];
     int32_t ranks[WAVES > 1 ? kMaxTokens : 1];
-    float scores[WAVES > 1 ? kMaxTokens : 1];
     int32_t listed;
 };
 
+// All lanes of the row have passed their LDS accesses.
 template <int WAVES>
 __device__ __forceinline__ void row_sync()
 {
@@ -163,278 +187,383 @@ __device__ __forceinline__ TokenWork token_work(void *w, int64_t items, int32_t 
     return r;
 }
 
+// NV packs a thread of a run of labels that begins at `first`; the thread's first
+// label is v0. A pack that crosses V is read from V - VEC on, its labels that belong
+// to the pack before it are -inf then.
 template <typename XT, int WAVES, int NV>
+struct TokenRun {
+    static constexpr int VEC = kTokenVec<XT>;
+    static constexpr int kSpan = WAVES * kWaveSize * VEC;
+    float z[NV][VEC], pm[NV];                           // pm: each pack's largest
+    float mine;                                         // the thread's
+    int first, v0, tid, V;
+
+    // The label of element j of pack i.
+    __device__ __forceinline__ int label(int i, int j) const { return min(v0 + i * kSpan, max(V - VEC, 0)) + j; }
+
+    // Pack i of this wavefront holds labels (the same for all its lanes).
+    __device__ __forceinline__ bool used(int i) const
+    {
+        return __builtin_amdgcn_readfirstlane(v0) + i * kSpan < V;
+    }
+
+    __device__ __forceinline__ void load(const XT *x, int labels, int f, int t)
+    {
+        asm volatile("" : "+v"(t));     // (else labels' numbers are kept in registers from row to row)
+        first = f;
+        tid = t;
+        V = labels;
+        v0 = f + t * VEC;
+        Pack<XT, VEC> p[NV];
+        if (V >= VEC) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) p[i] = *(const Pack<XT, VEC> *)(x + label(i, 0));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) p[i].v[j] = j < V ? x[j] : (XT)-INFINITY;
+        }
+        mine = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) z[i][j] = (float)p[i].v[j];
+            if (first + (i + 1) * kSpan > V) {          // (the last packs of a row)
+                const int before = v0 + i * kSpan - label(i, 0);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) z[i][j] = j >= before ? z[i][j] : -INFINITY;
+            }
+            pm[i] = z[i][0];
+#pragma unroll
+            for (int j = 1; j < VEC; ++j) pm[i] = fmaxf(pm[i], z[i][j]);
+            mine = fmaxf(mine, pm[i]);
+        }
+    }
+
+    // The sums below the row's largest over this wavefront's labels; TOP: it holds that
+    // largest, whose entries are counted and left out.
+    template <bool TOP>
+    __device__ __forceinline__ void add_up(const Base &base, TokenStat &s) const
+    {
+        uint32_t others = 0, packs = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!used(i)) continue;
+            ++packs;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float y = below(z[i][j], base), e = __builtin_amdgcn_exp2f(y);
+                const bool other = !TOP || z[i][j] != s.m;
+                if (TOP) others += count(other);        // (on the scalar unit)
+                s.sum += other ? e : 0.0f;
+                s.ysum = fmaf(e, fmaxf(y, -200.0f), s.ysum);
+            }
+        }
+        if (TOP) s.ones = (float)(packs * VEC * kWaveSize - others);
+    }
+
+    // A wavefront's part of the sums below the row's or run's largest, s.m (a NaN as its sum).
+    __device__ __forceinline__ void sums(const Heat &heat, float wave_max, TokenStat &s) const
+    {
+        s.ones = s.sum = s.ysum = 0.0f;
+        if (s.m > -INFINITY && heat.t > 0.0f) {
+            const Base base = base_of(s.m, heat);
+            if (WAVES == 1 || wave_max == s.m) add_up<true>(base, s);
+            else add_up<false>(base, s);
+        } else {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) nan |= z[i][j] != z[i][j];
+            s.sum = nan ? NAN : 0.0f;
+        }
+        s.sum = wave_sum_f(s.sum);
+        s.ysum = wave_sum_f(s.ysum);
+    }
+
+    // A wavefront's labels before the token `at` of score a (a label, or a = -inf).
+    // Packs before the token's own count its equals too, by the next smaller score as
+    // their bound; the wavefront `home` looks at the token's own pack. NaN and -inf
+    // stand last, by index.
+    __device__ __forceinline__ int before(const XT *x, float a, int at, bool home) const
+    {
+        int got = 0;
+        if (a > -INFINITY) {
+            const float down = next_below(a);
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                if (!used(q)) continue;
+                const float over = at - v0 >= q * kSpan + VEC ? down : a;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) got += z[q][j] > over;
+            }
+            const int pack = at / VEC * VEC, lane = tid & 63;
+            if (home && pack >= first && pack < first + kSpan * NV && lane < VEC && pack + lane < at)
+                got += (float)x[pack + lane] == a;
+        } else {
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) got += z[q][j] > -INFINITY || (v0 + q * kSpan <= label(q, j) && label(q, j) < at);
+        }
+        return wave_sum_i(got);
+    }
+
+    // Appends the labels that may be among the n best to the list (kept of them there,
+    // sorted): the ones that reach the n-th largest of the threads' own largest, at
+    // most n threads' labels. sh.top holds those and sh.listed is `kept`.
+    __device__ __forceinline__ void candidates(TokenShared<WAVES> &sh, u64 *list, int n, int kept) const
+    {
+        const int lane = tid & 63;
+        uint32_t u[WAVES];
+#pragma unroll
+        for (int q = 0; q < WAVES; ++q) u[q] = WAVES > 1 ? sh.top[q * kWaveSize + lane] : score_key(mine);
+        int reach, last = 0x7FFFFFFF;
+        const uint32_t bound = nth_key<uint32_t, WAVES>(u, n, reach);
+        if (reach > n) {                                // (the same for the whole row)
+            // more threads tie at the bound than are needed: those whose largest stands first
+            int at = 0x7FFFFFFF;
+#pragma unroll
+            for (int i = NV - 1; i >= 0; --i)
+#pragma unroll
+                for (int j = VEC - 1; j >= 0; --j)
+                    if (z[i][j] == mine) at = label(i, j);
+            if (WAVES > 1) {
+                sh.at[tid] = at;
+                row_sync<WAVES>();
+            }
+            uint32_t early[WAVES];                      // (the earliest is the largest)
+            int more = 0;
+#pragma unroll
+            for (int q = 0; q < WAVES; ++q) {
+                early[q] = u[q] == bound ? ~(uint32_t)(WAVES > 1 ? sh.at[q * kWaveSize + lane] : at) : 0u;
+                more += count(u[q] > bound);
+            }
+            int got;
+            last = (int)~nth_key<uint32_t, WAVES>(early, n - more, got);
+        }
+        float lo = key_score(max(bound, 0x00800000u));
+        if (kept == n) {                                // (later labels only pass with a larger score)
+            const float run = key_score((uint32_t)(list[n - 1] >> 32));
+            if (run >= lo) { lo = run; last = -1; }
+        }
+        if (!__ballot(mine >= lo)) return;
+        if (last == 0x7FFFFFFF) append<false>(sh, list, lo, last);
+        else append<true>(sh, list, lo, last);
+    }
+
+    // Labels above lo, or of lo itself and not behind `last` (FIRST; else all of lo).
+    template <bool FIRST>
+    __device__ __forceinline__ void append(TokenShared<WAVES> &sh, u64 *list, float lo, int last) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!__ballot(pm[i] >= lo)) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if (z[i][j] >= lo && (!FIRST || z[i][j] > lo || label(i, j) <= last))
+                    list[atomicAdd(&sh.listed, 1)] = label_key(z[i][j], label(i, j));
+        }
+    }
+};
+
+// Calls f(place, key) for the first n keys of a list in their order, by the threads of a row.
+template <int WAVES, typename F>
+__device__ __forceinline__ void best_of(const u64 *list, int L, int n, int tid, F &&f)
+{
+    for (int i = tid; i < L; i += WAVES * kWaveSize) {
+        const u64 k = list[i];
+        int place = 0;
+        for (int q = 0; q < L; ++q) place += list[q] > k;
+        if (place < n) f(place, k);
+    }
+}
+
+__device__ __forceinline__ void write_token(const TokenCall &c, const TokenRow &row, int64_t i, bool is, float z, int before)
+{
+    c.log_probs[i] = is ? log_prob(row, z, before) : -INFINITY;
+    c.ranks[i] = is ? before : -1;
+}
+
+__device__ __forceinline__ void write_top(const TokenCall &c, const TokenRow &row, int64_t r, int place, u64 k)
+{
+    c.top_tokens[r * c.top_n + place] = (int32_t)~(uint32_t)k;
+    c.top_log_probs[r * c.top_n + place] = log_prob(row, key_score((uint32_t)(k >> 32)), place);
+}
+
+__device__ __forceinline__ void write_no_top(const TokenCall &c, int64_t r, int place)
+{
+    c.top_tokens[r * c.top_n + place] = -1;
+    c.top_log_probs[r * c.top_n + place] = -INFINITY;
+}
+
+// A given token and its score, a lane each from the i-th on (-inf: no label).
+template <typename XT>
+__device__ __forceinline__ void load_tokens(const XT *x, const int32_t *tokens, int V, int i, int C, int &tok, float &zt)
+{
+    const int lane = threadIdx.x & 63;
+    tok = i + lane < C ? tokens[i + lane] : -1;
+    zt = tok >= 0 && tok < V ? (float)x[tok] : -INFINITY;
+}
+
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// A row a wavefront, four to a workgroup, no barriers.
+template <typename XT, int NV>
+__global__ __launch_bounds__(kTokenThreads) void k_token_short(TokenCall c, int32_t room)
+{
+    __shared__ TokenShared<1> shared[kTokenWaves];
+    extern __shared__ __align__(16) u64 lists[];
+    const int lane = threadIdx.x & 63, slot = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    TokenShared<1> &sh = shared[slot];
+    u64 *list = lists + (size_t)slot * room;
+    for (int64_t r = (int64_t)blockIdx.x * kTokenWaves + slot; r < c.rows; r += (int64_t)gridDim.x * kTokenWaves) {
+        if (!row_active(c.set, r)) continue;
+        const XT *x = (const XT *)c.x + r * c.x_stride;
+        const int32_t *tokens = c.tokens + r * c.C;
+        const Heat heat = row_heat(c, r);
+        TokenRun<XT, 1, NV> run;
+        run.load(x, c.V, 0, lane);
+        int tok;
+        float zt;
+        load_tokens<XT>(x, tokens, c.V, 0, c.C, tok, zt);
+        TokenStat s;
+        s.m = wave_max_f(run.mine);
+        run.sums(heat, s.m, s);
+        if (s.sum != s.sum) s.m = INFINITY;
+        const TokenRow row = row_result(s, heat);
+        if (lane == 0 && c.entropies) c.entropies[r] = row.entropy;
+        for (int i = 0; i < c.C; i += kWaveSize) {
+            if (i) load_tokens<XT>(x, tokens, c.V, i, c.C, tok, zt);
+            int before = 0;
+            const int m = min(c.C - i, kWaveSize);
+            for (int k = 0; k < m; ++k) {
+                const int got = run.before(x, read_lane(zt, k), __builtin_amdgcn_readlane(tok, k), true);
+                before = k == lane ? got : before;
+            }
+            if (lane < m) write_token(c, row, r * c.C + i + lane, tok >= 0 && tok < c.V, zt, before);
+        }
+        if (c.top_n) {
+            if (lane == 0) sh.listed = 0;
+            row_sync<1>();
+            run.candidates(sh, list, c.top_n, 0);
+            row_sync<1>();
+            const int L = sh.listed;
+            best_of<1>(list, L, c.top_n, lane, [&](int place, u64 k) { write_top(c, row, r, place, k); });
+            for (int i = L + lane; i < c.top_n; i += kWaveSize) write_no_top(c, r, i);
+            row_sync<1>();
+        }
+    }
+}
+
+// A row, or (CUT) a piece of one, a workgroup.
+template <typename XT, int NV, bool CUT>
 __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, TokenPlan plan)
 {
-    constexpr int VEC = kTokenVec<XT>;
-    constexpr int kSpan = WAVES * kWaveSize * VEC;
-    constexpr int kRows = kTokenWaves / WAVES;          // rows of a workgroup
-    __shared__ TokenShared<WAVES> shared[kRows];
-    extern __shared__ __align__(16) u64 lists[];
-    const int lane = threadIdx.x & 63, slot = WAVES > 1 ? 0 : threadIdx.x >> 6;
-    const int tid = WAVES > 1 ? threadIdx.x : lane, wave = WAVES > 1 ? threadIdx.x >> 6 : 0;
-    TokenShared<WAVES> &sh = shared[slot];
-    u64 *list = lists + (size_t)slot * plan.list, *best = list + plan.list - c.top_n;
+    constexpr int WAVES = kTokenWaves;
+    typedef TokenRun<XT, WAVES, NV> Run;
+    constexpr int kLen = Run::kSpan * NV;
+    __shared__ TokenShared<WAVES> sh;
+    extern __shared__ __align__(16) u64 list[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = c.top_n, C = c.C;
-    const int64_t items = c.rows * plan.pieces;
-    const TokenWork work = token_work(c.workspace, items, n);
+    const int64_t items = CUT ? c.rows * plan.pieces : c.rows;
+    const TokenWork work = CUT ? token_work(c.workspace, items, n) : TokenWork{};
 
-    for (int64_t w = (int64_t)blockIdx.x * kRows + slot; w < items; w += (int64_t)gridDim.x * kRows) {
-        const int64_t r = plan.pieces > 1 ? w / plan.pieces : w;
-        const int piece = (int)(w - r * plan.pieces);
+    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+        const int64_t r = CUT ? w / plan.pieces : w;
+        const int begin = CUT ? (int)(w - r * plan.pieces) * plan.subs * kLen : 0;
         if (!row_active(c.set, r)) continue;
         const XT *x = (const XT *)c.x + r * c.x_stride;
         const int32_t *tokens = c.tokens + r * C;
         const Heat heat = row_heat(c, r);
-
-        // the given tokens, a lane each, and their scores
-        int tok = lane < C ? tokens[lane] : -1;
-        float zt = tok >= 0 && tok < c.V ? (float)x[tok] : -INFINITY;
+        int tok;
+        float zt;
+        load_tokens<XT>(x, tokens, c.V, 0, C, tok, zt);
 
         TokenStat all = {-INFINITY, 0.0f, 0.0f, 0.0f};
         int kept = 0;                                   // keys at the head of the list, sorted
-        for (int sub = 0; sub < plan.subs; ++sub) {
-            const int first = (piece * plan.subs + sub) * (kSpan * NV);
-            if (first >= c.V) break;
-            const int v0 = first + tid * VEC;
-            float z[NV][VEC];
+        for (int sub = 0; sub < (CUT ? plan.subs : 1); ++sub) {
+            const int first = begin + sub * kLen;
+            if (CUT && first >= c.V) break;
+            const bool more = CUT && sub + 1 < plan.subs && first + kLen < c.V;
+            Run run;
+            run.load(x, c.V, first, tid);
+            TokenStat s;
+            const float wave_max = wave_max_f(run.mine);
+            s.m = wave_max;
+            if (n) sh.top[tid] = score_key(run.mine);
+            if (lane == 0) sh.red[wave] = s.m;
+            if (tid == 0) sh.listed = kept;
+            if (sub == 0)
+                for (int i = tid; i < C; i += kTokenThreads) sh.ranks[i] = 0;
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = v0 + i * kSpan;
-                if (v + VEC <= c.V) {
-                    const Pack<XT, VEC> p = *(const Pack<XT, VEC> *)(x + v);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) z[i][j] = (float)p.v[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) z[i][j] = v + j < c.V ? (float)x[v + j] : -INFINITY;
-                }
-            }
-            TokenStat s = {-INFINITY, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) s.m = fmaxf(s.m, z[i][j]);
-            const float mine = s.m;
-            s.m = wave_max_f(s.m);
-            if (WAVES > 1) {
-                if (n) sh.top[tid] = score_key(mine);
-                if (lane == 0) sh.red[wave] = s.m;
-                if (tid == 0) sh.listed = kept;
-                if (sub == 0)
-                    for (int i = tid; i < C; i += kTokenThreads) sh.ranks[i] = 0;
-                row_sync<WAVES>();
-#pragma unroll
-                for (int q = 0; q < WAVES; ++q) s.m = fmaxf(s.m, sh.red[q]);
-            } else if (tid == 0) {
-                sh.listed = 0;
-            }
-
-            // sums
-            if (s.m > -INFINITY && heat.t > 0.0f) {
-                const Base base = base_of(s.m, heat);
-                uint32_t ones = 0;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float y = below(z[i][j], base), e = __builtin_amdgcn_exp2f(y);
-                        const bool top = z[i][j] == s.m;
-                        ones += count(top);             // (on the scalar unit)
-                        s.sum += top ? 0.0f : e;
-                        s.ysum = fmaf(e, fmaxf(y, -200.0f), s.ysum);
-                    }
-                s.ones = (float)ones;
-            } else {
-                bool nan = false;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) nan |= z[i][j] != z[i][j];
-                s.sum = nan ? NAN : 0.0f;
-            }
-            s.sum = wave_sum_f(s.sum);
-            s.ysum = wave_sum_f(s.ysum);
-            if (WAVES > 1 && lane == 0) {
+            for (int q = 0; q < WAVES; ++q) s.m = fmaxf(s.m, sh.red[q]);
+            run.sums(heat, wave_max, s);
+            if (lane == 0) {
                 sh.red[WAVES + wave] = s.sum;
                 sh.red[2 * WAVES + wave] = s.ysum;
                 sh.red[3 * WAVES + wave] = s.ones;
             }
-
-            // ranks: labels of this run before each token
-            int before = 0;
-            for (int i = 0; i < C; ++i) {
-                if (i && i % kWaveSize == 0) {          // (the next 64 tokens)
-                    tok = i + lane < C ? tokens[i + lane] : -1;
-                    zt = tok >= 0 && tok < c.V ? (float)x[tok] : -INFINITY;
+            for (int i = 0; i < C; i += kWaveSize) {
+                if (C > kWaveSize && (i || sub)) load_tokens<XT>(x, tokens, c.V, i, C, tok, zt);
+                int before = 0;
+                const int m = min(C - i, kWaveSize);
+                for (int k = 0; k < m; ++k) {
+                    const int got = run.before(x, read_lane(zt, k), __builtin_amdgcn_readlane(tok, k), wave == 0);
+                    before = k == lane ? got : before;
                 }
-                const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(zt), i % kWaveSize));
-                const int at = __builtin_amdgcn_readlane(tok, i % kWaveSize);
-                int got = 0;
-                if (a > -INFINITY) {
-#pragma unroll
-                    for (int q = 0; q < NV; ++q)
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            got += count(z[q][j] > a);
-                            if (__ballot(z[q][j] == a)) got += count(z[q][j] == a && v0 + q * kSpan + j < at);
-                        }
-                } else {                                // (-inf and NaN stand last, by index)
-#pragma unroll
-                    for (int q = 0; q < NV; ++q)
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j)
-                            got += count(z[q][j] > -INFINITY || v0 + q * kSpan + j < at);
-                }
-                before = i % kWaveSize == lane ? got : before;
-                if (i % kWaveSize == kWaveSize - 1 || i == C - 1) {
-                    const int k = i / kWaveSize * kWaveSize + lane;
-                    if (WAVES > 1) {
-                        if (k < C) {
-                            atomicAdd(&sh.ranks[k], before);
-                            if (wave == 0) sh.scores[k] = zt;
-                        }
-                    } else if (k < C) {
-                        TokenStat f = s;
-                        if (f.sum != f.sum) f.m = INFINITY;
-                        const TokenRow row = row_result(f, heat);
-                        const bool is = tok >= 0 && tok < c.V;
-                        c.log_probs[r * C + k] = is ? log_prob(row, zt, before) : -INFINITY;
-                        c.ranks[r * C + k] = is ? before : -1;
-                    }
-                }
+                if (lane < m) atomicAdd(&sh.ranks[i + lane], before);
             }
-            if (C > kWaveSize && sub + 1 < plan.subs) {
-                tok = tokens[lane];
-                zt = tok >= 0 && tok < c.V ? (float)x[tok] : -INFINITY;
-            }
-
-            // labels that may be among the n best: those that reach the bound
-            if (n) {
-                int reach;
-                uint32_t bound;
-                uint32_t u[WAVES];
+            if (n) run.candidates(sh, list, n, kept);
+            __syncthreads();
+            s.sum = s.ysum = s.ones = 0.0f;
 #pragma unroll
-                for (int q = 0; q < WAVES; ++q) u[q] = WAVES > 1 ? sh.top[q * kWaveSize + lane] : score_key(mine);
-                bound = nth_key<uint32_t, WAVES>(u, n, reach);
-                // more threads tie at the bound than are needed: those whose largest stands first
-                int last = 0x7FFFFFFF;
-                const bool tie = reach > n;             // (the same for the whole row)
-                if (tie) {
-                    int at = 0x7FFFFFFF;
-#pragma unroll
-                    for (int i = NV - 1; i >= 0; --i)
-#pragma unroll
-                        for (int j = VEC - 1; j >= 0; --j)
-                            if (z[i][j] == mine) at = v0 + i * kSpan + j;
-                    if (WAVES > 1) {
-                        sh.at[tid] = at;
-                        row_sync<WAVES>();
-                    }
-                    uint32_t late[WAVES];               // (the earliest is the largest)
-                    int more = 0;
-#pragma unroll
-                    for (int q = 0; q < WAVES; ++q) {
-                        late[q] = u[q] == bound ? ~(uint32_t)(WAVES > 1 ? sh.at[q * kWaveSize + lane] : at) : 0u;
-                        more += count(u[q] > bound);
-                    }
-                    int got;
-                    last = (int)~nth_key<uint32_t, WAVES>(late, n - more, got);
-                }
-                float lo = key_score(max(bound, 0x00800000u));
-                if (kept == n) {                        // (later labels only pass with a larger score)
-                    const float run = key_score((uint32_t)(list[n - 1] >> 32));
-                    if (run >= lo) { lo = run; last = -1; }
-                }
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const int v = v0 + i * kSpan + j;
-                        bool hit = z[i][j] >= lo;
-                        u64 mask = __ballot(hit);
-                        if (!mask) continue;
-                        if (last != 0x7FFFFFFF) {
-                            hit = hit && (z[i][j] > lo || v <= last);
-                            mask = __ballot(hit);
-                            if (!mask) continue;
-                        }
-                        int base = 0;
-                        if (lane == 0) base = atomicAdd(&sh.listed, __popcll(mask));
-                        base = __builtin_amdgcn_readfirstlane(base);
-                        const int k = base + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
-                                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-                        if (hit) list[k] = label_key(z[i][j], v);
-                    }
-            }
-            row_sync<WAVES>();
-            if (WAVES > 1) {
-                s.sum = s.ysum = s.ones = 0.0f;
-#pragma unroll
-                for (int q = 0; q < WAVES; ++q) {
-                    s.sum += sh.red[WAVES + q];
-                    s.ysum += sh.red[2 * WAVES + q];
-                    s.ones += sh.red[3 * WAVES + q];
-                }
+            for (int q = 0; q < WAVES; ++q) {
+                s.sum += sh.red[WAVES + q];
+                s.ysum += sh.red[2 * WAVES + q];
+                s.ones += sh.red[3 * WAVES + q];
             }
             if (s.sum != s.sum) s.m = INFINITY;
-            all = sub == 0 ? s : stat_join(all, s, heat);
-
-            // the list sorted: each key counts the larger ones
-            if (n) {
-                const int L = sh.listed;
-                const bool more = sub + 1 < plan.subs && first + kSpan * NV < c.V;
-                const bool final = plan.pieces == 1 && !more;
-                TokenRow row;
-                if (final) row = row_result(all, heat);
-                for (int i = tid; i < L; i += WAVES * kWaveSize) {
-                    const u64 k = list[i];
-                    int rank = 0;
-                    for (int q = 0; q < L; ++q) rank += list[q] > k;
-                    if (rank >= n) continue;
-                    if (final) {
-                        const float f = key_score((uint32_t)(k >> 32));
-                        c.top_tokens[r * n + rank] = (int32_t)~(uint32_t)k;
-                        c.top_log_probs[r * n + rank] = log_prob(row, f, rank);
-                    } else if (!more) {
-                        work.keys[w * n + rank] = k;
-                    } else {
-                        best[rank] = k;
-                    }
-                }
-                if (!more) {
-                    for (int i = L + tid; i < n; i += WAVES * kWaveSize) {
-                        if (final) {
-                            c.top_tokens[r * n + i] = -1;
-                            c.top_log_probs[r * n + i] = -INFINITY;
-                        } else {
-                            work.keys[w * n + i] = 0;
-                        }
-                    }
-                } else {
-                    row_sync<WAVES>();
-                    kept = min(L, n);
-                    for (int i = tid; i < kept; i += WAVES * kWaveSize) list[i] = best[i];
-                }
+            all = CUT && sub ? stat_join(all, s, heat) : s;
+            const int L = sh.listed;
+            if (more && n) {                            // the best so far to the head of the list
+                u64 *best = list + plan.list - n;
+                best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { best[place] = k; });
+                __syncthreads();
+                kept = min(L, n);
+                for (int i = tid; i < kept; i += kTokenThreads) list[i] = best[i];
             }
-            if (WAVES > 1) row_sync<WAVES>();
+            if (more) __syncthreads();
         }
 
-        if (plan.pieces > 1) {
+        const int L = sh.listed;
+        if constexpr (CUT) {
+            best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { work.keys[w * n + place] = k; });
+            for (int i = L + tid; i < n; i += kTokenThreads) work.keys[w * n + i] = 0;
             if (tid == 0) work.stats[w] = all;
-            for (int i = tid; i < C; i += WAVES * kWaveSize) work.ranks[w * C + i] = sh.ranks[i];
+            for (int i = tid; i < C; i += kTokenThreads) work.ranks[w * C + i] = sh.ranks[i];
         } else {
             const TokenRow row = row_result(all, heat);
+            if (n) {
+                best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { write_top(c, row, r, place, k); });
+                for (int i = L + tid; i < n; i += kTokenThreads) write_no_top(c, r, i);
+            }
             if (tid == 0 && c.entropies) c.entropies[r] = row.entropy;
-            if (WAVES > 1)
-                for (int i = tid; i < C; i += kTokenThreads) {
-                    const int t = tokens[i];
-                    const bool is = t >= 0 && t < c.V;
-                    c.log_probs[r * C + i] = is ? log_prob(row, sh.scores[i], sh.ranks[i]) : -INFINITY;
-                    c.ranks[r * C + i] = is ? sh.ranks[i] : -1;
+            if (wave == WAVES - 1)                      // (the list's first keys lie with the first)
+                for (int i = 0; i < C; i += kWaveSize) {
+                    if (C > kWaveSize) load_tokens<XT>(x, tokens, c.V, i, C, tok, zt);
+                    if (i + lane < C)
+                        write_token(c, row, r * C + i + lane, tok >= 0 && tok < c.V, zt, sh.ranks[i + lane]);
                 }
         }
-        row_sync<WAVES>();
+        __syncthreads();
     }
 }
 
@@ -471,8 +600,7 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32
                 z = xcode == kF32 ? ((const float *)c.x)[at] : xcode == kF16 ? (float)((const _Float16 *)c.x)[at]
                                                                             : (float)((const __bf16 *)c.x)[at];
             }
-            c.log_probs[r * C + i] = is ? log_prob(row, z, before) : -INFINITY;
-            c.ranks[r * C + i] = is ? before : -1;
+            write_token(c, row, r * C + i, is, z, before);
         }
         if (!n) continue;
         const u64 *keys = work.keys + r * P * n;
@@ -492,18 +620,8 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32
         }
         __syncthreads();
         const int L = listed;
-        for (int i = tid; i < L; i += kTokenThreads) {
-            const u64 k = list[i];
-            int rank = 0;
-            for (int q = 0; q < L; ++q) rank += list[q] > k;
-            if (rank >= n) continue;
-            c.top_tokens[r * n + rank] = (int32_t)~(uint32_t)k;
-            c.top_log_probs[r * n + rank] = log_prob(row, key_score((uint32_t)(k >> 32)), rank);
-        }
-        for (int i = L + tid; i < n; i += kTokenThreads) {
-            c.top_tokens[r * n + i] = -1;
-            c.top_log_probs[r * n + i] = -INFINITY;
-        }
+        best_of<kTokenWaves>(list, L, n, tid, [&](int place, u64 k) { write_top(c, row, r, place, k); });
+        for (int i = L + tid; i < n; i += kTokenThreads) write_no_top(c, r, i);
         __syncthreads();
     }
 }
@@ -513,44 +631,67 @@ struct TokenShape { int waves, nv, pieces, subs; };
 
 TokenShape token_shape(int64_t rows, int32_t V, int32_t x_dtype)
 {
-    const int vec = x_dtype == kF32 ? 4 : 8, lane = kWaveSize * vec;
+    const int vec = x_dtype == kF32 ? 4 : 8, most = 32 / vec, lane = kWaveSize * vec;
     const auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
-    if (V <= 8 * lane) return {1, V <= 2 * lane ? 2 : V <= 4 * lane ? 4 : 8, 1, 1};
+    if (V <= most * lane) return {1, up(V, lane) <= 4 ? up(V, lane) : most, 1, 1};
     const int span = kTokenWaves * lane;
-    if (V <= 8 * span) return {kTokenWaves, std::max(3, up(V, span)), 1, 1};
-    const int nv = rows * up(V, 8 * span) >= 512 ? 8 : 2, len = nv * span;
+    if (V <= most * span) return {kTokenWaves, std::max(2, up(V, span)), 1, 1};
+    const int nv = rows * up(V, most * span) >= 512 ? most : 2, len = nv * span;
     const int subs = up(up(V, len), kMaxPieces);
     return {kTokenWaves, nv, up(V, (int64_t)len * subs), subs};
 }
 
-template <typename XT, int WAVES, int NV>
+// u64 of a row's list in LDS: the labels of n threads, and twice the n best so far.
+int token_list(const TokenCall &c, int nv, int vec, bool cut)
+{
+    return c.top_n ? std::min(c.top_n * nv * vec, c.V) + (cut ? 2 * c.top_n : 0) : 0;
+}
+
+template <typename XT, int NV>
+void short_launch(const TokenCall &c, hipStream_t s)
+{
+    const int room = token_list(c, NV, kTokenVec<XT>, false);
+    const int64_t groups = (c.rows + kTokenWaves - 1) / kTokenWaves;
+    hipLaunchKernelGGL((k_token_short<XT, NV>), dim3((unsigned)std::min<int64_t>(groups, kTokenGrid)),
+                       dim3(kTokenThreads), (size_t)kTokenWaves * room * sizeof(u64), s, c, room);
+}
+
+template <typename XT, int NV, bool CUT>
 void rows_launch(const TokenCall &c, const TokenShape &t, hipStream_t s)
 {
-    const int rows = kTokenWaves / WAVES, each = NV * kTokenVec<XT>;
-    const int most = std::min(c.top_n * each, c.V);       // labels that reach the bound
-    const TokenPlan plan = {t.pieces, t.subs, c.top_n + most + c.top_n};
-    const size_t lds = c.top_n ? (size_t)rows * plan.list * sizeof(u64) : 0;
-    const int64_t groups = (c.rows * t.pieces + rows - 1) / rows;
-    hipLaunchKernelGGL((k_token_rows<XT, WAVES, NV>), dim3((unsigned)std::min<int64_t>(groups, kMaxRowGrid)),
-                       dim3(kTokenThreads), lds, s, c, plan);
+    const TokenPlan plan = {t.pieces, t.subs, token_list(c, NV, kTokenVec<XT>, CUT)};
+    const int64_t groups = c.rows * t.pieces;
+    hipLaunchKernelGGL((k_token_rows<XT, NV, CUT>), dim3((unsigned)std::min<int64_t>(groups, kTokenGrid)),
+                       dim3(kTokenThreads), (size_t)plan.list * sizeof(u64), s, c, plan);
 }
 
 template <typename XT>
 hipError_t token_launch(const TokenCall &c, hipStream_t s)
 {
+    constexpr int kMost = 32 / kTokenVec<XT>;
     const TokenShape t = token_shape(c.rows, c.V, c.x_dtype);
     if (t.waves == 1) {
-        if (t.nv == 2) rows_launch<XT, 1, 2>(c, t, s);
-        else if (t.nv == 4) rows_launch<XT, 1, 4>(c, t, s);
-        else rows_launch<XT, 1, 8>(c, t, s);
-    } else {
         switch (t.nv) {
-        case 2: rows_launch<XT, kTokenWaves, 2>(c, t, s); break;
-        case 3: rows_launch<XT, kTokenWaves, 3>(c, t, s); break;
-        case 4: rows_launch<XT, kTokenWaves, 4>(c, t, s); break;
-        case 5: rows_launch<XT, kTokenWaves, 5>(c, t, s); break;
-        case 6: rows_launch<XT, kTokenWaves, 6>(c, t, s); break;
-        default: rows_launch<XT, kTokenWaves, 8>(c, t, s); break;
+        case 1: short_launch<XT, 1>(c, s); break;
+        case 2: short_launch<XT, 2>(c, s); break;
+        case 3: short_launch<XT, 3>(c, s); break;
+        case 4: short_launch<XT, 4>(c, s); break;
+        default: short_launch<XT, kMost>(c, s); break;
+        }
+    } else if (t.pieces > 1) {
+        if (t.nv == 2) rows_launch<XT, 2, true>(c, t, s);
+        else rows_launch<XT, kMost, true>(c, t, s);
+    } else if (t.nv <= 4) {
+        switch (t.nv) {
+        case 2: rows_launch<XT, 2, false>(c, t, s); break;
+        case 3: rows_launch<XT, 3, false>(c, t, s); break;
+        default: rows_launch<XT, 4, false>(c, t, s); break;
+        }
+    } else if constexpr (kMost > 4) {
+        switch (t.nv) {
+        case 5: rows_launch<XT, 5, false>(c, t, s); break;
+        case 6: rows_launch<XT, 6, false>(c, t, s); break;
+        default: rows_launch<XT, 8, false>(c, t, s); break;
         }
     }
     if (t.pieces > 1)
@@ -568,8 +709,10 @@ size_t token_workspace(int64_t rows, int32_t V, int32_t C, int32_t top_n, int32_
     return (size_t)rows * t.pieces * (sizeof(TokenStat) + (size_t)top_n * sizeof(u64) + (size_t)C * 4);
 }
 
-hipError_t launch_token_scores(const TokenCall &c, hipStream_t s)
+hipError_t launch_token_scores(const TokenCall &call, hipStream_t s)
 {
+    TokenCall c = call;
+    c.scale = kLog2e / std::max(c.temperature, 0x1p-125f);
     if (c.x_dtype == kF32) return token_launch<float>(c, s);
     if (c.x_dtype == kF16) return token_launch<_Float16>(c, s);
     return token_launch<__bf16>(c, s);
