@@ -131,20 +131,22 @@ __device__ __forceinline__ float log_prob(const TokenRow &r, float z, int rank)
     return (r.t == 1.0f ? d : d / r.t) * (r.half == 1.0f ? 1.0f : 2.0f) - r.lz;
 }
 
-// The n-th largest (at least) of the keys that WORDS words of each lane hold (0:
-// none): the largest prefix of bits that n or more reach, all bits where more than n
-// do. reach: how many do. 0 where there are fewer.
-template <typename K, int WORDS>
-__device__ __forceinline__ K nth_key(const K (&u)[WORDS], int n, int &reach)
+// How many labels or threads may reach a bound that n have to.
+__host__ __device__ constexpr int bound_cap(int n) { return n + n / 4 + 2; }
+
+// A bound that n or more of a set of keys reach: the first prefix of bits, from the
+// highest on, that n to bound_cap(n) do, or with all bits the n-th largest key itself
+// (more of its kind may reach it). got(t): how many reach t. reach: how many reach the
+// result. 0 where there are fewer than n, or few keys at all.
+template <typename K, typename F>
+__device__ __forceinline__ K nth_key(int n, int all, int &reach, F &&got)
 {
     K b = 0;
-    reach = 0;
-    for (int bit = 8 * (int)sizeof(K) - 1; bit >= 0 && reach != n; --bit) {
+    reach = all;
+    for (int bit = 8 * (int)sizeof(K) - 1; bit >= 0 && reach > bound_cap(n); --bit) {
         const K t = b | (K)1 << bit;
-        int got = 0;
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) got += count(u[w] >= t);
-        if (got >= n) { b = t; reach = got; }
+        const int g = got(t);
+        if (g >= n) { b = t; reach = g; }
     }
     return b;
 }
@@ -187,6 +189,11 @@ __device__ __forceinline__ TokenWork token_work(void *w, int64_t items, int32_t 
     return r;
 }
 
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
 // NV packs a thread of a run of labels that begins at `first`; the thread's first
 // label is v0. A pack that crosses V is read from V - VEC on, its labels that belong
 // to the pack before it are -inf then.
@@ -198,8 +205,17 @@ struct TokenRun {
     float mine;                                         // the thread's
     int first, v0, tid, V;
 
-    // The label of element j of pack i.
-    __device__ __forceinline__ int label(int i, int j) const { return min(v0 + i * kSpan, max(V - VEC, 0)) + j; }
+    // The label of element j of pack i of the thread whose first label is v.
+    __device__ __forceinline__ int label(int v, int i, int j) const { return min(v + i * kSpan, max(V - VEC, 0)) + j; }
+
+    // v0 for use in a branch that few threads take: the compiler neither computes what
+    // follows from it before the branch nor keeps it from row to row (2.4 registers a label).
+    __device__ __forceinline__ int own_v0() const
+    {
+        int v = v0;
+        asm volatile("" : "+v"(v));
+        return v;
+    }
 
     // Pack i of this wavefront holds labels (the same for all its lanes).
     __device__ __forceinline__ bool used(int i) const
@@ -207,30 +223,42 @@ struct TokenRun {
         return __builtin_amdgcn_readfirstlane(v0) + i * kSpan < V;
     }
 
-    __device__ __forceinline__ void load(const XT *x, int labels, int f, int t)
+    struct __attribute__((packed, aligned(sizeof(XT)))) Raw { uint32_t w[4]; };
+    typedef Raw Packs[NV];
+
+    static __device__ __forceinline__ float element(const Raw &p, int j)
     {
-        asm volatile("" : "+v"(t));     // (else labels' numbers are kept in registers from row to row)
-        first = f;
-        tid = t;
-        V = labels;
-        v0 = f + t * VEC;
-        Pack<XT, VEC> p[NV];
+        if constexpr (sizeof(XT) == 4) return __uint_as_float(p.w[j]);
+        const uint32_t h = j & 1 ? p.w[j / 2] >> 16 : p.w[j / 2] & 0xFFFFu;
+        union { uint16_t u; _Float16 f; } c;
+        c.u = (uint16_t)h;
+        return __is_same(XT, _Float16) ? (float)c.f : __uint_as_float(h << 16);
+    }
+
+    static __device__ __forceinline__ void fetch(const XT *x, int V, int first, int tid, Packs &p)
+    {
         if (V >= VEC) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) p[i] = *(const Pack<XT, VEC> *)(x + label(i, 0));
+            for (int i = 0; i < NV; ++i) p[i] = *(const Raw *)(x + min(first + tid * VEC + i * kSpan, V - VEC));
         } else {
+            union { XT v[VEC]; Raw r; } u;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int j = 0; j < VEC; ++j) u.v[j] = j < V ? x[j] : (XT)-INFINITY;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) p[i].v[j] = j < V ? x[j] : (XT)-INFINITY;
+            for (int i = 0; i < NV; ++i) p[i] = u.r;
         }
+    }
+
+    __device__ __forceinline__ TokenRun(const Packs &p, int labels, int f, int t) : first(f), v0(f + t * VEC), tid(t), V(labels)
+    {
+        const int v = own_v0();
         mine = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) z[i][j] = (float)p[i].v[j];
+            for (int j = 0; j < VEC; ++j) z[i][j] = element(p[i], j);
             if (first + (i + 1) * kSpan > V) {          // (the last packs of a row)
-                const int before = v0 + i * kSpan - label(i, 0);
+                const int before = v + i * kSpan - label(v, i, 0);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) z[i][j] = j >= before ? z[i][j] : -INFINITY;
             }
@@ -283,10 +311,10 @@ struct TokenRun {
         s.ysum = wave_sum_f(s.ysum);
     }
 
-    // A wavefront's labels before the token `at` of score a (a label, or a = -inf).
-    // Packs before the token's own count its equals too, by the next smaller score as
-    // their bound; the wavefront `home` looks at the token's own pack. NaN and -inf
-    // stand last, by index.
+    // A lane's labels before the token `at` of score a (a label, or a = -inf). Packs
+    // before the token's own count its equals too, by the next smaller score as their
+    // bound; the wavefront `home` looks at the token's own pack. NaN and -inf stand
+    // last, by index.
     __device__ __forceinline__ int before(const XT *x, float a, int at, bool home) const
     {
         int got = 0;
@@ -303,46 +331,99 @@ struct TokenRun {
             if (home && pack >= first && pack < first + kSpan * NV && lane < VEC && pack + lane < at)
                 got += (float)x[pack + lane] == a;
         } else {
+            const int v = own_v0();
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) got += z[q][j] > -INFINITY || (v0 + q * kSpan <= label(q, j) && label(q, j) < at);
+                for (int j = 0; j < VEC; ++j)
+                    got += z[q][j] > -INFINITY || (v + q * kSpan <= label(v, q, j) && label(v, q, j) < at);
         }
-        return wave_sum_i(got);
+        return got;
+    }
+
+    // Of m tokens, a lane each, this wavefront's labels before them.
+    __device__ __forceinline__ int ranks(const XT *x, float zt, int tok, int m, bool home) const
+    {
+        const int lane = tid & 63;
+        int mine_of = 0;
+        for (int k = 0; k < m; k += 2) {                // (two counts below 2^16 in one sum)
+            int got = before(x, read_lane(zt, k), __builtin_amdgcn_readlane(tok, k), home);
+            if (k + 1 < m) got += before(x, read_lane(zt, k + 1), __builtin_amdgcn_readlane(tok, k + 1), home) << 16;
+            got = wave_sum_i(got);
+            mine_of = lane == k ? got & 0xFFFF : lane == k + 1 ? got >> 16 : mine_of;
+        }
+        return mine_of;
     }
 
     // Appends the labels that may be among the n best to the list (kept of them there,
-    // sorted): the ones that reach the n-th largest of the threads' own largest, at
-    // most n threads' labels. sh.top holds those and sh.listed is `kept`.
+    // sorted): the ones that reach a bound. sh.top holds the threads' largest and
+    // sh.listed is `kept`. The labels of at most bound_cap(n) threads are listed.
     __device__ __forceinline__ void candidates(TokenShared<WAVES> &sh, u64 *list, int n, int kept) const
     {
         const int lane = tid & 63;
-        uint32_t u[WAVES];
-#pragma unroll
-        for (int q = 0; q < WAVES; ++q) u[q] = WAVES > 1 ? sh.top[q * kWaveSize + lane] : score_key(mine);
         int reach, last = 0x7FFFFFFF;
-        const uint32_t bound = nth_key<uint32_t, WAVES>(u, n, reach);
-        if (reach > n) {                                // (the same for the whole row)
-            // more threads tie at the bound than are needed: those whose largest stands first
-            int at = 0x7FFFFFFF;
+        uint32_t bound;
+        if (WAVES == 1 && n > kWaveSize / 2) {
+            // threads are too few to bound with: the labels themselves
+            const auto got = [&](uint32_t t) {
+                const float lo = key_score(max(t, 0x00800000u));
+                int g = 0;
 #pragma unroll
-            for (int i = NV - 1; i >= 0; --i)
+                for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = VEC - 1; j >= 0; --j)
-                    if (z[i][j] == mine) at = label(i, j);
-            if (WAVES > 1) {
-                sh.at[tid] = at;
-                row_sync<WAVES>();
+                    for (int j = 0; j < VEC; ++j) g += count(z[i][j] >= lo);
+                return g;
+            };
+            bound = nth_key<uint32_t>(n, V, reach, got);
+            if (reach > bound_cap(n) && bound) {        // ties: the first of them
+                const float lo = key_score(bound);
+                const int v = own_v0();
+                const auto first_of = [&](int end) {
+                    int g = 0;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) g += count(z[i][j] > lo || (z[i][j] == lo && label(v, i, j) < end));
+                    return g;
+                };
+                last = 0;                               // (the n-th stands here)
+                for (int bit = 23; bit >= 0; --bit)
+                    if (first_of(last | 1 << bit) < n) last |= 1 << bit;
             }
-            uint32_t early[WAVES];                      // (the earliest is the largest)
-            int more = 0;
+        } else {
+            uint32_t u[WAVES];
 #pragma unroll
-            for (int q = 0; q < WAVES; ++q) {
-                early[q] = u[q] == bound ? ~(uint32_t)(WAVES > 1 ? sh.at[q * kWaveSize + lane] : at) : 0u;
-                more += count(u[q] > bound);
+            for (int q = 0; q < WAVES; ++q) u[q] = WAVES > 1 ? sh.top[q * kWaveSize + lane] : score_key(mine);
+            const auto reach_of = [&](const uint32_t (&k)[WAVES], uint32_t t) {
+                int g = 0;
+#pragma unroll
+                for (int q = 0; q < WAVES; ++q) g += count(k[q] >= t);
+                return g;
+            };
+            bound = nth_key<uint32_t>(n, WAVES * kWaveSize, reach, [&](uint32_t t) { return reach_of(u, t); });
+            if (reach > bound_cap(n) && bound) {        // (the same for the whole row)
+                // more threads tie at the bound than are needed: those whose largest stands first
+                int at = 0x7FFFFFFF;
+                const int v = own_v0();
+#pragma unroll
+                for (int i = NV - 1; i >= 0; --i)
+#pragma unroll
+                    for (int j = VEC - 1; j >= 0; --j)
+                        if (z[i][j] == mine) at = label(v, i, j);
+                if (WAVES > 1) {
+                    sh.at[tid] = at;
+                    row_sync<WAVES>();
+                }
+                uint32_t early[WAVES];                  // (the earliest is the largest)
+                int more = 0, got;
+#pragma unroll
+                for (int q = 0; q < WAVES; ++q) {
+                    early[q] = u[q] == bound ? ~(uint32_t)(WAVES > 1 ? sh.at[q * kWaveSize + lane] : at) : 0u;
+                    more += count(u[q] > bound);
+                }
+                last = (int)~nth_key<uint32_t>(n - more, WAVES * kWaveSize, got,
+                                               [&](uint32_t t) { return reach_of(early, t); });
             }
-            int got;
-            last = (int)~nth_key<uint32_t, WAVES>(early, n - more, got);
         }
         float lo = key_score(max(bound, 0x00800000u));
         if (kept == n) {                                // (later labels only pass with a larger score)
@@ -363,20 +444,31 @@ struct TokenRun {
             if (!__ballot(pm[i] >= lo)) continue;
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
-                if (z[i][j] >= lo && (!FIRST || z[i][j] > lo || label(i, j) <= last))
-                    list[atomicAdd(&sh.listed, 1)] = label_key(z[i][j], label(i, j));
+                if (z[i][j] >= lo) {
+                    const int v = label(own_v0(), i, j);
+                    if (!FIRST || z[i][j] > lo || v <= last) list[atomicAdd(&sh.listed, 1)] = label_key(z[i][j], v);
+                }
         }
     }
 };
 
-// Calls f(place, key) for the first n keys of a list in their order, by the threads of a row.
+// Calls f(place, key) for the first n of a list's L keys in their order, by the threads
+// of a row. Each wavefront first ends the list with 8 zeros for itself.
 template <int WAVES, typename F>
-__device__ __forceinline__ void best_of(const u64 *list, int L, int n, int tid, F &&f)
+__device__ __forceinline__ void best_of(u64 *list, int L, int n, int tid, F &&f)
 {
+    if ((tid & 63) < 8) list[L + (tid & 63)] = 0;
+    row_sync<1>();
     for (int i = tid; i < L; i += WAVES * kWaveSize) {
         const u64 k = list[i];
         int place = 0;
-        for (int q = 0; q < L; ++q) place += list[q] > k;
+        for (int q = 0; q < L; q += 8) {
+            u64 o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = list[q + j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) place += o[j] > k;
+        }
         if (place < n) f(place, k);
     }
 }
@@ -399,19 +491,33 @@ __device__ __forceinline__ void write_no_top(const TokenCall &c, int64_t r, int 
     c.top_log_probs[r * c.top_n + place] = -INFINITY;
 }
 
-// A given token and its score, a lane each from the i-th on (-inf: no label).
-template <typename XT>
-__device__ __forceinline__ void load_tokens(const XT *x, const int32_t *tokens, int V, int i, int C, int &tok, float &zt)
+// The i-th given token on, a lane each (-1: none), and their scores (-inf: no label).
+__device__ __forceinline__ int load_tokens(const int32_t *tokens, int i, int C)
 {
     const int lane = threadIdx.x & 63;
-    tok = i + lane < C ? tokens[i + lane] : -1;
-    zt = tok >= 0 && tok < V ? (float)x[tok] : -INFINITY;
+    return C ? (i + lane < C ? tokens[min(i + lane, C - 1)] : -1) : -1;
 }
 
-__device__ __forceinline__ float read_lane(float v, int lane)
-{
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
+template <typename XT>
+__device__ __forceinline__ XT gather(const XT *x, int tok, int V) { return x[min(max(tok, 0), V - 1)]; }
+
+template <typename XT>
+__device__ __forceinline__ float token_score(XT x, int tok, int V) { return tok >= 0 && tok < V ? (float)x : -INFINITY; }
+
+// What a loop over rows knows of the rows ahead: whether they hold data.
+struct RowAhead {
+    int32_t t, length;
+    __device__ __forceinline__ RowAhead(const RowSet &s, int64_t r, int64_t rows) : t(0), length(0)
+    {
+        if (r >= rows) return;
+        length = 1;
+        if (!s.lengths) return;
+        const int64_t b = r / s.T;
+        t = (int32_t)(r - b * s.T);
+        length = s.lengths[b];
+    }
+    __device__ __forceinline__ bool holds() const { return t < length; }
+};
 
 // A row a wavefront, four to a workgroup, no barriers.
 template <typename XT, int NV>
@@ -422,16 +528,34 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_short(TokenCall c, int3
     const int lane = threadIdx.x & 63, slot = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     TokenShared<1> &sh = shared[slot];
     u64 *list = lists + (size_t)slot * room;
-    for (int64_t r = (int64_t)blockIdx.x * kTokenWaves + slot; r < c.rows; r += (int64_t)gridDim.x * kTokenWaves) {
-        if (!row_active(c.set, r)) continue;
+    typedef TokenRun<XT, 1, NV> Run;
+    const int64_t step = (int64_t)gridDim.x * kTokenWaves;
+    int64_t r = (int64_t)blockIdx.x * kTokenWaves + slot;
+    // the next row's labels and tokens are under way while a row is worked on
+    typename Run::Packs packs;
+    int tok_next = -1;
+    const auto ahead = [&](int64_t row) {
+        Run::fetch((const XT *)c.x + row * c.x_stride, c.V, 0, lane, packs);
+        tok_next = load_tokens(c.tokens + row * c.C, 0, c.C);
+    };
+    RowAhead now(c.set, r, c.rows), next(c.set, r + step, c.rows);
+    if (now.holds()) ahead(r);
+    for (; r < c.rows; r += step) {
+        const RowAhead after(c.set, r + 2 * step, c.rows);
+        const bool here = now.holds(), more = next.holds();
+        now = next;
+        next = after;
+        if (!here) {
+            if (more) ahead(r + step);
+            continue;
+        }
         const XT *x = (const XT *)c.x + r * c.x_stride;
         const int32_t *tokens = c.tokens + r * c.C;
+        Run run(packs, c.V, 0, lane);
+        int tok = tok_next;
+        XT raw = c.C ? gather(x, tok, c.V) : (XT)0.0f;
+        if (more) ahead(r + step);
         const Heat heat = row_heat(c, r);
-        TokenRun<XT, 1, NV> run;
-        run.load(x, c.V, 0, lane);
-        int tok;
-        float zt;
-        load_tokens<XT>(x, tokens, c.V, 0, c.C, tok, zt);
         TokenStat s;
         s.m = wave_max_f(run.mine);
         run.sums(heat, s.m, s);
@@ -439,13 +563,12 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_short(TokenCall c, int3
         const TokenRow row = row_result(s, heat);
         if (lane == 0 && c.entropies) c.entropies[r] = row.entropy;
         for (int i = 0; i < c.C; i += kWaveSize) {
-            if (i) load_tokens<XT>(x, tokens, c.V, i, c.C, tok, zt);
-            int before = 0;
-            const int m = min(c.C - i, kWaveSize);
-            for (int k = 0; k < m; ++k) {
-                const int got = run.before(x, read_lane(zt, k), __builtin_amdgcn_readlane(tok, k), true);
-                before = k == lane ? got : before;
+            if (i) {
+                tok = load_tokens(tokens, i, c.C);
+                raw = gather(x, tok, c.V);
             }
+            const float zt = token_score(raw, tok, c.V);
+            const int m = min(c.C - i, kWaveSize), before = run.ranks(x, zt, tok, m, true);
             if (lane < m) write_token(c, row, r * c.C + i + lane, tok >= 0 && tok < c.V, zt, before);
         }
         if (c.top_n) {
@@ -475,16 +598,37 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
     const int64_t items = CUT ? c.rows * plan.pieces : c.rows;
     const TokenWork work = CUT ? token_work(c.workspace, items, n) : TokenWork{};
 
-    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+    typename Run::Packs packs;
+    int tok_next = -1;
+    const int64_t step = gridDim.x;
+    const auto ahead = [&](int64_t row) {               // (as above)
+        Run::fetch((const XT *)c.x + row * c.x_stride, c.V, 0, tid, packs);
+        tok_next = load_tokens(c.tokens + row * C, 0, C);
+    };
+    RowAhead now(c.set, blockIdx.x, CUT ? 0 : items), next(c.set, blockIdx.x + step, CUT ? 0 : items);
+    if (!CUT && now.holds()) ahead(blockIdx.x);
+    for (int64_t w = blockIdx.x; w < items; w += step) {
         const int64_t r = CUT ? w / plan.pieces : w;
         const int begin = CUT ? (int)(w - r * plan.pieces) * plan.subs * kLen : 0;
-        if (!row_active(c.set, r)) continue;
+        bool following = false;
+        if (CUT) {
+            if (!row_active(c.set, r)) continue;
+        } else {
+            const RowAhead after(c.set, w + 2 * step, items);
+            const bool here = now.holds();
+            following = next.holds();
+            now = next;
+            next = after;
+            if (!here) {
+                if (following) ahead(w + step);
+                continue;
+            }
+        }
         const XT *x = (const XT *)c.x + r * c.x_stride;
         const int32_t *tokens = c.tokens + r * C;
+        int tok = CUT ? load_tokens(tokens, 0, C) : tok_next;
+        XT raw = (XT)0.0f;
         const Heat heat = row_heat(c, r);
-        int tok;
-        float zt;
-        load_tokens<XT>(x, tokens, c.V, 0, C, tok, zt);
 
         TokenStat all = {-INFINITY, 0.0f, 0.0f, 0.0f};
         int kept = 0;                                   // keys at the head of the list, sorted
@@ -492,8 +636,10 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
             const int first = begin + sub * kLen;
             if (CUT && first >= c.V) break;
             const bool more = CUT && sub + 1 < plan.subs && first + kLen < c.V;
-            Run run;
-            run.load(x, c.V, first, tid);
+            if (CUT) Run::fetch(x, c.V, first, tid, packs);
+            if (sub == 0 && C) raw = gather(x, tok, c.V);
+            Run run(packs, c.V, first, tid);
+            if (following) ahead(w + step);
             TokenStat s;
             const float wave_max = wave_max_f(run.mine);
             s.m = wave_max;
@@ -512,13 +658,12 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
                 sh.red[3 * WAVES + wave] = s.ones;
             }
             for (int i = 0; i < C; i += kWaveSize) {
-                if (C > kWaveSize && (i || sub)) load_tokens<XT>(x, tokens, c.V, i, C, tok, zt);
-                int before = 0;
-                const int m = min(C - i, kWaveSize);
-                for (int k = 0; k < m; ++k) {
-                    const int got = run.before(x, read_lane(zt, k), __builtin_amdgcn_readlane(tok, k), wave == 0);
-                    before = k == lane ? got : before;
+                if (C > kWaveSize && (i || sub)) {
+                    tok = load_tokens(tokens, i, C);
+                    raw = gather(x, tok, c.V);
                 }
+                const int m = min(C - i, kWaveSize);
+                const int before = run.ranks(x, token_score(raw, tok, c.V), tok, m, wave == 0);
                 if (lane < m) atomicAdd(&sh.ranks[i + lane], before);
             }
             if (n) run.candidates(sh, list, n, kept);
@@ -558,9 +703,13 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
             if (tid == 0 && c.entropies) c.entropies[r] = row.entropy;
             if (wave == WAVES - 1)                      // (the list's first keys lie with the first)
                 for (int i = 0; i < C; i += kWaveSize) {
-                    if (C > kWaveSize) load_tokens<XT>(x, tokens, c.V, i, C, tok, zt);
+                    if (C > kWaveSize) {
+                        tok = load_tokens(tokens, i, C);
+                        raw = gather(x, tok, c.V);
+                    }
                     if (i + lane < C)
-                        write_token(c, row, r * C + i + lane, tok >= 0 && tok < c.V, zt, sh.ranks[i + lane]);
+                        write_token(c, row, r * C + i + lane, tok >= 0 && tok < c.V, token_score(raw, tok, c.V),
+                                    sh.ranks[i + lane]);
                 }
         }
         __syncthreads();
@@ -568,11 +717,12 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
 }
 
 // Joins a row's pieces: one workgroup a row.
-constexpr int kJoinList = kMaxTop * ((kMaxPieces * kMaxTop + kTokenThreads - 1) / kTokenThreads);
+constexpr int kJoinList = bound_cap(kMaxTop) * ((kMaxTop + kTokenThreads / kMaxPieces - 1) / (kTokenThreads / kMaxPieces));
 
 __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32_t P, int32_t xcode)
 {
-    __shared__ u64 top[kTokenThreads], list[kJoinList];
+    __shared__ u64 top[kTokenThreads];
+    __shared__ __align__(16) u64 list[kJoinList + 8];
     __shared__ int32_t listed;
     const int tid = threadIdx.x, lane = tid & 63, n = c.top_n, C = c.C;
     const TokenWork work = token_work(c.workspace, c.rows * P, n);
@@ -604,8 +754,11 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32
         }
         if (!n) continue;
         const u64 *keys = work.keys + r * P * n;
+        // a piece's keys over `share` threads in turn, so that the best of all lie far apart
+        const int share = kTokenThreads / P, piece = tid / share;
+        const int i0 = piece < P ? piece * n + tid % share : 0, end = piece < P ? piece * n + n : 0;
         u64 mine = 0;
-        for (int i = tid; i < P * n; i += kTokenThreads) mine = max(mine, keys[i]);
+        for (int i = i0; i < end; i += share) mine = max(mine, keys[i]);
         top[tid] = mine;
         if (tid == 0) listed = 0;
         __syncthreads();
@@ -613,8 +766,13 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32
 #pragma unroll
         for (int q = 0; q < kTokenWaves; ++q) u[q] = top[q * kWaveSize + lane];
         int reach;
-        const u64 bound = max(nth_key<u64, kTokenWaves>(u, n, reach), (u64)1);
-        for (int i = tid; i < P * n; i += kTokenThreads) {
+        const u64 bound = max(nth_key<u64>(n, kTokenThreads, reach, [&](u64 t) {
+            int g = 0;
+#pragma unroll
+            for (int q = 0; q < kTokenWaves; ++q) g += count(u[q] >= t);
+            return g;
+        }), (u64)1);
+        for (int i = i0; i < end; i += share) {
             const u64 k = keys[i];
             if (k >= bound) list[atomicAdd(&listed, 1)] = k;
         }
@@ -641,10 +799,11 @@ TokenShape token_shape(int64_t rows, int32_t V, int32_t x_dtype)
     return {kTokenWaves, nv, up(V, (int64_t)len * subs), subs};
 }
 
-// u64 of a row's list in LDS: the labels of n threads, and twice the n best so far.
+// u64 of a row's list in LDS: the labels that may reach the bound, 8 zeros, and twice
+// the n best so far.
 int token_list(const TokenCall &c, int nv, int vec, bool cut)
 {
-    return c.top_n ? std::min(c.top_n * nv * vec, c.V) + (cut ? 2 * c.top_n : 0) : 0;
+    return c.top_n ? (std::min(bound_cap(c.top_n) * nv * vec, c.V) + 8 + (cut ? 2 * c.top_n : 0) + 1) / 2 * 2 : 0;
 }
 
 template <typename XT, int NV>
