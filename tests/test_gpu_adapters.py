@@ -298,6 +298,21 @@ def test_captured_replays_read_the_slots_anew():
             assert torch.equal(a[act], b[act])
 
 
+@pytest.mark.parametrize("N", [300, 24600, 17000])
+def test_rows_do_not_depend_on_the_rows_beside_them(N):
+    """Within a path of the layer (here: up to 16 rows, or more than 16 of a large layer)."""
+    K = 300
+    layer, _ = _layer(31, K, N)
+    ad = wb.Adapters(layer, 9, 70, dtype="bf16")
+    _fill(ad, layer, 9, [70, 16, 33, 1, 0, 48, 17, 64, 5], "bf16")
+    M = 16 if N != 17000 else 80
+    h = torch.randn(M, K, device="cuda")
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) * 5 % 10 - 1
+    y = layer.logits(h, adapters=ad, ids=ids)
+    for lo, hi in ((0, 1), (3, 4), (5, 11)) if M == 16 else ((0, 20), (33, 80)):
+        assert torch.equal(layer.logits(h[lo:hi], adapters=ad, ids=ids[lo:hi]), y[lo:hi])
+
+
 def test_streams_at_once():
     K, N, R = 300, 17000, 70
     layer, _ = _layer(24, K, N)
@@ -325,7 +340,7 @@ def test_hidden_states_to_scores_and_words():
     layer, arrays = _layer(25, K, g.vocab, 32)
     ad = wb.Adapters(layer, 3, 8, dtype="f32")
     held = _fill(ad, layer, 7, [8, 4, 0], "f32")
-    h = torch.randn(B, T, K, device="cuda")
+    h = torch.randn(B, T, K, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
     L = np.array([30, 17, 0, 9], np.int32)
     ids = [1, 0, 0, -1]
     lp = layer.log_probs(h, adapters=ad, ids=ids)
@@ -340,16 +355,22 @@ def test_hidden_states_to_scores_and_words():
     r = dec.decode_hidden(layer, h, L, adapters=ad, ids=ids)
     w = dec.decode(lp, L)
     assert all(np.array_equal(a, b) for a, b in zip(r.arcs, w.arcs)) and np.array_equal(r.scores, w.scores)
-    ch = dec.create_streams(2)
+    # streams, whose search does not know its last frames, against streams of the same rows' log-posteriors
+    ch, other = dec.create_streams(2), dec.create_streams(2)
     for t0 in range(0, 30, 7):
         n = np.clip(L[:2] - t0, 0, 7).astype(np.int32)
         part = torch.zeros(2, 7, K, device="cuda")
         k = min(7, T - t0)
         part[:, :k] = h[:2, t0:t0 + k]
         dec.advance_hidden(ch, layer, part, n, adapters=ad, ids=ids[:2])
-    for c, lane in zip(ch, (0, 1)):
-        assert np.array_equal(dec.finalize_stream(c).arcs[0], r.arcs[lane])
-        dec.release_stream(c)
+        rows = torch.zeros(2, 7, g.vocab, device="cuda")
+        rows[:, :k] = lp[:2, t0:t0 + k]
+        dec.advance_chunk(other, rows, n)
+    for a, b in zip(ch, other):
+        ra, rb = dec.finalize_stream(a), dec.finalize_stream(b)
+        assert np.array_equal(ra.arcs[0], rb.arcs[0]) and ra.scores[0] == rb.scores[0]
+        dec.release_stream(a)
+        dec.release_stream(b)
     tok = lp.argmax(-1).int()
     Lg = torch.from_numpy(L).cuda()
     s = layer.token_scores(h, tok, top_n=3, lengths=Lg, adapters=ad, ids=ids)

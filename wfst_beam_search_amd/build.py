@@ -11,11 +11,10 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwfst_mi355x.so")
-SOURCES = [os.path.join(HERE, "csrc", "wfst_kernels.hip"), os.path.join(HERE, "csrc", "wfst_noalloc.hip"),
-           os.path.join(HERE, "csrc", "wfst_api.cpp"), os.path.join(HERE, "csrc", "wfst_layer.hip"),
-           os.path.join(HERE, "csrc", "wfst_norm.hip"), os.path.join(HERE, "csrc", "wfst_sample.hip"),
-           os.path.join(HERE, "csrc", "wfst_adapters.hip"), os.path.join(HERE, "csrc", "wfst_tokens.hip"),
-           os.path.join(HERE, "csrc", "wfst_score_api.cpp")]
+SOURCES = [os.path.join(HERE, "csrc", name) for name in (
+    "wfst_layer_f32.hip", "wfst_layer_bf16.hip", "wfst_layer_f16.hip", "wfst_kernels.hip", "wfst_tokens.hip",
+    "wfst_sample.hip", "wfst_noalloc.hip", "wfst_api.cpp", "wfst_layer.hip", "wfst_adapters.hip", "wfst_norm.hip",
+    "wfst_score_api.cpp")]          # (the longest to compile first)
 
 FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",

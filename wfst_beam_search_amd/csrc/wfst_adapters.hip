@@ -1,6 +1,5 @@
-// gfx950 (CDNA4) kernels of the low-rank adapters beside the output layer: a slot laid out for the
-// kernels, and the product of hidden states with the adapters' down matrices. What the up
-// matrices give is added by the layer's kernels before they round (wfst_layer.hip).
+// gfx950 (CDNA4) kernels that lay a low-rank adapter out in its slot. The products run beside the
+// output layer's (wfst_adapters_device.h, wfst_layer.hip).
 #include "wfst_score_device.h"
 
 namespace wfst {
@@ -39,47 +38,6 @@ __global__ void k_adapters_clear(Adapters a)
     }
 }
 
-// One wavefront for each row and rank.
-template <typename XT, typename AT>
-__global__ __launch_bounds__(256) void k_adapt_shrink(LayerCall c, int32_t K)
-{
-    const AdaptCall &ad = c.ad;
-    const int lane = threadIdx.x & 63, R = ad.a.rb * 16;
-    const int64_t n = (int64_t)c.M * R, step = (int64_t)gridDim.x * 4;
-    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += step) {
-        const int64_t m = i / R;
-        const int j = (int)(i - m * R);
-        if (!row_active(c.rows, m)) continue;
-        const int slot = row_adapter(ad, m);
-        if (slot < 0) continue;
-        float sum = 0.0f;
-        if (j < ad.a.ranks[slot]) {
-            const AT *w = (const AT *)ad.a.down + ((size_t)slot * R + j) * ad.a.kp;
-            const XT *x = (const XT *)c.x + m * c.x_stride;
-            for (int k = lane * 8; k < K; k += kWaveSize * 8) {
-                float v[8];
-                load_x<XT>(x, true, k, K, v);
-                const Pack<AT, 8> p = *(const Pack<AT, 8> *)(w + k);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(v[e], (float)p.v[e], sum);
-            }
-            sum = wave_sum_f(sum) * ad.a.scales[slot];
-        }
-        if (lane == 0) ad.h[i] = sum;
-    }
-}
-
-template <typename XT>
-hipError_t shrink(const LayerCall &c, int32_t K, hipStream_t s)
-{
-    const int64_t n = ((int64_t)c.M * c.ad.a.rb * 16 + 3) / 4;
-    const dim3 g((unsigned)std::min<int64_t>(n, kMaxRowGrid)), b(256);
-    if (c.ad.a.dtype == kF32) hipLaunchKernelGGL((k_adapt_shrink<XT, float>), g, b, 0, s, c, K);
-    else if (c.ad.a.dtype == kF16) hipLaunchKernelGGL((k_adapt_shrink<XT, _Float16>), g, b, 0, s, c, K);
-    else hipLaunchKernelGGL((k_adapt_shrink<XT, __bf16>), g, b, 0, s, c, K);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_adapters_clear(const Adapters &a, hipStream_t s)
@@ -96,13 +54,6 @@ hipError_t launch_adapter_load(const Adapters &a, int32_t slot, const AdapterSou
     else if (a.dtype == kF16) hipLaunchKernelGGL(k_adapter_load<_Float16>, g, b, 0, s, a, slot, src);
     else hipLaunchKernelGGL(k_adapter_load<__bf16>, g, b, 0, s, a, slot, src);
     return hipGetLastError();
-}
-
-hipError_t launch_adapt_shrink(const LayerCall &c, int32_t K, hipStream_t s)
-{
-    if (c.x_dtype == kF32) return shrink<float>(c, K, s);
-    if (c.x_dtype == kF16) return shrink<_Float16>(c, K, s);
-    return shrink<__bf16>(c, K, s);
 }
 
 }  // namespace wfst

@@ -83,7 +83,8 @@ struct AdaptCall {
     Adapters a;
     const int32_t *ids;         // null: no adapters
     int32_t per_id;
-    float *h;                   // [rows up to a multiple of 16][rb * 16], in the workspace
+    int32_t *info;              // [rows]: slot and blocks of ranks, -1: none; in the workspace
+    char *h;                    // blocks of 16 rows and 16 ranks, [rows / 16][rb], in the workspace
 };
 
 hipError_t launch_adapters_clear(const Adapters &a, hipStream_t s);
@@ -100,13 +101,14 @@ struct LayerCall {
     AdaptCall ad;
 };
 
-// h[r, j] = scale * sum_k down[j, k] x[r, k] of each row's adapter.
-hipError_t launch_adapt_shrink(const LayerCall &c, int32_t K, hipStream_t s);
-
+size_t adapters_h_bytes(const Adapters &a, int32_t rows);
 size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype);
 hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, void *scales, uint8_t *zeros,
                              float *bias, hipStream_t s);
 hipError_t launch_layer(const Layer &l, const LayerCall &c, hipStream_t s);
+hipError_t launch_layer_f32(const Layer &l, const LayerCall &c, hipStream_t s);    // (by the type of x)
+hipError_t launch_layer_f16(const Layer &l, const LayerCall &c, hipStream_t s);
+hipError_t launch_layer_bf16(const Layer &l, const LayerCall &c, hipStream_t s);
 
 // ---- log-softmax
 

@@ -266,7 +266,7 @@ size_t adapt_offset(const Layer &l, int32_t rows, int32_t x_dtype)
 
 size_t adapt_workspace(const Layer &l, const Adapters &a, int32_t rows, int32_t x_dtype)
 {
-    return adapt_offset(l, rows, x_dtype) + ((size_t)rows + 15) / 16 * 16 * a.rb * 16 * sizeof(float);
+    return adapt_offset(l, rows, x_dtype) + adapters_h_bytes(a, rows) + (size_t)rows * sizeof(int32_t);
 }
 
 int check_same_layer(const Layer &l, int device, wfst_adapters_t ad)
@@ -315,7 +315,8 @@ int layer_logits(wfst_layer_t layer, wfst_adapters_t ad, const int32_t *ids, int
         TRY(api_check_buffer(ids, (size_t)ib, layer->device, "ids"));
         if (ranges_meet(ids, ib, out, ob) || ranges_meet(ids, ib, workspace, (int64_t)need))
             return api_fail(WFST_EINVAL, "out and workspace must not overlap ids");
-        c.ad = {ad->a, ids, rows_per_id, (float *)((char *)workspace + adapt_offset(l, rows, x_dtype))};
+        char *h = (char *)workspace + adapt_offset(l, rows, x_dtype);
+        c.ad = {ad->a, ids, rows_per_id, (int32_t *)(h + adapters_h_bytes(ad->a, rows)), h};
     }
     HIP_TRY(launch_layer(l, c, (hipStream_t)stream));
     return WFST_OK;

@@ -21,7 +21,7 @@ typedef float float4_t __attribute__((ext_vector_type(4)));
 // The adapter slot of row r of a call, -1: none.
 __device__ __forceinline__ int row_adapter(const AdaptCall &ad, int64_t r)
 {
-    const int s = ad.ids[r / ad.per_id];
+    const int s = ad.ids[(uint32_t)r / (uint32_t)ad.per_id];
     return s >= 0 && s < ad.a.slots && ad.a.ranks[s] > 0 ? s : -1;
 }
 
