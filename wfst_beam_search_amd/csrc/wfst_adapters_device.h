@@ -71,10 +71,6 @@ __device__ __forceinline__ float finite_abs(float v)
     return a < INFINITY ? a : 0.0f;
 }
 
-// What the product needs to know of a row: its slot and how many blocks of 16 ranks
-// that has; -1: nothing to add.
-__device__ __forceinline__ int row_info(const AdaptCall &ad, int id) { return id < 0 ? -1 : id | (ad.a.ranks[id] + 15) / 16 << 20; }
-
 constexpr int kRowWaves = 16;
 
 // Row by row: a workgroup of 16 wavefronts for each row and 16 ranks, a wavefront for
@@ -89,7 +85,6 @@ __device__ __forceinline__ void shrink_row(const LayerCall &c, int32_t K, int64_
     int slot = row_active(c.rows, m) ? ad.ids[(uint32_t)m / (uint32_t)ad.per_id] : -1;
     if (slot >= ad.a.slots) slot = -1;
     const int rank = slot >= 0 ? ad.a.ranks[slot] : 0, j = jb * 16 + wave;
-    if (jb == 0 && threadIdx.x == 0) ad.info[m] = rank > 0 ? slot | (rank + 15) / 16 << 20 : -1;
     if (jb * 16 >= rank) return;
     float sum = 0.0f;
     if (j < rank) {
@@ -187,7 +182,6 @@ __device__ __forceinline__ void shrink_tile(const LayerCall &c, int32_t K, int64
     const int id = m < c.M && row_active(c.rows, m) ? row_adapter(ad, m) : -1;
     const XT *x = (const XT *)c.x + (id >= 0 ? m : 0) * c.x_stride;
     const int kb = ad.a.kp / 32, b0 = kb * wave / 4, b1 = kb * (wave + 1) / 4;
-    if (wave == 0 && lane < kRowsTile && m < c.M) ad.info[m] = row_info(ad, id);
     uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
     while (todo) {
         const int slot = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
@@ -234,94 +228,94 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w, uint32_t exponent, u
     return w & ~((bad >> 15) * 0xFFFFu);
 }
 
-// The blocks (slot, 16 ranks) of the slots among up to 64 rows, a row's id in each
-// lane (-1: none): for the lane whose row it is, each slot once.
-struct AdapterCursor {
-    uint64_t todo, mine;        // rows of slots to come; rows of this one
-    int slot, jb, nb;           // nb = 0: no more
-
-    __device__ __forceinline__ void pick(int id, int blocks)
-    {
-        nb = 0;
-        if (!todo) return;
-        const int l = __builtin_ctzll(todo);
-        slot = __builtin_amdgcn_readlane(id, l);
-        nb = __builtin_amdgcn_readlane(blocks, l);
-        mine = __ballot(id == slot);
-        todo &= ~mine;
-        jb = 0;
-    }
-    // On to the next block that is wavefront `part` of `parts`' own, from this one on (skip: behind it).
-    __device__ __forceinline__ void next(int id, int blocks, int part, int parts, bool skip)
-    {
-        while (nb && (skip || ((slot + jb) & (parts - 1)) != part)) {
-            skip = false;
-            if (++jb == nb) pick(id, blocks);
+// The blocks (slot, 16 ranks) that a group of 16, 32 or 64 rows takes, each once, in one
+// list for each of the wavefronts that share the group's sums: by the slot's number and
+// the block's, so that a row's sum does not depend on the rows beside it. An entry:
+// slot | block << 16, the rows it is for (64 bits), 0. One wavefront makes the lists of
+// a group, a lane for each row.
+__device__ __forceinline__ void make_lists(const LayerCall &c, int64_t group)
+{
+    const AdaptCall &ad = c.ad;
+    const int lane = threadIdx.x & 63, G = ad.group, cap = G * ad.a.rb;
+    const int64_t m = group * G + lane;
+    const int id = lane < G && m < c.M && row_active(c.rows, m) ? row_adapter(ad, m) : -1;
+    const int blocks = id >= 0 ? (ad.a.ranks[id] + 15) / 16 : 0;
+    uint64_t mine = 0;
+    for (int q = 0; q < G; ++q) mine |= (uint64_t)(id == __builtin_amdgcn_readlane(id, q)) << q;
+    const bool first = id >= 0 && __builtin_ctzll(mine) == lane;
+    uint4 *list = ad.lists + group * ad.parts * cap;
+    for (int p = 0; p < ad.parts; ++p, list += cap) {
+        const int j0 = (p - id) & (ad.parts - 1);       // the slot's first block of this part, then every parts-th
+        const int n = first && blocks > j0 ? (blocks - j0 + ad.parts - 1) / ad.parts : 0;
+        int end = n;
+#pragma unroll
+        for (int d = 1; d < kWaveSize; d <<= 1) {
+            const int o = __shfl_up(end, d, kWaveSize);
+            end += lane >= d ? o : 0;
         }
+        for (int i = 0; i < n; ++i)
+            list[end - n + i] = make_uint4((uint32_t)(id | (j0 + i * ad.parts) << 16), (uint32_t)mine, (uint32_t)(mine >> 32), 0);
+        if (lane == kWaveSize - 1) ad.counts[group * ad.parts + p] = end;
     }
-};
+}
 
-// What the adapters of MT * 16 rows from m0 on give to NT feature tiles. `parts` (1, 2,
-// 4) wavefronts with the same sums share the blocks by the slot's number and the block's,
-// so that a row's sum does not depend on the rows beside it. Blocks of up are loaded
-// kAhead steps before they are used.
-template <int MT, int NT>
+// What the adapters of a group of MT * 16 rows give to NT feature tiles, by the list of
+// this wavefront, 64 entries at a time, a lane each. Blocks of up are loaded kAhead
+// entries before they are used.
+template <int MT, int NT, int kAhead>
 struct AdapterTiles {
-    static constexpr int kAhead = NT == 1 ? 2 : 4;
-    int id, blocks, part, parts;
-    AdapterCursor use, load;
+    const uint4 *list;
+    int n, cap;
+    uint4 entry;
     uint4 up[kAhead][NT];
 
-    __device__ __forceinline__ void fetch(const AdaptCall &ad, int nt0, uint4 (&u)[NT])
+    __device__ __forceinline__ void hold(int i)
     {
-        const int lane = threadIdx.x & 63;
-        if (!load.nb) return;
+        if (MT == 1) {
+            const uint2 e = *(const uint2 *)(list + i);
+            entry = make_uint4(e.x, e.y, 0, 0);
+        } else {
+            entry = list[i];
+        }
+    }
+
+    // The list's length and first entries (under way during the layer's product; what
+    // lies behind the last entry is not used).
+    __device__ __forceinline__ void begin(const AdaptCall &ad, int64_t group, int part)
+    {
+        cap = ad.group * ad.a.rb;
+        list = ad.lists + (group * ad.parts + part) * cap;
+        n = ad.counts[group * ad.parts + part];
+        hold(min((int)(threadIdx.x & 63), cap - 1));
+    }
+
+    // (No branch: the count of loads under way has to be known. 16-bit blocks have 8 bytes
+    // a lane, read twice.)
+    __device__ __forceinline__ void fetch(const AdaptCall &ad, int nt0, int i, uint4 (&u)[NT]) const
+    {
+        const uint32_t lane = threadIdx.x & 63, bytes = ad.a.dtype == kF32 ? 16 : 8;
+        const uint32_t e = (uint32_t)__builtin_amdgcn_readlane((int)entry.x, i);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const size_t t = (((size_t)load.slot * ad.a.nt + min(nt0 + n, ad.a.nt - 1)) * ad.a.rb + load.jb) * kWaveSize + lane;
-            if (ad.a.dtype == kF32) {
-                u[n] = ((const uint4 *)ad.a.up)[t];
-            } else {
-                const uint2 h = ((const uint2 *)ad.a.up)[t];
-                u[n].x = h.x;
-                u[n].y = h.y;
-            }
+            const size_t t = ((size_t)(e & 0xFFFFu) * ad.a.nt + min(nt0 + n, ad.a.nt - 1)) * ad.a.rb + (e >> 16);
+            const char *from = (const char *)ad.a.up + t * (kWaveSize * bytes) + lane * bytes;
+            const uint2 lo = *(const uint2 *)from, hi = *(const uint2 *)(from + bytes - 8);
+            u[n] = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
-        load.next(id, blocks, part, parts, true);
     }
 
-    // What is known of the rows from m0 on (under way during the layer's product).
-    static __device__ __forceinline__ int rows(const LayerCall &c, int64_t m0)
+    __device__ __forceinline__ void block(const AdaptCall &ad, const char *h, int i, const uint4 (&u)[NT], float4_t (&acc)[MT][NT]) const
     {
-        const int lane = threadIdx.x & 63;
-        return lane < MT * kRowsTile && m0 + lane < c.M ? c.ad.info[m0 + lane] : -1;
-    }
-
-    __device__ __forceinline__ void start(const AdaptCall &ad, int info, int nt0, int mine, int of)
-    {
-        id = info < 0 ? -1 : info & 0xFFFFF;
-        blocks = info < 0 ? 0 : info >> 20;
-        part = mine;
-        parts = of;
-        use.todo = __ballot(id >= 0);
-        use.mine = 0;
-        use.slot = use.jb = 0;
-        use.pick(id, blocks);
-        use.next(id, blocks, part, parts, false);
-        load = use;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(ad, nt0, up[i]);
-    }
-
-    __device__ __forceinline__ void block(const AdaptCall &ad, const char *h, const uint4 (&u)[NT], float4_t (&acc)[MT][NT]) const
-    {
+        const int jb = __builtin_amdgcn_readlane((int)entry.x, i) >> 16;
+        const uint32_t rows[2] = {(uint32_t)__builtin_amdgcn_readlane((int)entry.y, i),
+                                  MT > 2 ? (uint32_t)__builtin_amdgcn_readlane((int)entry.z, i) : 0u};
         const int lane = threadIdx.x & 63, quad = lane >> 4;
         const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const uint32_t mine = (uint32_t)(use.mine >> (m * 16)) & 0xFFFFu;
+            const uint32_t mine = rows[m / 2] >> (m % 2 * 16) & 0xFFFFu;
             if (!mine) continue;
-            const char *b = h + (m * ad.a.rb + use.jb) * h_block_bytes(ad.a.dtype);
+            const char *b = h + (m * ad.a.rb + jb) * h_block_bytes(ad.a.dtype);
             float4_t d[NT];
             if (ad.a.dtype == kF32) {
                 const float4_t a = ((const float4_t *)b)[lane];
@@ -371,29 +365,38 @@ struct AdapterTiles {
         }
     }
 
-    // h: the rows' blocks [MT][rb], in LDS.
-    __device__ __forceinline__ void add(const AdaptCall &ad, const char *h, int nt0, float4_t (&acc)[MT][NT])
-    {
-        while (use.nb) {
-            step<0>(ad, h, nt0, acc);
-            step<1>(ad, h, nt0, acc);
-            if constexpr (kAhead > 2) {
-                step<2>(ad, h, nt0, acc);
-                step<3>(ad, h, nt0, acc);
-            }
-        }
-    }
-
     template <int I>
-    __device__ __forceinline__ void step(const AdaptCall &ad, const char *h, int nt0, float4_t (&acc)[MT][NT])
+    __device__ __forceinline__ void step(const AdaptCall &ad, const char *h, int nt0, int i, int end, float4_t (&acc)[MT][NT])
     {
-        if (!use.nb) return;
         uint4 u[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) u[n] = up[I][n];
-        fetch(ad, nt0, up[I]);
-        block(ad, h, u, acc);
-        use.next(id, blocks, part, parts, true);
+        fetch(ad, nt0, min(i + I + kAhead, end - 1), up[I]);
+        if (i + I < end) block(ad, h, i + I, u, acc);
+        if constexpr (I + 1 < kAhead) step<I + 1>(ad, h, nt0, i, end, acc);
+    }
+
+    // h: the rows' blocks [MT][rb], in LDS.
+    __device__ __forceinline__ void add(const AdaptCall &ad, const char *h, int nt0, float4_t (&acc)[MT][NT])
+    {
+        const int all = __builtin_amdgcn_readfirstlane(n);
+        for (int base = 0; base < all; base += kWaveSize) {
+            const int end = min(all - base, kWaveSize);
+            if (base) hold(min(base + (int)(threadIdx.x & 63), all - 1));
+            if (end <= 4) {                             // (filling the ring would cost more than it gains)
+                for (int i = 0; i < end; i += 2) {
+                    uint4 u[2][NT];
+                    fetch(ad, nt0, i, u[0]);
+                    fetch(ad, nt0, min(i + 1, end - 1), u[1]);
+                    block(ad, h, i, u[0], acc);
+                    if (i + 1 < end) block(ad, h, i + 1, u[1], acc);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) fetch(ad, nt0, min(i, end - 1), up[i]);
+            for (int i = 0; i < end; i += kAhead) step<0>(ad, h, nt0, i, end, acc);
+        }
     }
 };
 

@@ -63,7 +63,9 @@ int dalloc(T **p, size_t count, std::vector<void *> *owned, size_t *bytes)
 // A caller's buffer of `bytes` bytes at p that the kernels will read or write
 // (page section 4: a bad tensor fails with an error, never an out-of-bounds
 // access): device (or managed) memory of `device`, inside one allocation.
-int check_device_buffer(const void *p, size_t bytes, int device, const char *what)
+// lo, hi (or null): the allocation's bounds where they are known.
+int check_device_buffer(const void *p, size_t bytes, int device, const char *what, const char **lo = nullptr,
+                        const char **hi = nullptr)
 {
     if (bytes == 0) return WFST_OK;
     hipPointerAttribute_t a{};
@@ -78,6 +80,10 @@ int check_device_buffer(const void *p, size_t bytes, int device, const char *wha
     if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)p) == hipSuccess && base) {
         if ((const char *)p + bytes > (const char *)base + size)
             return fail(WFST_EINVAL, std::string(what) + " ends past its allocation");
+        if (lo) {
+            *lo = (const char *)base;
+            *hi = (const char *)base + size;
+        }
     } else {
         (void)hipGetLastError();
     }
@@ -1754,9 +1760,9 @@ namespace wfst {
 
 int api_fail(int code, const std::string &msg) { return fail(code, msg); }
 
-int api_check_buffer(const void *p, size_t bytes, int device, const char *what)
+int api_check_buffer(const void *p, size_t bytes, int device, const char *what, const char **lo, const char **hi)
 {
-    return check_device_buffer(p, bytes, device, what);
+    return check_device_buffer(p, bytes, device, what, lo, hi);
 }
 
 }  // namespace wfst

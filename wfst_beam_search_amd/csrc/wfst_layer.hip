@@ -78,9 +78,11 @@ hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, v
     return hipGetLastError();
 }
 
-size_t adapters_h_bytes(const Adapters &a, int32_t rows)
+AdaptBytes adapt_bytes(const Adapters &a, int32_t rows)
 {
-    return ((size_t)rows + kRowsM - 1) / kRowsM * a.rb * h_block_bytes(a.dtype);
+    // (groups of 16 to 64 rows, up to 4 lists each)
+    const size_t r64 = ((size_t)rows + 63) / 64 * 64, r16 = ((size_t)rows + 15) / 16;
+    return {r16 * a.rb * h_block_bytes(a.dtype), 4 * r64 * a.rb * sizeof(uint4), 4 * r16 * sizeof(int32_t)};
 }
 
 size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype)

@@ -159,7 +159,7 @@ __device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, fl
 template <int KS, int SPL> constexpr int kTilesAhead = KS == 1 ? (SPL == 1 ? 3 : 4) : 2;
 
 template <typename XT, int WS, int GPT, int KS, int SPL, bool AD>
-__global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall c, int RP, int kc)
+__global__ __launch_bounds__(kLayerThreads, AD && SPL == 1 ? 4 : 1) void k_layer_few(Layer l, LayerCall c, int RP, int kc)
 {
     constexpr int P = kParts<XT>;
     constexpr int D = kTilesAhead<KS, SPL>;
@@ -191,8 +191,8 @@ __global__ __launch_bounds__(kLayerThreads) void k_layer_few(Layer l, LayerCall 
         sq[i] = load_tile_scale<WS, GPT>(l, min(t, (size_t)l.nt * l.kb - 1) * kTileN + col);
     }
 
-    int info = -1;
-    if constexpr (AD) info = AdapterTiles<1, 1>::rows(c, m0);
+    AdapterTiles<1, 1, 2> tiles;
+    if constexpr (AD) tiles.begin(c.ad, blockIdx.y, slice);
 
     // staging: 16 * RP threads (at most 64) take a block of 128 features, each up to four runs of 8
     const int per = min(64, 16 * RP), bpw = 64 / per;
@@ -281,8 +281,6 @@ const int at = (u * 16 + j * 4 + quad) * RP + arow;
         }
     }
     if constexpr (AD) {
-        AdapterTiles<1, 1> tiles;
-        tiles.start(c.ad, info, nt, slice, KS);
         float4_t sums[1][1] = {{acc}};
         tiles.add(c.ad, hs, nt, sums);
         acc = sums[0][0];
@@ -352,15 +350,24 @@ __global__ __launch_bounds__(256) void k_layer_operands(Layer l, LayerCall c, ha
     make_operands<XT>(l, c, xa, xf);
 }
 
-// h of the adapters, by tiles of 16 rows or row by row; the workgroups before those make operands.
+// h of the adapters, by tiles of 16 rows or row by row; the workgroups before those
+// make operands, the ones behind them lists.
 template <typename XT, typename AT, bool TILES>
 __global__ __launch_bounds__(TILES ? 256 : kRowWaves * kWaveSize)
-void k_layer_shrink(Layer l, LayerCall c, half8_t *xa, float *xf, unsigned operands)
+void k_layer_shrink(Layer l, LayerCall c, half8_t *xa, float *xf, unsigned operands, unsigned items)
 {
     __shared__ __align__(16) char smem[TILES ? kShrinkBytes : 64];
-    if (blockIdx.x < operands) make_operands<XT>(l, c, xa, xf);
-    else if constexpr (TILES) shrink_tile<XT, AT>(c, l.K, blockIdx.x - operands, (float4_t *)smem);
-    else shrink_row<XT, AT>(c, l.K, blockIdx.x - operands, (float *)smem);
+    const unsigned b = blockIdx.x;
+    if (b < operands) {
+        make_operands<XT>(l, c, xa, xf);
+    } else if (b >= operands + items) {
+        const int64_t group = (int64_t)(b - operands - items) * (blockDim.x / kWaveSize) + threadIdx.x / kWaveSize;
+        if (group * c.ad.group < c.M) make_lists(c, group);
+    } else if constexpr (TILES) {
+        shrink_tile<XT, AT>(c, l.K, b - operands, (float4_t *)smem);
+    } else {
+        shrink_row<XT, AT>(c, l.K, b - operands, (float *)smem);
+    }
 }
 
 // The product for many rows: a workgroup of 8 wavefronts makes 16 MT rows by 128
@@ -375,7 +382,7 @@ void k_layer_shrink(Layer l, LayerCall c, half8_t *xa, float *xf, unsigned opera
 // the wait for the loads costs more (binary32 3 % of its 12.8 ms, groups of 32 3 %, 32
 // rows 7 %).
 template <typename XT, int WS, int GPT, int MT, bool AD>
-__global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf)
+__global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf)
 {
     constexpr int P = kParts<XT>;
     constexpr int NT = 2;
@@ -444,8 +451,10 @@ __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const 
         }
     };
 
-    int info = -1;
-    if constexpr (AD) info = AdapterTiles<MT, NT>::rows(c, (int64_t)mblk * MT * kRowsM);
+    // (one workgroup a CU where x has two parts; binary16 leaves registers for two with the shortest ring)
+    constexpr int kAhead = P == 2 ? 8 : kScaled<XT> || GPT > 1 ? 4 : 2;
+    AdapterTiles<MT, NT, kAhead> tiles;
+    if constexpr (AD) tiles.begin(c.ad, mblk, half);
     float4_t acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -525,12 +534,12 @@ __global__ __launch_bounds__(512) void k_layer_many(Layer l, LayerCall c, const 
         __syncthreads();
     }
     if constexpr (AD) {
-        AdapterTiles<MT, NT> tiles;
-        tiles.start(c.ad, info, nt0, half, 2);
-        char *hs = smem + 4 * MT * NT * kWaveSize * sizeof(float4_t);      // (behind joint)
-        stage_h(c, (int64_t)mblk * MT, MT, hs);
-        __syncthreads();
-        tiles.add(c.ad, hs, nt0, acc);
+        if (c.ad.counts[mblk * 2] | c.ad.counts[mblk * 2 + 1]) {        // (the same for the workgroup)
+            char *hs = smem + 4 * MT * NT * kWaveSize * sizeof(float4_t);      // (behind joint)
+            stage_h(c, (int64_t)mblk * MT, MT, hs);
+            __syncthreads();
+            tiles.add(c.ad, hs, nt0, acc);
+        }
     }
     if (half) {
 #pragma unroll
@@ -564,21 +573,22 @@ bool shrink_tiles(const LayerCall &c) { return c.M > 512; }
 template <typename XT, typename AT>
 void launch_shrink(const Layer &l, const LayerCall &c, half8_t *xa, float *xf, int64_t blocks, hipStream_t s)
 {
-    if (shrink_tiles(c)) {
-        const unsigned n = (unsigned)((c.M + kRowsM - 1) / kRowsM), operands = (unsigned)((blocks + 3) / 4);
-        hipLaunchKernelGGL((k_layer_shrink<XT, AT, true>), dim3(operands + n), dim3(256), 0, s, l, c, xa, xf, operands);
-    } else {
-        const unsigned n = (unsigned)c.M * (unsigned)c.ad.a.rb, operands = (unsigned)((blocks + kRowWaves - 1) / kRowWaves);
-        hipLaunchKernelGGL((k_layer_shrink<XT, AT, false>), dim3(operands + n), dim3(kRowWaves * kWaveSize), 0, s, l, c, xa,
-                           xf, operands);
-    }
+    const bool tiles = shrink_tiles(c);
+    const int waves = tiles ? 4 : kRowWaves;
+    const auto up = [](int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); };
+    const unsigned operands = up(blocks, waves), items = tiles ? up(c.M, kRowsM) : (unsigned)c.M * (unsigned)c.ad.a.rb;
+    const dim3 g(operands + items + up(up(c.M, c.ad.group), waves)), b(waves * kWaveSize);
+    if (tiles) hipLaunchKernelGGL((k_layer_shrink<XT, AT, true>), g, b, 0, s, l, c, xa, xf, operands, items);
+    else hipLaunchKernelGGL((k_layer_shrink<XT, AT, false>), g, b, 0, s, l, c, xa, xf, operands, items);
 }
 
 // What comes before the product: `blocks` of operands and, with adapters, their h.
 template <typename XT, bool AD>
-void launch_before(const Layer &l, const LayerCall &c, half8_t *xa, float *xf, int64_t blocks, hipStream_t s)
+void launch_before(const Layer &l, LayerCall &c, int group, int parts, half8_t *xa, float *xf, int64_t blocks, hipStream_t s)
 {
     if constexpr (AD) {
+        c.ad.group = group;
+        c.ad.parts = parts;
         if (c.ad.a.dtype == kF32) launch_shrink<XT, float>(l, c, xa, xf, blocks, s);
         else if (c.ad.a.dtype == kF16) launch_shrink<XT, _Float16>(l, c, xa, xf, blocks, s);
         else launch_shrink<XT, __bf16>(l, c, xa, xf, blocks, s);
@@ -588,8 +598,10 @@ void launch_before(const Layer &l, const LayerCall &c, half8_t *xa, float *xf, i
 }
 
 template <typename XT, int WS, int GPT, int KS, int SPL, bool AD>
-hipError_t few_launch(const Layer &l, const LayerCall &c, int RP, hipStream_t s)
+hipError_t few_launch(const Layer &l, const LayerCall &call, int RP, hipStream_t s)
 {
+    LayerCall c = call;
+    launch_before<XT, AD>(l, c, kRowsM, KS, nullptr, nullptr, 0, s);
     constexpr int D = kTilesAhead<KS, SPL>;
     // blocks of 128 features staged at a time: all, or what 40 KiB hold
     const int longest = (l.kb + KS - 1) / KS;
@@ -615,7 +627,6 @@ hipError_t layer_few(const Layer &l, const LayerCall &c, hipStream_t s)
 {
     int RP = 1;
     while (RP < std::min(c.M, kRowsM)) RP *= 2;
-    launch_before<XT, AD>(l, c, nullptr, nullptr, 0, s);
     if (l.nt < 1536)
         return RP <= 4 ? few_launch<XT, WS, GPT, 4, 1, AD>(l, c, RP, s) : few_launch<XT, WS, GPT, 4, 4, AD>(l, c, RP, s);
     return RP <= 4 ? few_launch<XT, WS, GPT, 1, 1, AD>(l, c, RP, s) : few_launch<XT, WS, GPT, 1, 4, AD>(l, c, RP, s);
@@ -648,12 +659,13 @@ size_t operand_bytes(const Layer &l, int32_t rows, int32_t x_dtype)
 }
 
 template <typename XT, int WS, int GPT, int MT, bool AD>
-hipError_t layer_many(const Layer &l, const LayerCall &c, hipStream_t s)
+hipError_t layer_many(const Layer &l, const LayerCall &call, hipStream_t s)
 {
+    LayerCall c = call;
     const int64_t blocks = (int64_t)((c.M + kRowsM - 1) / kRowsM) * l.kb;
     half8_t *xa = (half8_t *)c.workspace;
     float *xf = (float *)((char *)c.workspace + operand_bytes(l, c.M, c.x_dtype));
-    launch_before<XT, AD>(l, c, xa, xf, blocks, s);
+    launch_before<XT, AD>(l, c, MT * kRowsM, 2, xa, xf, blocks, s);
     size_t lds = 2 * 2 * MT * (kParts<XT> * kBlockHalves * 2 + 64);
     if (AD) lds = std::max(lds, 8 * MT * kWaveSize * sizeof(float4_t) + (size_t)MT * c.ad.a.rb * h_block_bytes(c.ad.a.dtype));
     const dim3 g((l.nt + 7) / 8, (c.M + MT * kRowsM - 1) / (MT * kRowsM));

@@ -15,7 +15,8 @@ namespace wfst {
 // Host helpers of wfst_api.cpp: record the calling thread's error message and
 // return `code`; check a caller's device buffer (see there).
 int api_fail(int code, const std::string &msg);
-int api_check_buffer(const void *p, size_t bytes, int device, const char *what);
+int api_check_buffer(const void *p, size_t bytes, int device, const char *what, const char **lo = nullptr,
+                     const char **hi = nullptr);
 
 // Element types (the public WFST_LP_* values).
 enum : int32_t { kF32 = 0, kF16 = 1, kBF16 = 2 };
@@ -83,8 +84,10 @@ struct AdaptCall {
     Adapters a;
     const int32_t *ids;         // null: no adapters
     int32_t per_id;
-    int32_t *info;              // [rows]: slot and blocks of ranks, -1: none; in the workspace
     char *h;                    // blocks of 16 rows and 16 ranks, [rows / 16][rb], in the workspace
+    uint4 *lists;               // [rows / group][parts][group * rb], there too
+    int32_t *counts;            // [rows / group][parts]
+    int32_t group, parts;       // rows whose blocks are listed together, and lists for them (set by the launch)
 };
 
 hipError_t launch_adapters_clear(const Adapters &a, hipStream_t s);
@@ -101,7 +104,9 @@ struct LayerCall {
     AdaptCall ad;
 };
 
-size_t adapters_h_bytes(const Adapters &a, int32_t rows);
+// Bytes of h, of the lists and of their lengths in a call's workspace.
+struct AdaptBytes { size_t h, lists, counts; };
+AdaptBytes adapt_bytes(const Adapters &a, int32_t rows);
 size_t layer_workspace(const Layer &l, int32_t rows, int32_t x_dtype);
 hipError_t launch_layer_pack(const Layer &l, const LayerSource &src, uint4 *w, void *scales, uint8_t *zeros,
                              float *bias, hipStream_t s);

@@ -106,6 +106,31 @@ int device_of(const void *p, const char *what)
     return a.device;
 }
 
+// Checks of one call's buffers: one that lies in an allocation already looked up in this
+// call needs no second look (a lookup costs about 1 us; a caching allocator puts most of
+// a call's small buffers into one block).
+class Buffers {
+public:
+    explicit Buffers(int device) : device_(device) {}
+    int check(const void *p, size_t bytes, const char *what)
+    {
+        const char *const at = (const char *)p;
+        for (int i = 0; i < n_; ++i)
+            if (p && at >= known_[i].lo && bytes <= (size_t)(known_[i].hi - known_[i].lo) && at <= known_[i].hi - bytes)
+                return WFST_OK;
+        Range r{nullptr, nullptr};
+        const int rc = api_check_buffer(p, bytes, device_, what, &r.lo, &r.hi);
+        if (rc == WFST_OK && r.lo && n_ < kMost) known_[n_++] = r;
+        return rc;
+    }
+
+private:
+    static constexpr int kMost = 8;
+    struct Range { const char *lo, *hi; };
+    int device_, n_ = 0;
+    Range known_[kMost];
+};
+
 int check_stream(void *stream, int device)
 {
     if (!stream) return WFST_OK;
@@ -127,12 +152,18 @@ int check_aligned(const void *p, size_t align, const char *what)
         if (_rc < 0) return _rc;           \
     } while (0)
 
-int check_lengths(const int32_t *lengths, int64_t rows, int32_t T, int device)
+int check_lengths(const int32_t *lengths, int64_t rows, int32_t T, Buffers &buffers)
 {
     if (!lengths) return WFST_OK;
     if (T < 1 || rows % T) return api_fail(WFST_EINVAL, "with lengths, rows must be a multiple of T >= 1");
     TRY(check_aligned(lengths, 4, "lengths"));
-    return api_check_buffer(lengths, (size_t)(rows / T) * 4, device, "lengths");
+    return buffers.check(lengths, (size_t)(rows / T) * 4, "lengths");
+}
+
+int check_lengths(const int32_t *lengths, int64_t rows, int32_t T, int device)
+{
+    Buffers buffers(device);
+    return check_lengths(lengths, rows, T, buffers);
 }
 
 // A range that a call writes (workspaces among them) must leave its lengths alone:
@@ -143,17 +174,24 @@ int check_off_lengths(const void *p, int64_t bytes, const int32_t *lengths, int6
     return api_fail(WFST_EINVAL, std::string(what) + " must not overlap lengths");
 }
 
-int check_workspace(const void *w, int64_t bytes, size_t need, int device, const void *x, int64_t xb, const void *out,
-                    int64_t ob)
+int check_workspace(const void *w, int64_t bytes, size_t need, Buffers &buffers, const void *x, int64_t xb,
+                    const void *out, int64_t ob)
 {
     if (!need) return WFST_OK;
     if (!w || bytes < 0 || (size_t)bytes < need)
         return api_fail(WFST_EINVAL, "workspace must hold " + std::to_string(need) + " bytes");
     TRY(check_aligned(w, 16, "workspace"));
-    TRY(api_check_buffer(w, need, device, "workspace"));
+    TRY(buffers.check(w, need, "workspace"));
     if (ranges_meet(w, (int64_t)need, out, ob) || ranges_meet(w, (int64_t)need, x, xb))
         return api_fail(WFST_EINVAL, "workspace must not overlap the input or the output");
     return WFST_OK;
+}
+
+int check_workspace(const void *w, int64_t bytes, size_t need, int device, const void *x, int64_t xb, const void *out,
+                    int64_t ob)
+{
+    Buffers buffers(device);
+    return check_workspace(w, bytes, need, buffers, x, xb, out, ob);
 }
 
 }  // namespace
@@ -266,7 +304,8 @@ size_t adapt_offset(const Layer &l, int32_t rows, int32_t x_dtype)
 
 size_t adapt_workspace(const Layer &l, const Adapters &a, int32_t rows, int32_t x_dtype)
 {
-    return adapt_offset(l, rows, x_dtype) + adapters_h_bytes(a, rows) + (size_t)rows * sizeof(int32_t);
+    const AdaptBytes b = adapt_bytes(a, rows);
+    return adapt_offset(l, rows, x_dtype) + b.h + b.lists + b.counts;
 }
 
 int check_same_layer(const Layer &l, int device, wfst_adapters_t ad)
@@ -299,24 +338,26 @@ int layer_logits(wfst_layer_t layer, wfst_adapters_t ad, const int32_t *ids, int
     HIP_TRY(scope.enter(layer->device));
     TRY(check_aligned(x, xe, "x"));
     TRY(check_aligned(out, oe, "out"));
-    TRY(api_check_buffer(x, (size_t)xb, layer->device, "x"));
-    TRY(api_check_buffer(out, (size_t)ob, layer->device, "out"));
-    TRY(check_lengths(lengths, rows, T, layer->device));
+    Buffers buffers(layer->device);
+    TRY(buffers.check(x, (size_t)xb, "x"));
+    TRY(buffers.check(out, (size_t)ob, "out"));
+    TRY(check_lengths(lengths, rows, T, buffers));
     TRY(check_stream(stream, layer->device));
     if (ranges_meet(x, xb, out, ob)) return api_fail(WFST_EINVAL, "out must not overlap x");
     const size_t need = ad ? adapt_workspace(l, ad->a, rows, x_dtype) : layer_workspace(l, rows, x_dtype);
-    TRY(check_workspace(workspace, workspace_bytes, need, layer->device, x, xb, out, ob));
+    TRY(check_workspace(workspace, workspace_bytes, need, buffers, x, xb, out, ob));
     TRY(check_off_lengths(out, ob, lengths, rows, T, "out"));
     TRY(check_off_lengths(workspace, (int64_t)need, lengths, rows, T, "workspace"));
     LayerCall c{x, out, x_stride, out_stride, rows, x_dtype, out_dtype, {lengths, T}, workspace, {}};
     if (ad) {
         const int64_t ib = (int64_t)(rows / rows_per_id) * 4;
         TRY(check_aligned(ids, 4, "ids"));
-        TRY(api_check_buffer(ids, (size_t)ib, layer->device, "ids"));
+        TRY(buffers.check(ids, (size_t)ib, "ids"));
         if (ranges_meet(ids, ib, out, ob) || ranges_meet(ids, ib, workspace, (int64_t)need))
             return api_fail(WFST_EINVAL, "out and workspace must not overlap ids");
         char *h = (char *)workspace + adapt_offset(l, rows, x_dtype);
-        c.ad = {ad->a, ids, rows_per_id, (int32_t *)(h + adapters_h_bytes(ad->a, rows)), h};
+        const AdaptBytes b = adapt_bytes(ad->a, rows);
+        c.ad = {ad->a, ids, rows_per_id, h, (uint4 *)(h + b.h), (int32_t *)(h + b.h + b.lists), 0, 0};
     }
     HIP_TRY(launch_layer(l, c, (hipStream_t)stream));
     return WFST_OK;
@@ -656,7 +697,8 @@ extern "C" int wfst_token_scores(const void *x, int32_t x_dtype, int64_t x_strid
         DeviceScope scope;
         HIP_TRY(scope.enter(device));
         TRY(check_aligned(x, xe, "scores"));
-        TRY(api_check_buffer(x, (size_t)xb, device, "scores"));
+        Buffers buffers(device);
+        TRY(buffers.check(x, (size_t)xb, "scores"));
         const int64_t cb = rows * C * 4, nb = rows * top_n * 4;
         const struct { const void *p; int64_t bytes; const char *name; bool out; } args[] = {
             {C ? tokens : nullptr, cb, "tokens", false}, {temperatures, rows * 4, "temperatures", false},
@@ -669,7 +711,7 @@ extern "C" int wfst_token_scores(const void *x, int32_t x_dtype, int64_t x_strid
             if (!a.p) continue;
             any |= a.out;
             TRY(check_aligned(a.p, 4, a.name));
-            TRY(api_check_buffer(a.p, (size_t)a.bytes, device, a.name));
+            TRY(buffers.check(a.p, (size_t)a.bytes, a.name));
         }
         if (!any) return api_fail(WFST_EINVAL, "no output is wanted");
         for (const auto &o : args) {
@@ -679,10 +721,10 @@ extern "C" int wfst_token_scores(const void *x, int32_t x_dtype, int64_t x_strid
                 if (a.p && &a != &o && ranges_meet(o.p, o.bytes, a.p, a.bytes))
                     return api_fail(WFST_EINVAL, std::string(o.name) + " overlaps " + a.name);
         }
-        TRY(check_lengths(lengths, rows, T, device));
+        TRY(check_lengths(lengths, rows, T, buffers));
         TRY(check_stream(stream, device));
         const size_t need = token_workspace(rows, V, C, top_n, x_dtype);
-        TRY(check_workspace(workspace, workspace_bytes, need, device, x, xb, nullptr, 0));
+        TRY(check_workspace(workspace, workspace_bytes, need, buffers, x, xb, nullptr, 0));
         for (const auto &a : args) {
             if (need && a.p && ranges_meet(workspace, (int64_t)need, a.p, a.bytes))
                 return api_fail(WFST_EINVAL, std::string("workspace overlaps ") + a.name);
