@@ -21,7 +21,7 @@ typedef unsigned long long u64;
 constexpr int kTokenWaves = 4;                 // wavefronts of a row (or of a piece of one)
 constexpr int kTokenThreads = kTokenWaves * kWaveSize;
 constexpr int kMaxPieces = 64;                 // pieces of one row
-constexpr int kTokenGrid = 4096;               // workgroups of a launch: each takes several rows where there are more
+constexpr int kShortGrid = 4096;               // workgroups of a launch over short rows: each takes several where there are more
 
 // Order of labels as integers: larger scores first, then lower indexes; 0: none
 // (-inf, NaN). One zero.
@@ -332,11 +332,13 @@ struct TokenRun {
                 got += (float)x[pack + lane] == a;
         } else {
             const int v = own_v0();
+            float none = -INFINITY;
+            asm volatile("" : "+v"(none));              // (else every row compares ahead of this branch)
 #pragma unroll
             for (int q = 0; q < NV; ++q)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j)
-                    got += z[q][j] > -INFINITY || (v + q * kSpan <= label(v, q, j) && label(v, q, j) < at);
+                    got += z[q][j] > none || (v + q * kSpan <= label(v, q, j) && label(v, q, j) < at);
         }
         return got;
     }
@@ -504,21 +506,6 @@ __device__ __forceinline__ XT gather(const XT *x, int tok, int V) { return x[min
 template <typename XT>
 __device__ __forceinline__ float token_score(XT x, int tok, int V) { return tok >= 0 && tok < V ? (float)x : -INFINITY; }
 
-// What a loop over rows knows of the rows ahead: whether they hold data.
-struct RowAhead {
-    int32_t t, length;
-    __device__ __forceinline__ RowAhead(const RowSet &s, int64_t r, int64_t rows) : t(0), length(0)
-    {
-        if (r >= rows) return;
-        length = 1;
-        if (!s.lengths) return;
-        const int64_t b = r / s.T;
-        t = (int32_t)(r - b * s.T);
-        length = s.lengths[b];
-    }
-    __device__ __forceinline__ bool holds() const { return t < length; }
-};
-
 // A row a wavefront, four to a workgroup, no barriers.
 template <typename XT, int NV>
 __global__ __launch_bounds__(kTokenThreads) void k_token_short(TokenCall c, int32_t room)
@@ -529,32 +516,15 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_short(TokenCall c, int3
     TokenShared<1> &sh = shared[slot];
     u64 *list = lists + (size_t)slot * room;
     typedef TokenRun<XT, 1, NV> Run;
-    const int64_t step = (int64_t)gridDim.x * kTokenWaves;
-    int64_t r = (int64_t)blockIdx.x * kTokenWaves + slot;
-    // the next row's labels and tokens are under way while a row is worked on
-    typename Run::Packs packs;
-    int tok_next = -1;
-    const auto ahead = [&](int64_t row) {
-        Run::fetch((const XT *)c.x + row * c.x_stride, c.V, 0, lane, packs);
-        tok_next = load_tokens(c.tokens + row * c.C, 0, c.C);
-    };
-    RowAhead now(c.set, r, c.rows), next(c.set, r + step, c.rows);
-    if (now.holds()) ahead(r);
-    for (; r < c.rows; r += step) {
-        const RowAhead after(c.set, r + 2 * step, c.rows);
-        const bool here = now.holds(), more = next.holds();
-        now = next;
-        next = after;
-        if (!here) {
-            if (more) ahead(r + step);
-            continue;
-        }
+    for (int64_t r = (int64_t)blockIdx.x * kTokenWaves + slot; r < c.rows; r += (int64_t)gridDim.x * kTokenWaves) {
+        if (!row_active(c.set, r)) continue;
         const XT *x = (const XT *)c.x + r * c.x_stride;
         const int32_t *tokens = c.tokens + r * c.C;
-        Run run(packs, c.V, 0, lane);
-        int tok = tok_next;
+        int tok = load_tokens(tokens, 0, c.C);
+        typename Run::Packs packs;
+        Run::fetch(x, c.V, 0, lane, packs);
         XT raw = c.C ? gather(x, tok, c.V) : (XT)0.0f;
-        if (more) ahead(r + step);
+        Run run(packs, c.V, 0, lane);
         const Heat heat = row_heat(c, r);
         TokenStat s;
         s.m = wave_max_f(run.mine);
@@ -585,10 +555,10 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_short(TokenCall c, int3
 }
 
 // A row, or (CUT) a piece of one, a workgroup.
-template <typename XT, int NV, bool CUT>
-__global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, TokenPlan plan)
+template <typename XT, int WAVES, int NV, bool CUT>
+__global__ __launch_bounds__(WAVES *kWaveSize) void k_token_rows(TokenCall c, TokenPlan plan)
 {
-    constexpr int WAVES = kTokenWaves;
+    constexpr int kThreads = WAVES * kWaveSize;
     typedef TokenRun<XT, WAVES, NV> Run;
     constexpr int kLen = Run::kSpan * NV;
     __shared__ TokenShared<WAVES> sh;
@@ -598,35 +568,13 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
     const int64_t items = CUT ? c.rows * plan.pieces : c.rows;
     const TokenWork work = CUT ? token_work(c.workspace, items, n) : TokenWork{};
 
-    typename Run::Packs packs;
-    int tok_next = -1;
-    const int64_t step = gridDim.x;
-    const auto ahead = [&](int64_t row) {               // (as above)
-        Run::fetch((const XT *)c.x + row * c.x_stride, c.V, 0, tid, packs);
-        tok_next = load_tokens(c.tokens + row * C, 0, C);
-    };
-    RowAhead now(c.set, blockIdx.x, CUT ? 0 : items), next(c.set, blockIdx.x + step, CUT ? 0 : items);
-    if (!CUT && now.holds()) ahead(blockIdx.x);
-    for (int64_t w = blockIdx.x; w < items; w += step) {
+    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
         const int64_t r = CUT ? w / plan.pieces : w;
         const int begin = CUT ? (int)(w - r * plan.pieces) * plan.subs * kLen : 0;
-        bool following = false;
-        if (CUT) {
-            if (!row_active(c.set, r)) continue;
-        } else {
-            const RowAhead after(c.set, w + 2 * step, items);
-            const bool here = now.holds();
-            following = next.holds();
-            now = next;
-            next = after;
-            if (!here) {
-                if (following) ahead(w + step);
-                continue;
-            }
-        }
+        if (!row_active(c.set, r)) continue;
         const XT *x = (const XT *)c.x + r * c.x_stride;
         const int32_t *tokens = c.tokens + r * C;
-        int tok = CUT ? load_tokens(tokens, 0, C) : tok_next;
+        int tok = load_tokens(tokens, 0, C);
         XT raw = (XT)0.0f;
         const Heat heat = row_heat(c, r);
 
@@ -636,10 +584,10 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
             const int first = begin + sub * kLen;
             if (CUT && first >= c.V) break;
             const bool more = CUT && sub + 1 < plan.subs && first + kLen < c.V;
-            if (CUT) Run::fetch(x, c.V, first, tid, packs);
+            typename Run::Packs packs;
+            Run::fetch(x, c.V, first, tid, packs);
             if (sub == 0 && C) raw = gather(x, tok, c.V);
             Run run(packs, c.V, first, tid);
-            if (following) ahead(w + step);
             TokenStat s;
             const float wave_max = wave_max_f(run.mine);
             s.m = wave_max;
@@ -647,7 +595,7 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
             if (lane == 0) sh.red[wave] = s.m;
             if (tid == 0) sh.listed = kept;
             if (sub == 0)
-                for (int i = tid; i < C; i += kTokenThreads) sh.ranks[i] = 0;
+                for (int i = tid; i < C; i += kThreads) sh.ranks[i] = 0;
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < WAVES; ++q) s.m = fmaxf(s.m, sh.red[q]);
@@ -683,7 +631,7 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
                 best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { best[place] = k; });
                 __syncthreads();
                 kept = min(L, n);
-                for (int i = tid; i < kept; i += kTokenThreads) list[i] = best[i];
+                for (int i = tid; i < kept; i += kThreads) list[i] = best[i];
             }
             if (more) __syncthreads();
         }
@@ -691,14 +639,14 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_rows(TokenCall c, Token
         const int L = sh.listed;
         if constexpr (CUT) {
             best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { work.keys[w * n + place] = k; });
-            for (int i = L + tid; i < n; i += kTokenThreads) work.keys[w * n + i] = 0;
+            for (int i = L + tid; i < n; i += kThreads) work.keys[w * n + i] = 0;
             if (tid == 0) work.stats[w] = all;
-            for (int i = tid; i < C; i += kTokenThreads) work.ranks[w * C + i] = sh.ranks[i];
+            for (int i = tid; i < C; i += kThreads) work.ranks[w * C + i] = sh.ranks[i];
         } else {
             const TokenRow row = row_result(all, heat);
             if (n) {
                 best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { write_top(c, row, r, place, k); });
-                for (int i = L + tid; i < n; i += kTokenThreads) write_no_top(c, r, i);
+                for (int i = L + tid; i < n; i += kThreads) write_no_top(c, r, i);
             }
             if (tid == 0 && c.entropies) c.entropies[r] = row.entropy;
             if (wave == WAVES - 1)                      // (the list's first keys lie with the first)
@@ -792,8 +740,9 @@ TokenShape token_shape(int64_t rows, int32_t V, int32_t x_dtype)
     const int vec = x_dtype == kF32 ? 4 : 8, most = 32 / vec, lane = kWaveSize * vec;
     const auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
     if (V <= most * lane) return {1, up(V, lane) <= 4 ? up(V, lane) : most, 1, 1};
+    if (V <= 2 * lane * (most + most / 4)) return {2, x_dtype == kF32 ? std::max(3, up(V, 4 * lane)) * 2 : std::max(3, up(V, 2 * lane)), 1, 1};
     const int span = kTokenWaves * lane;
-    if (V <= most * span) return {kTokenWaves, std::max(2, up(V, span)), 1, 1};
+    if (V <= most * span) return {kTokenWaves, x_dtype == kF32 ? most : up(V, span), 1, 1};
     const int nv = rows * up(V, most * span) >= 512 ? most : 2, len = nv * span;
     const int subs = up(up(V, len), kMaxPieces);
     return {kTokenWaves, nv, up(V, (int64_t)len * subs), subs};
@@ -811,17 +760,17 @@ void short_launch(const TokenCall &c, hipStream_t s)
 {
     const int room = token_list(c, NV, kTokenVec<XT>, false);
     const int64_t groups = (c.rows + kTokenWaves - 1) / kTokenWaves;
-    hipLaunchKernelGGL((k_token_short<XT, NV>), dim3((unsigned)std::min<int64_t>(groups, kTokenGrid)),
+    hipLaunchKernelGGL((k_token_short<XT, NV>), dim3((unsigned)std::min<int64_t>(groups, kShortGrid)),
                        dim3(kTokenThreads), (size_t)kTokenWaves * room * sizeof(u64), s, c, room);
 }
 
-template <typename XT, int NV, bool CUT>
+template <typename XT, int WAVES, int NV, bool CUT>
 void rows_launch(const TokenCall &c, const TokenShape &t, hipStream_t s)
 {
     const TokenPlan plan = {t.pieces, t.subs, token_list(c, NV, kTokenVec<XT>, CUT)};
     const int64_t groups = c.rows * t.pieces;
-    hipLaunchKernelGGL((k_token_rows<XT, NV, CUT>), dim3((unsigned)std::min<int64_t>(groups, kTokenGrid)),
-                       dim3(kTokenThreads), (size_t)plan.list * sizeof(u64), s, c, plan);
+    hipLaunchKernelGGL((k_token_rows<XT, WAVES, NV, CUT>), dim3((unsigned)std::min<int64_t>(groups, kMaxRowGrid)),
+                       dim3(WAVES * kWaveSize), (size_t)plan.list * sizeof(u64), s, c, plan);
 }
 
 template <typename XT>
@@ -838,20 +787,20 @@ hipError_t token_launch(const TokenCall &c, hipStream_t s)
         default: short_launch<XT, kMost>(c, s); break;
         }
     } else if (t.pieces > 1) {
-        if (t.nv == 2) rows_launch<XT, 2, true>(c, t, s);
-        else rows_launch<XT, kMost, true>(c, t, s);
-    } else if (t.nv <= 4) {
-        switch (t.nv) {
-        case 2: rows_launch<XT, 2, false>(c, t, s); break;
-        case 3: rows_launch<XT, 3, false>(c, t, s); break;
-        default: rows_launch<XT, 4, false>(c, t, s); break;
-        }
-    } else if constexpr (kMost > 4) {
-        switch (t.nv) {
-        case 5: rows_launch<XT, 5, false>(c, t, s); break;
-        case 6: rows_launch<XT, 6, false>(c, t, s); break;
-        default: rows_launch<XT, 8, false>(c, t, s); break;
-        }
+        if (t.nv == 2) rows_launch<XT, kTokenWaves, 2, true>(c, t, s);
+        else rows_launch<XT, kTokenWaves, kMost, true>(c, t, s);
+    } else if constexpr (kMost == 8) {
+        if (t.waves == kTokenWaves) rows_launch<XT, kTokenWaves, 8, false>(c, t, s);
+        else if (t.nv == 6) rows_launch<XT, 2, 6, false>(c, t, s);
+        else if (t.nv == 8) rows_launch<XT, 2, 8, false>(c, t, s);
+        else rows_launch<XT, 2, 10, false>(c, t, s);
+    } else if (t.waves == kTokenWaves) {
+        if (t.nv == 3) rows_launch<XT, kTokenWaves, 3, false>(c, t, s);
+        else rows_launch<XT, kTokenWaves, 4, false>(c, t, s);
+    } else {
+        if (t.nv == 3) rows_launch<XT, 2, 3, false>(c, t, s);
+        else if (t.nv == 4) rows_launch<XT, 2, 4, false>(c, t, s);
+        else rows_launch<XT, 2, 5, false>(c, t, s);
     }
     if (t.pieces > 1)
         hipLaunchKernelGGL(k_token_join, dim3((unsigned)std::min<int64_t>(c.rows, kMaxRowGrid)), dim3(kTokenThreads), 0,
