@@ -16,8 +16,10 @@ namespace {
 // unit's binary32 products take it as it is; with up in bfloat16 as three bfloat16 parts
 // of 8 bits; with up in binary16 as hi + lo / 2^11, two binary16 values scaled by a
 // power of two per row and 16 ranks (off by at most 2^-23 of itself or 2^-50 of the
-// largest of those 16). Utterances of 16000 rows x 5000 x 1024, rank 32, binary16: the
-// products in binary32 took 211 us, these TBD.
+// largest of those 16). 16000 rows x 5000 x 1024 of binary16, one slot of rank 16, 32, 128, us
+// for the whole call: 406, 420, 562, without a slot 363; 64 rows x 32003 x 2050 over 64 slots
+// of rank 16, 32: 72, 106 in binary32 (up alone 131, 262 MB: 4.6, 4.2 TB/s of the time that the
+// layer does not take), 69, 83 in bfloat16; without a slot 48.
 
 constexpr int kRowsTile = 16;
 

@@ -14,6 +14,12 @@ namespace {
 // digits (log1p). A rank is a count over ballots. The alternatives: the n-th largest
 // of the threads' own largest scores is a bound that n labels reach and few others;
 // those it leaves go to a list in LDS, where each counts the ones before it.
+//
+// What bounds it: the vector instructions, about 16 a label (the exponential counts 4)
+// and some 250 a wavefront; binary32 rows without tokens and alternatives run at 5.9 TB/s
+// (16000 x 5000 in 54 us), binary16 ones at 4.1 (39 us; one token 49, with 4 alternatives 61).
+// Registers decide how many rows are under way at once: loading the next row ahead cost
+// more of them than it hid (binary16 107 us).
 
 typedef unsigned long long u64;
 
@@ -732,20 +738,30 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32
     }
 }
 
-// Runs of a wavefront's or a workgroup's registers that a row takes.
+// Wavefronts and packs a thread of a row (or a run of one), its pieces and their runs.
+// One wavefront a row up to 2048 labels, two up to 5120, four up to 8192, pieces of that
+// beyond. 16000 rows, one given token and no / 4 / 20 / 64 alternatives, us: 2000 binary16
+// labels on 1 / 2 wavefronts 23 / 30, 32 / 41, 41 / 48, 129 / 74; 5000 on 2 / 4 46 / 55, 60 /
+// 79, 72 / 92, 147 / 117 (binary32 68 / 81, 83 / 107, 97 / 120, 155 / 148), 3000 82 / 129 with
+// 64: many alternatives take more wavefronts where a thread holds many labels. Fewer rows
+// than fill the card take about as long either way. Pieces of 8192 labels, or of 2048 and
+// more of them: one row of 131072 18 / 19 us, 64 rows 21 / 34.
 struct TokenShape { int waves, nv, pieces, subs; };
 
-TokenShape token_shape(int64_t rows, int32_t V, int32_t x_dtype)
+TokenShape token_shape(int32_t V, int32_t top_n, int32_t x_dtype)
 {
-    const int vec = x_dtype == kF32 ? 4 : 8, most = 32 / vec, lane = kWaveSize * vec;
+    const bool f32 = x_dtype == kF32, many = top_n > kMaxTop / 2;
+    const int vec = f32 ? 4 : 8, most = 32 / vec, lane = kWaveSize * vec;
     const auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
-    if (V <= most * lane) return {1, up(V, lane) <= 4 ? up(V, lane) : most, 1, 1};
-    if (V <= 2 * lane * (most + most / 4)) return {2, x_dtype == kF32 ? std::max(3, up(V, 4 * lane)) * 2 : std::max(3, up(V, 2 * lane)), 1, 1};
-    const int span = kTokenWaves * lane;
-    if (V <= most * span) return {kTokenWaves, x_dtype == kF32 ? most : up(V, span), 1, 1};
-    const int nv = rows * up(V, most * span) >= 512 ? most : 2, len = nv * span;
+    if (V <= (many ? most / 2 : most) * lane) return {1, up(V, lane) <= 4 ? up(V, lane) : most, 1, 1};
+    if (V <= 2 * lane * (many ? most : most + most / 4)) {
+        const int nv = f32 ? std::max(3, up(V, 4 * lane)) * 2 : std::max(3, up(V, 2 * lane));
+        return {2, nv, 1, 1};
+    }
+    const int len = kTokenWaves * lane * most;
+    if (V <= len) return {kTokenWaves, f32 ? most : std::max(3, up(V, kTokenWaves * lane)), 1, 1};
     const int subs = up(up(V, len), kMaxPieces);
-    return {kTokenWaves, nv, up(V, (int64_t)len * subs), subs};
+    return {kTokenWaves, most, up(V, (int64_t)len * subs), subs};
 }
 
 // u64 of a row's list in LDS: the labels that may reach the bound, 8 zeros, and twice
@@ -777,7 +793,7 @@ template <typename XT>
 hipError_t token_launch(const TokenCall &c, hipStream_t s)
 {
     constexpr int kMost = 32 / kTokenVec<XT>;
-    const TokenShape t = token_shape(c.rows, c.V, c.x_dtype);
+    const TokenShape t = token_shape(c.V, c.top_n, c.x_dtype);
     if (t.waves == 1) {
         switch (t.nv) {
         case 1: short_launch<XT, 1>(c, s); break;
@@ -787,8 +803,7 @@ hipError_t token_launch(const TokenCall &c, hipStream_t s)
         default: short_launch<XT, kMost>(c, s); break;
         }
     } else if (t.pieces > 1) {
-        if (t.nv == 2) rows_launch<XT, kTokenWaves, 2, true>(c, t, s);
-        else rows_launch<XT, kTokenWaves, kMost, true>(c, t, s);
+        rows_launch<XT, kTokenWaves, kMost, true>(c, t, s);
     } else if constexpr (kMost == 8) {
         if (t.waves == kTokenWaves) rows_launch<XT, kTokenWaves, 8, false>(c, t, s);
         else if (t.nv == 6) rows_launch<XT, 2, 6, false>(c, t, s);
@@ -812,7 +827,7 @@ hipError_t token_launch(const TokenCall &c, hipStream_t s)
 
 size_t token_workspace(int64_t rows, int32_t V, int32_t C, int32_t top_n, int32_t x_dtype)
 {
-    const TokenShape t = token_shape(rows, V, x_dtype);
+    const TokenShape t = token_shape(V, top_n, x_dtype);
     if (t.pieces == 1) return 0;
     return (size_t)rows * t.pieces * (sizeof(TokenStat) + (size_t)top_n * sizeof(u64) + (size_t)C * 4);
 }
