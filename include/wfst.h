@@ -681,6 +681,9 @@ int wfst_adapters_load(wfst_adapters_t adapters, int32_t slot, int32_t rank, con
  * of slot ids[r / rows_per_id] (device int32 [rows / rows_per_id]); an id outside
  * [0, slots) or of an empty slot is none: such rows hold the layer's y. x, down and
  * up count with all their bits; h and the sums are binary32, and out is rounded once.
+ * With up in binary16, h meets it off by at most 2^-23 of itself, or 2^-50 of the largest
+ * finite |h| among a row's 16 ranks that begin at a multiple of 16; with up in
+ * bfloat16, what of h lies below 2^-126 may be lost.
  * Rows take nothing from each other's adapters, infinities and NaN included. out and
  * the workspace (wfst_layer_adapted_workspace's bytes) must not overlap ids; all
  * else is as for wfst_layer_logits.

@@ -134,7 +134,7 @@ def test_ids_that_are_no_slot(M, N):
 
 
 @pytest.mark.parametrize("M,N", [(16, 90), (16, 24600), (40, 17000), (600, 600)])
-@pytest.mark.parametrize("a", ["f32", "bf16"])
+@pytest.mark.parametrize("a", ["f32", "f16", "bf16"])
 def test_infinities_and_nan_stay_in_their_rows(M, N, a):
     K = 200
     layer, _ = _layer(4, K, N)
@@ -311,6 +311,18 @@ def test_rows_do_not_depend_on_the_rows_beside_them(N):
     y = layer.logits(h, adapters=ad, ids=ids)
     for lo, hi in ((0, 1), (3, 4), (5, 11)) if M == 16 else ((0, 20), (33, 80)):
         assert torch.equal(layer.logits(h[lo:hi], adapters=ad, ids=ids[lo:hi]), y[lo:hi])
+
+
+def test_most_slots_of_a_group():
+    """Each of 64 rows with a slot of eight blocks of its own: lists past 64 entries."""
+    K, N = 140, 16500
+    layer, arrays = _layer(33, K, N)
+    for a in ("f16", "f32"):
+        ad = wb.Adapters(layer, 64, 128, dtype=a)
+        held = _fill(ad, layer, 11, [128 - s % 7 for s in range(64)], a)
+        h = torch.randn(64, K, device="cuda")
+        ids = (torch.arange(64, device="cuda", dtype=torch.int32) * 11) % 64
+        _check(layer.logits(h, adapters=ad, ids=ids), h, arrays, ids.cpu().numpy(), held)
 
 
 def test_streams_at_once():

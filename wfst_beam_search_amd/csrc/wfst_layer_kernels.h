@@ -308,14 +308,14 @@ const int at = (u * 16 + j * 4 + quad) * RP + arow;
 // scale factors. One wavefront makes one such block.
 constexpr size_t kBlockHalves = 4 * 64 * 8;            // halves of one part of a block
 
-template <typename XT>
+template <typename XT, int WAVES>
 __device__ __forceinline__ void make_operands(const Layer &l, const LayerCall &c, half8_t *xa, float *xf)
 {
     constexpr int P = kParts<XT>;
     const int lane = threadIdx.x & 63;
     const int row = lane & 15, quad = lane >> 4;
     const int64_t nblk = (int64_t)((c.M + kRowsM - 1) / kRowsM) * l.kb;
-    const int64_t u = (int64_t)blockIdx.x * (blockDim.x / kWaveSize) + (threadIdx.x >> 6);
+    const int64_t u = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
     if (u >= nblk) return;
     const int64_t mt = u / l.kb;
     const int b = (int)(u - mt * l.kb);
@@ -347,7 +347,7 @@ __device__ __forceinline__ void make_operands(const Layer &l, const LayerCall &c
 template <typename XT>
 __global__ __launch_bounds__(256) void k_layer_operands(Layer l, LayerCall c, half8_t *xa, float *xf)
 {
-    make_operands<XT>(l, c, xa, xf);
+    make_operands<XT, 4>(l, c, xa, xf);
 }
 
 // h of the adapters, by tiles of 16 rows or row by row; the workgroups before those
@@ -356,12 +356,13 @@ template <typename XT, typename AT, bool TILES>
 __global__ __launch_bounds__(TILES ? 256 : kRowWaves * kWaveSize)
 void k_layer_shrink(Layer l, LayerCall c, half8_t *xa, float *xf, unsigned operands, unsigned items)
 {
+    constexpr int kWaves = TILES ? 4 : kRowWaves;
     __shared__ __align__(16) char smem[TILES ? kShrinkBytes : 64];
     const unsigned b = blockIdx.x;
     if (b < operands) {
-        make_operands<XT>(l, c, xa, xf);
+        make_operands<XT, kWaves>(l, c, xa, xf);
     } else if (b >= operands + items) {
-        const int64_t group = (int64_t)(b - operands - items) * (blockDim.x / kWaveSize) + threadIdx.x / kWaveSize;
+        const int64_t group = (int64_t)(b - operands - items) * kWaves + threadIdx.x / kWaveSize;
         if (group * c.ad.group < c.M) make_lists(c, group);
     } else if constexpr (TILES) {
         shrink_tile<XT, AT>(c, l.K, b - operands, (float4_t *)smem);
