@@ -84,7 +84,7 @@ __device__ __forceinline__ void shrink_row(const LayerCall &c, int32_t K, int64_
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m = item / ad.a.rb;
     const int jb = (int)(item - m * ad.a.rb);
-    int slot = row_active(c.rows, m) ? ad.ids[(uint32_t)m / (uint32_t)ad.per_id] : -1;
+    int slot = row_active32(c.rows, (uint32_t)m) ? ad.ids[(uint32_t)m / (uint32_t)ad.per_id] : -1;
     if (slot >= ad.a.slots) slot = -1;
     const int rank = slot >= 0 ? ad.a.ranks[slot] : 0, j = jb * 16 + wave;
     if (jb * 16 >= rank) return;
@@ -181,7 +181,7 @@ __device__ __forceinline__ void shrink_tile(const LayerCall &c, int32_t K, int64
     const AdaptCall &ad = c.ad;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
     const int64_t m = tile * kRowsTile + col;
-    const int id = m < c.M && row_active(c.rows, m) ? row_adapter(ad, m) : -1;
+    const int id = m < c.M && row_active32(c.rows, (uint32_t)m) ? row_adapter(ad, m) : -1;
     const XT *x = (const XT *)c.x + (id >= 0 ? m : 0) * c.x_stride;
     const int kb = ad.a.kp / 32, b0 = kb * wave / 4, b1 = kb * (wave + 1) / 4;
     uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
@@ -240,7 +240,7 @@ __device__ __forceinline__ void make_lists(const LayerCall &c, int64_t group)
     const AdaptCall &ad = c.ad;
     const int lane = threadIdx.x & 63, G = ad.group, cap = G * ad.a.rb;
     const int64_t m = group * G + lane;
-    const int id = lane < G && m < c.M && row_active(c.rows, m) ? row_adapter(ad, m) : -1;
+    const int id = lane < G && m < c.M && row_active32(c.rows, (uint32_t)m) ? row_adapter(ad, m) : -1;
     const int blocks = id >= 0 ? (ad.a.ranks[id] + 15) / 16 : 0;
     uint64_t mine = 0;
     for (int q = 0; q < G; ++q) mine |= (uint64_t)(id == __builtin_amdgcn_readlane(id, q)) << q;

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kLayerThreads, AD && SPL == 1 ? 4 : 1) void k_layer
     // staging: 16 * RP threads (at most 64) take a block of 128 features, each up to four runs of 8
     const int per = min(64, 16 * RP), bpw = 64 / per;
     const int l2 = lane % per, sr = l2 % RP, s0 = l2 / RP, sstep = per / RP, spl = SPL == 1 ? 1 : 16 / sstep;
-    const bool there = sr < M && row_active(c.rows, m0 + sr);
+    const bool there = sr < M && row_active32(c.rows, (uint32_t)(m0 + sr));
     const int longest = (l.kb + KS - 1) / KS;
     float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
     const int arow = min(col, RP - 1), frow = min(quad * 4, RP - 1);
@@ -299,7 +299,7 @@ const int at = (u * 16 + j * 4 + quad) * RP + arow;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = quad * 4 + i;
-        if (m < M && row_active(c.rows, m0 + m)) store_y(c, m0 + m, n, acc[i] + bias);
+        if (m < M && row_active32(c.rows, (uint32_t)(m0 + m))) store_y(c, m0 + m, n, acc[i] + bias);
     }
 }
 
@@ -320,7 +320,7 @@ __device__ __forceinline__ void make_operands(const Layer &l, const LayerCall &c
     const int64_t mt = u / l.kb;
     const int b = (int)(u - mt * l.kb);
     const int64_t m = mt * kRowsM + row;
-    const bool there = m < c.M && row_active(c.rows, m);
+    const bool there = m < c.M && row_active32(c.rows, (uint32_t)m);
     const XT *x = (const XT *)c.x + (there ? m : 0) * c.x_stride;
     float v[4][8], mx = 0.0f, inv = 1.0f;
 #pragma unroll
@@ -371,6 +371,9 @@ void k_layer_shrink(Layer l, LayerCall c, half8_t *xa, float *xf, unsigned opera
     }
 }
 
+// LDS of the product below for x: two buffers of operands and factors.
+__host__ __device__ constexpr int many_bytes(int parts, int mt) { return 2 * 2 * mt * (parts * (int)kBlockHalves * 2 + 64); }
+
 // The product for many rows: a workgroup of 8 wavefronts makes 16 MT rows by 128
 // output features. Each wavefront owns 32 features; the two halves of the
 // workgroup take alternate blocks of 128 input features (joined in LDS at the
@@ -383,7 +386,7 @@ void k_layer_shrink(Layer l, LayerCall c, half8_t *xa, float *xf, unsigned opera
 // the wait for the loads costs more (binary32 3 % of its 12.8 ms, groups of 32 3 %, 32
 // rows 7 %).
 template <typename XT, int WS, int GPT, int MT, bool AD>
-__global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf)
+__global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k_layer_many(Layer l, LayerCall c, const half8_t *xa, const float *xf, int h_at)
 {
     constexpr int P = kParts<XT>;
     constexpr int NT = 2;
@@ -455,7 +458,12 @@ __global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k
     // (one workgroup a CU where x has two parts; binary16 leaves registers for two with the shortest ring)
     constexpr int kAhead = P == 2 ? 8 : kScaled<XT> || GPT > 1 ? 4 : 2;
     AdapterTiles<MT, NT, kAhead> tiles;
-    if constexpr (AD) tiles.begin(c.ad, mblk, half);
+    bool listed = false;                                // (the same for the workgroup)
+    if constexpr (AD) {
+        tiles.begin(c.ad, mblk, half);
+        listed = c.ad.counts[mblk * 2] | c.ad.counts[mblk * 2 + 1];
+        if (listed && h_at >= many_bytes(P, MT)) stage_h(c, (int64_t)mblk * MT, MT, smem + h_at);
+    }
     float4_t acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -535,11 +543,12 @@ __global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k
         __syncthreads();
     }
     if constexpr (AD) {
-        if (c.ad.counts[mblk * 2] | c.ad.counts[mblk * 2 + 1]) {        // (the same for the workgroup)
-            char *hs = smem + 4 * MT * NT * kWaveSize * sizeof(float4_t);      // (behind joint)
-            stage_h(c, (int64_t)mblk * MT, MT, hs);
-            __syncthreads();
-            tiles.add(c.ad, hs, nt0, acc);
+        if (listed) {
+            if (h_at < many_bytes(P, MT)) {
+                stage_h(c, (int64_t)mblk * MT, MT, smem + h_at);
+                __syncthreads();
+            }
+            tiles.add(c.ad, smem + h_at, nt0, acc);
         }
     }
     if (half) {
@@ -561,7 +570,7 @@ __global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t r = ((int64_t)mblk * MT + m) * kRowsM + quad * 4 + i;
-                if (r < c.M && row_active(c.rows, r)) store_y(c, r, f, y[i] + bias);
+                if (r < c.M && row_active32(c.rows, (uint32_t)r)) store_y(c, r, f, y[i] + bias);
             }
         }
     }
@@ -671,10 +680,18 @@ hipError_t layer_many(const Layer &l, const LayerCall &call, hipStream_t s)
     half8_t *xa = (half8_t *)c.workspace;
     float *xf = (float *)((char *)c.workspace + operand_bytes(l, c.M, c.x_dtype));
     launch_before<XT, AD>(l, c, MT * kRowsM, 2, xa, xf, blocks, s);
-    size_t lds = 2 * 2 * MT * (kParts<XT> * kBlockHalves * 2 + 64);
-    if (AD) lds = std::max(lds, 8 * MT * kWaveSize * sizeof(float4_t) + (size_t)MT * c.ad.a.rb * h_block_bytes(c.ad.a.dtype));
+    // h lies behind the operands, there from the start, where that leaves as many workgroups
+    // on a CU, else behind what the halves join, once the operands are done with
+    constexpr size_t kLds = 160 * 1024;
+    size_t lds = many_bytes(kParts<XT>, MT), h_at = lds;
+    if (AD) {
+        const size_t h = (size_t)MT * c.ad.a.rb * h_block_bytes(c.ad.a.dtype);
+        if (lds + h > kLds || kLds / (lds + h) < kLds / lds) h_at = 8 * MT * kWaveSize * sizeof(float4_t);
+        lds = std::max(lds, h_at + h);
+    }
     const dim3 g((l.nt + 7) / 8, (c.M + MT * kRowsM - 1) / (MT * kRowsM));
-    hipLaunchKernelGGL((k_layer_many<XT, WS, GPT, MT, AD>), g, dim3(512), lds, s, l, c, (const half8_t *)xa, (const float *)xf);
+    hipLaunchKernelGGL((k_layer_many<XT, WS, GPT, MT, AD>), g, dim3(512), lds, s, l, c, (const half8_t *)xa, (const float *)xf,
+                       (int)h_at);
     return hipGetLastError();
 }
 

@@ -18,6 +18,15 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 
+// The same for a call of fewer than 2^32 rows (a division of 64 bits takes some 100
+// instructions).
+__device__ __forceinline__ bool row_active32(const RowSet &s, uint32_t r)
+{
+    if (!s.lengths) return true;
+    const uint32_t b = r / (uint32_t)s.T;
+    return (int32_t)(r - b * (uint32_t)s.T) < s.lengths[b];
+}
+
 // The adapter slot of row r of a call, -1: none.
 __device__ __forceinline__ int row_adapter(const AdaptCall &ad, int64_t r)
 {
