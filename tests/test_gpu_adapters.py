@@ -325,6 +325,20 @@ def test_most_slots_of_a_group():
         _check(layer.logits(h, adapters=ad, ids=ids), h, arrays, ids.cpu().numpy(), held)
 
 
+@pytest.mark.parametrize("M,N", [(20, 300), (70, 17000)])
+def test_sets_of_several_types_and_ranks_beside_one_layer(M, N):
+    K = 96
+    layer, arrays = _layer(35, K, N)
+    h = torch.randn(M, K, device="cuda")
+    ids = np.resize(np.array([0, 1, -1], np.int32), M)
+    sets = []
+    for a, rank in (("f32", 16), ("f16", 16), ("bf16", 16), ("f16", 40), ("bf16", 3)):
+        ad = wb.Adapters(layer, 2, rank, dtype=a)
+        sets.append((ad, _fill(ad, layer, rank, [rank, 1], a)))
+    for ad, held in sets + sets[::-1]:
+        _check(layer.logits(h, adapters=ad, ids=ids), h, arrays, ids, held)
+
+
 def test_streams_at_once():
     K, N, R = 300, 17000, 70
     layer, _ = _layer(24, K, N)

@@ -1,5 +1,5 @@
 // gfx950 (CDNA4) kernels that lay a low-rank adapter out in its slot. The products run beside the
-// output layer's (wfst_adapters_device.h, wfst_layer.hip).
+// output layer's (wfst_adapters_device.h, wfst_layer_kernels.h).
 #include "wfst_score_device.h"
 
 namespace wfst {

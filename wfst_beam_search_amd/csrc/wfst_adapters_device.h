@@ -1,4 +1,4 @@
-// Device code of the low-rank adapters beside the output layer, for wfst_layer.hip. Not part of the ABI.
+// Device code of the low-rank adapters beside the output layer, for wfst_layer_kernels.h. Not part of the ABI.
 #pragma once
 
 #include "wfst_score_device.h"

@@ -1,5 +1,5 @@
 // Shared by the host entry points (wfst_score_api.cpp) and the gfx950 kernels
-// (wfst_layer.hip, wfst_adapters.hip, wfst_norm.hip, wfst_sample.hip, wfst_tokens.hip)
+// (wfst_layer*.hip, wfst_adapters.hip, wfst_norm.hip, wfst_sample.hip, wfst_tokens.hip)
 // of the operators around the search: the output layer with 4-bit weights and the
 // low-rank adapters beside it, the log-softmax, the draw of tokens and the scores of
 // given tokens. Not part of the ABI.

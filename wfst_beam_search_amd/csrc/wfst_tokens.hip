@@ -499,7 +499,7 @@ __device__ __forceinline__ void write_no_top(const TokenCall &c, int64_t r, int 
     c.top_log_probs[r * c.top_n + place] = -INFINITY;
 }
 
-// The i-th given token on, a lane each (-1: none), and their scores (-inf: no label).
+// The given tokens from the i-th on, a lane each (-1: none), and their scores (-inf: no label).
 __device__ __forceinline__ int load_tokens(const int32_t *tokens, int i, int C)
 {
     const int lane = threadIdx.x & 63;
@@ -644,8 +644,10 @@ __global__ __launch_bounds__(WAVES *kWaveSize) void k_token_rows(TokenCall c, To
 
         const int L = sh.listed;
         if constexpr (CUT) {
-            best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { work.keys[w * n + place] = k; });
-            for (int i = L + tid; i < n; i += kThreads) work.keys[w * n + i] = 0;
+            if (n) {
+                best_of<WAVES>(list, L, n, tid, [&](int place, u64 k) { work.keys[w * n + place] = k; });
+                for (int i = L + tid; i < n; i += kThreads) work.keys[w * n + i] = 0;
+            }
             if (tid == 0) work.stats[w] = all;
             for (int i = tid; i < C; i += kThreads) work.ranks[w * C + i] = sh.ranks[i];
         } else {

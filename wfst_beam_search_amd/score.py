@@ -264,7 +264,7 @@ class OutputLayer:
         self.handle = h
         self._logits = lib.wfst_layer_logits
         self._adapted = lib.wfst_layer_adapted_logits
-        self._bytes = {}                        # (element type, rows, rank blocks) -> workspace bytes
+        self._bytes = {}                        # (element type, rows, the adapters' blocks) -> workspace bytes
         self.device = device
         self.in_features, self.out_features = K, N
 
@@ -292,7 +292,7 @@ class OutputLayer:
             raise ValueError("ids need adapters")
         out = _out(out, (*lead, self.out_features), _named(dtype), self.device, other)
         _, ostep = _rows(out, "out")
-        key = (code, rows, 0 if adapters is None else -(-adapters.rank // 16))
+        key = (code, rows) if adapters is None else (code, rows, adapters._blocks)
         need = self._bytes.get(key)
         if need is None:
             n = ctypes.c_int64(0)
@@ -384,6 +384,7 @@ class Adapters:
         lib = load_library()
         self._dtype = _named(dtype)
         self.slots, self.rank = _int32(slots, "slots"), _int32(rank, "rank")
+        self._blocks = (DTYPES[dtype], -(-self.rank // 16))      # what a call's workspace goes by
         self.in_features, self.out_features, self.device = layer.in_features, layer.out_features, layer.device
         raw, _ = _stream(stream, self.device)
         desc = _AdaptersDesc(self.in_features, self.out_features, self.slots, self.rank, DTYPES[dtype])
