@@ -356,7 +356,8 @@ def _ids(ids, lead, slots, device, other):
     if isinstance(ids, torch.Tensor) and ids.is_cuda:
         if ids.dtype != torch.int32 or not ids.is_contiguous():
             raise TypeError("ids on the GPU must be a packed int32 tensor")
-        _gpu(ids, "ids", device)
+        if ids.device != device:
+            raise ValueError(f"ids must be on {device}")
     else:
         host = ids.numpy() if isinstance(ids, torch.Tensor) else np.array(ids)
         if host.size and (host.dtype.kind not in "iu" or int(host.max()) >= slots):
@@ -608,17 +609,21 @@ def token_scores(scores, tokens=None, top_n: int = 0, temperature=1.0, lengths=N
         if len(out) > 5:
             raise ValueError("out must be the result's tensors")
         res = TokenScores(*out, *(None,) * (5 - len(out)))
-        want = ((tshape, torch.float32), (tshape, torch.int32), (shape, torch.float32),
-                ((*shape, n) if n else None, torch.int32), ((*shape, n) if n else None, torch.float32))
-        for o, (w, dt), name in zip(res, want, res._fields):
-            if (o is None) != (w is None):
-                raise ValueError(f"out must {'not ' if w is None else ''}hold {name}")
-            if o is not None and not _checked(o, torch.Size(w), dt, device).is_contiguous():
-                raise ValueError("out must be packed tensors")
-        _written(tuple(o for o in res if o is not None))
+        i, f = torch.int32, torch.float32
+        top = (*shape, n) if n else None
+        dual = _fw._current_level >= 0              # (set by _gpu above)
+        for o, w, dt, name in zip(res, (tshape, tshape, shape, top, top), (f, i, f, i, f), res._fields):
+            if o is None or w is None:
+                if o is not None or w is not None:
+                    raise ValueError(f"out must {'not ' if w is None else ''}hold {name}")
+            elif (dual or type(o) is not torch.Tensor or o.dtype is not dt or o.shape != w or o.device != device
+                  or o.requires_grad or not o.is_contiguous()):
+                if not _checked(o, torch.Size(w), dt, device).is_contiguous():      # (says what is wrong)
+                    raise ValueError("out must be packed tensors")
+        _written([o for o in res if o is not None])
     need = _token_bytes(code, rows, V, C, n)
     work = _workspace(need, device, other)
-    dst = _TokenScoresOut(*(_p(o) for o in res))
+    dst = _TokenScoresOut(*[None if o is None else o.data_ptr() for o in res])
     _check(lib.wfst_token_scores(scores.data_ptr(), code, step, rows, V, _p(tokens), C, n, float(t), _p(ts),
                                  _p(lengths), T, ctypes.byref(dst), _p(work), need, raw))
     return res
