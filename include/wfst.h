@@ -565,7 +565,7 @@ int wfst_decoder_kernel_times(wfst_decoder_t d, double *out, int32_t n);
 
 /*
  * Operators around the search: what makes log_prob from a model's last hidden
- * states, and the draw of tokens from scores. They take no decoder. Each call is
+ * states, the draw of tokens from scores, and the scores of given tokens. They take no decoder. Each call is
  * asynchronous: it is ordered on the caller's HIP stream (null: the null stream
  * of the operands' device) and returns without waiting for it, so operands must
  * stay valid until the stream has passed it. None allocates device memory or
