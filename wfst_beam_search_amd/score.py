@@ -362,7 +362,7 @@ def _ids(ids, lead, slots, device, other):
         host = ids.numpy() if isinstance(ids, torch.Tensor) else np.array(ids)
         if host.size and (host.dtype.kind not in "iu" or int(host.max()) >= slots):
             raise ValueError(f"ids must be integers below {slots}, the adapters' slots")
-        host = np.array(np.maximum(host, -1), dtype=np.int32)
+        host = np.array(np.maximum(host.astype(np.int64), -1), dtype=np.int32)    # (unsigned types hold no -1)
         ids = torch.from_numpy(host).to(device)         # (the copy has ended when this returns)
         if other is not None:
             ids.record_stream(other)
