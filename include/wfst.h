@@ -683,7 +683,8 @@ int wfst_adapters_load(wfst_adapters_t adapters, int32_t slot, int32_t rank, con
  * up count with all their bits; h and the sums are binary32, and out is rounded once.
  * With up in binary16, h meets it off by at most 2^-23 of itself, or 2^-50 of the largest
  * finite |h| among a row's 16 ranks that begin at a multiple of 16; with up in
- * bfloat16, what of h lies below 2^-126 may be lost.
+ * bfloat16, what of h lies below 2^-126 may be lost. Infinities and NaN in x, down
+ * and up go where the formula takes them (an infinite up meets a nonzero h of any size).
  * Rows take nothing from each other's adapters, infinities and NaN included. out and
  * the workspace (wfst_layer_adapted_workspace's bytes) must not overlap ids; all
  * else is as for wfst_layer_logits.

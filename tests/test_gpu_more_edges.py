@@ -1,0 +1,46 @@
+"""Edges of the adapters beside the output layer and of the token scores, each against its definition."""
+
+import numpy as np
+import pytest
+import torch
+
+import wfst_beam_search_amd as wb
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+E = 2.0 ** -23
+INF = float("inf")
+# rows and features: few rows with K over the wavefronts, with a wavefront a tile, many rows, past 512 rows (few, many)
+PATHS = [(5, 70), (2, 24580), (40, 17000), (600, 600), (600, 17000)]
+
+
+def _silent_layer(K, N):
+    """A layer whose own logits are 0: scales of 0, no bias."""
+    q = torch.randint(0, 256, (N, (K + 1) // 2), dtype=torch.uint8, device="cuda")
+    return wb.OutputLayer(q, torch.zeros(N, -(-K // 32), device="cuda"), in_features=K, group_size=32)
+
+
+@pytest.mark.parametrize("M,N", PATHS)
+@pytest.mark.parametrize("a,big,small", [
+    ("f32", 2.0 ** 30, 2.0 ** -15), ("f32", 1.0, 2.0 ** -149),
+    ("bf16", 2.0 ** 30, 2.0 ** -15), ("bf16", 1.0, 2.0 ** -133), ("bf16", 1.0, 2.0 ** -140), ("bf16", 1.0, 2.0 ** -149),
+    ("f16", 2.0 ** 30, 2.0 ** -15), ("f16", 2.0 ** 30, 2.0 ** -126), ("f16", 2.0 ** 100, 2.0 ** -149),
+    ("f16", 2.0 ** 30, 1.25 * 2.0 ** -10),
+])
+def test_an_infinite_weight_meets_a_small_h(M, N, a, big, small):
+    """h of very different sizes among a row's 16 ranks: the small ones' infinite weights give infinities of their
+    sign (not NaN), and their finite weights their product, off by at most 2^-50 of the largest h (binary16) or what
+    lies below 2^-126 (bfloat16), and a binary32 rounding or two."""
+    K = 32
+    layer = _silent_layer(K, N)
+    ad = wb.Adapters(layer, 1, 20, dtype=a)
+    down, up = torch.eye(20, K), torch.zeros(N, 20)
+    up[1::4, 1], up[2::4, 2], up[3::4, 3] = INF, INF, 3.0
+    ad.load(0, down.to(DT[a]).cuda(), up.to(DT[a]).cuda())
+    h = torch.zeros(M, K)
+    h[:, 0], h[:, 1], h[:, 2], h[:, 3] = big, small, -small, small
+    y = layer.logits(h.cuda(), adapters=ad, ids=np.zeros(M, np.int32)).double().cpu()
+    assert (y[:, 0::4] == 0).all() and (y[:, 1::4] == INF).all() and (y[:, 2::4] == -INF).all()
+    lost = {"f32": 0.0, "f16": 2.0 ** -50 * big, "bf16": 2.0 ** -126}[a]
+    assert ((y[:, 3::4] - 3 * small).abs() <= 3 * lost + 3 * E * 3 * small + 2.0 ** -149).all()

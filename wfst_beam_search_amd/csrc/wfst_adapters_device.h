@@ -43,6 +43,8 @@ __device__ __forceinline__ int block_exponent(float mx)
 }
 
 // Writes h of one row (of 16) and rank (of 16); mx: the largest finite |h| of the row's 16.
+// An infinite up meets the first part alone, which therefore is 0 only where h is: below
+// its type's smallest number it holds that one, and the next part the difference.
 template <typename AT>
 __device__ __forceinline__ void put_h(char *block, int row, int j, float v, float mx)
 {
@@ -52,14 +54,16 @@ __device__ __forceinline__ void put_h(char *block, int row, int j, float v, floa
     } else if constexpr (__is_same(AT, _Float16)) {
         const int e = block_exponent(mx);
         const float s = v * ldexpf(1.0f, -e);
-        const _Float16 hi = (_Float16)s;
+        _Float16 hi = (_Float16)s;
+        if (hi == (_Float16)0.0f && v != 0.0f) hi = (_Float16)copysignf(0x1p-24f, v);      // (lo takes it back)
         ((_Float16 *)block)[at] = hi;
         ((_Float16 *)block)[256 + at] = (_Float16)(fabsf(s) < INFINITY ? (s - (float)hi) * 2048.0f : 0.0f);
         if (j == 0) ((float *)(block + 1024))[row] = ldexpf(1.0f, e);
     } else {
         // (cut, not rounded: the parts add up to v and none passes the largest number)
         const bool finite = fabsf(v) < INFINITY;
-        const float a = finite ? __uint_as_float(__float_as_uint(v) & 0xFFFF0000u) : v;
+        float a = finite ? __uint_as_float(__float_as_uint(v) & 0xFFFF0000u) : v;
+        if (a == 0.0f && v != 0.0f) a = copysignf(0x1p-133f, v);
         const float b = finite ? v - a : 0.0f, b1 = __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
         ((__bf16 *)block)[at] = (__bf16)a;
         ((__bf16 *)block)[256 + at] = (__bf16)b1;
@@ -223,7 +227,7 @@ __device__ __forceinline__ void shrink_tile(const LayerCall &c, int32_t K, int64
 }
 
 // Two 16-bit numbers with infinities and NaN as 0: those meet h in its first part
-// alone (its other parts may be 0).
+// alone (its other parts may be 0 where h is not).
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w, uint32_t exponent, uint32_t one)
 {
     const uint32_t bad = ((w & exponent) + one) & 0x80008000u;      // (both halves: the exponent's last value carries)
