@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import more_digits as digits
 import wfst_beam_search_amd as wb
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,18 @@ def test_an_infinite_weight_meets_a_small_h(M, N, a, big, small):
     assert (y[:, 0::4] == 0).all() and (y[:, 1::4] == INF).all() and (y[:, 2::4] == -INF).all()
     lost = {"f32": 0.0, "f16": 2.0 ** -50 * big, "bf16": 2.0 ** -126}[a]
     assert ((y[:, 3::4] - 3 * small).abs() <= 3 * lost + 3 * E * 3 * small + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("M,N", PATHS)
+@pytest.mark.parametrize("x,a", [("f32", "f32"), ("f32", "f16"), ("f16", "f16"), ("f32", "bf16"), ("bf16", "bf16"),
+                                 ("bf16", "f32"), ("f16", "bf16")])
+def test_h_keeps_its_binary32_digits(M, N, x, a):
+    K, rank = 70, 40
+    layer = _silent_layer(K, N)
+    xs, down, up = digits.inputs(M + N, M, K, rank, N, x, a)
+    ad = wb.Adapters(layer, 2, rank, dtype=a)
+    ad.load(1, down.cuda(), up.cuda(), scale=digits.SCALE)
+    y = layer.logits(xs.cuda(), adapters=ad, ids=np.ones(M, np.int32)).double().cpu().numpy()
+    want = digits.exact(xs, up)[1]
+    bad = digits.wrong(y, want)
+    assert not bad.any(), (np.argwhere(bad)[:4], y[bad][:4], want[bad][:4])
