@@ -6,6 +6,7 @@ import torch
 
 import more_digits as digits
 import wfst_beam_search_amd as wb
+from test_gpu_token_scores import _check as check_scores
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,22 @@ def test_h_keeps_its_binary32_digits(M, N, x, a):
     want = digits.exact(xs, up)[1]
     bad = digits.wrong(y, want)
     assert not bad.any(), (np.argwhere(bad)[:4], y[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("V", [2, 30, 500, 3000, 6007, 30011])
+@pytest.mark.parametrize("T", [2.0 ** -149, 3 * 2.0 ** -149, 2.0 ** -140, 2.0 ** -127, 2.0 ** -126, 1.5 * 2.0 ** -126, 2.0 ** -125])
+def test_temperatures_of_the_smallest_numbers(V, T):
+    """Scores as close to each other as such a temperature tells apart, far ones and large ones beside them."""
+    rng = np.random.default_rng(V)
+    x = np.zeros((7, V), np.float32)
+    for r, steps in enumerate((1.0, 0.3, 4.0)):         # multiples of T, rounded to the numbers there are
+        x[r] = -np.abs(rng.normal(size=V)) * steps * T
+    x[2, ::3] = -1.0
+    x[3] = np.float32(2.0 ** -130) - x[0]
+    x[4] = rng.normal(size=V)
+    x[5] = rng.choice(np.array([3e38, 2.9e38, 1.0, -3e38], np.float32), V)
+    x[6] = rng.choice(np.array([-3e38, -3.1e38, -np.inf], np.float32), V)
+    s = torch.from_numpy(x).cuda()
+    tok = torch.from_numpy(rng.integers(0, V, (7, 4)).astype(np.int32)).cuda()
+    check_scores(wb.token_scores(s, tok, top_n=5, temperature=T), s, tok, 5, T)
+    check_scores(wb.token_scores(s, tok, top_n=5, temperature=torch.full((7,), T, device="cuda")), s, tok, 5, T)

@@ -169,7 +169,7 @@ struct TokenCall {
     int32_t C, top_n;
     float temperature;
     const float *temperatures;  // one a row, or null
-    float scale;                // log2 e / temperature (set by the launch)
+    float unit, scale;          // a power of two and log2 e / (unit temperature) (set by the launch)
     float *log_probs;           // [rows, C]
     int32_t *ranks;             // [rows, C]
     float *entropies;           // [rows] or null

@@ -44,28 +44,32 @@ __device__ __forceinline__ float key_score(uint32_t u) { return __uint_as_float(
 __device__ __forceinline__ int count(bool b) { return __popcll(__ballot(b)); }
 
 // What a row's temperature makes of its distances. Where z - m could pass binary32's
-// range, half of it is taken times 2 / T. T below 2^-125 counts as that for the sums.
+// range, half of it is taken times 2 / T; where 1 / T could, unit = 2^24 times it and 1 / (unit T).
 constexpr float kLog2e = 1.44269504088896341f;
 
-struct Heat { float t, scale; };
+struct Heat { float t, unit, scale; };
+
+__host__ __device__ __forceinline__ Heat heat_of(float t)
+{
+    const float unit = t < 0x1p-125f ? 0x1p24f : 1.0f, d = t * unit;
+    return {t, unit, kLog2e / (d < 0x1p-125f ? 0x1p-125f : d)};        // (T = 0: of no use, but finite)
+}
 
 __device__ __forceinline__ Heat row_heat(const TokenCall &c, int64_t r)
 {
-    float t = c.temperature, scale = c.scale;
-    if (c.temperatures) {
-        t = c.temperatures[r];
-        t = t > 0.0f ? fminf(t, 3.402823466e38f) : 0.0f;
-        scale = kLog2e / fmaxf(t, 0x1p-125f);
-    }
-    return {t, scale};
+    if (!c.temperatures) return {c.temperature, c.unit, c.scale};
+    const float t = c.temperatures[r];
+    return heat_of(t > 0.0f ? fminf(t, 3.402823466e38f) : 0.0f);
 }
 
-struct Base { float half, mh, scale; };        // y = (z half - mh) scale
+struct Base { float half, mh, scale; };        // y = (z half - mh) scale, half a power of two
 
 __device__ __forceinline__ Base base_of(float m, const Heat &h)
 {
-    const float half = m > 0x1p100f ? 0.5f : 1.0f;
-    return {half, m * half, m > 0x1p100f ? 2.0f * h.scale : h.scale};
+    // (far out distances are 0 or 2^76 and more, whose exponentials are 0 at any T that has a unit)
+    const bool far = fabsf(m) > 0x1p100f;
+    const float half = far ? 0.5f : h.unit;
+    return {half, m * half, far ? 2.0f * h.scale : h.scale};
 }
 
 __device__ __forceinline__ float below(float z, const Base &b) { return fmaf(z, b.half, -b.mh) * b.scale; }
@@ -837,7 +841,9 @@ size_t token_workspace(int64_t rows, int32_t V, int32_t C, int32_t top_n, int32_
 hipError_t launch_token_scores(const TokenCall &call, hipStream_t s)
 {
     TokenCall c = call;
-    c.scale = kLog2e / std::max(c.temperature, 0x1p-125f);
+    const Heat h = heat_of(c.temperature);
+    c.unit = h.unit;
+    c.scale = h.scale;
     if (c.x_dtype == kF32) return token_launch<float>(c, s);
     if (c.x_dtype == kF16) return token_launch<_Float16>(c, s);
     return token_launch<__bf16>(c, s);
