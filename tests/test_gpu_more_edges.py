@@ -80,3 +80,16 @@ def test_temperatures_of_the_smallest_numbers(V, T):
     tok = torch.from_numpy(rng.integers(0, V, (7, 4)).astype(np.int32)).cuda()
     check_scores(wb.token_scores(s, tok, top_n=5, temperature=T), s, tok, 5, T)
     check_scores(wb.token_scores(s, tok, top_n=5, temperature=torch.full((7,), T, device="cuda")), s, tok, 5, T)
+
+
+def test_emptying_a_slot_ignores_the_matrices():
+    """Rank 0 with pointers that are no matrices, as the header allows; with a rank they are refused."""
+    lib = wb.load_library()
+    layer = _silent_layer(32, 8)
+    ad = wb.Adapters(layer, 2, 4, dtype="f32")
+    ad.load(1, torch.eye(4, 32, device="cuda"), torch.ones(8, 4, device="cuda"))
+    h = torch.ones(3, 32, device="cuda")
+    assert (layer.logits(h, adapters=ad, ids=[1, 1, 1]) == 4).all()
+    assert lib.wfst_adapters_load(ad.handle, 1, 1, 2, 32, 3, 4, 1.0, None) == -1
+    assert lib.wfst_adapters_load(ad.handle, 1, 0, 2, -5, 3, 0, 1.0, None) == 0
+    assert (layer.logits(h, adapters=ad, ids=[1, 1, 1]) == 0).all()

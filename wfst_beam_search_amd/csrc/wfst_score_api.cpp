@@ -485,10 +485,12 @@ extern "C" int wfst_adapters_load(wfst_adapters_t adapters, int32_t slot, int32_
         if (db < 0 || ub < 0) return api_fail(WFST_EINVAL, "a tensor is too large");
         DeviceScope scope;
         HIP_TRY(scope.enter(adapters->device));
-        TRY(check_aligned(down, es, "down"));
-        TRY(check_aligned(up, es, "up"));
-        TRY(api_check_buffer(down, (size_t)db, adapters->device, "down"));
-        TRY(api_check_buffer(up, (size_t)ub, adapters->device, "up"));
+        if (rank) {
+            TRY(check_aligned(down, es, "down"));
+            TRY(check_aligned(up, es, "up"));
+            TRY(api_check_buffer(down, (size_t)db, adapters->device, "down"));
+            TRY(api_check_buffer(up, (size_t)ub, adapters->device, "up"));
+        }
         TRY(check_stream(stream, adapters->device));
         HIP_TRY(launch_adapter_load(a, slot, {down, up, down_stride, up_stride, rank, scale}, (hipStream_t)stream));
         return WFST_OK;
