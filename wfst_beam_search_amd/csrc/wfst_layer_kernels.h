@@ -169,7 +169,7 @@ __global__ __launch_bounds__(kLayerThreads, AD && SPL == 1 ? 4 : 1) void k_layer
     const int part = KS * kc * 16 * RP;
     float *xf = (float *)(xs + P * part);                               // [KS * kc][RP]
     char *hs = (char *)(xf + KS * kc * RP) + (16 - KS * kc * RP * 4 % 16) % 16;            // (AD: blocks of h)
-    float4_t *joint = (float4_t *)(smem);                               // (KS = 4, after the last use of xs)
+    float4_t *joint = (float4_t *)(smem);                               // (KS = 4, after the last use of xs and hs)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int m0 = blockIdx.y * kRowsM, M = min(kRowsM, c.M - m0);
     const int nt = min((int)(KS == 1 ? blockIdx.x * kLayerWaves + wave : blockIdx.x), l.nt - 1);
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kLayerThreads, AD && SPL == 1 ? 4 : 1) void k_layer
                 for (int j = 0; j < 4; ++j) {
                     if (j && j % (4 / GPT) == 0) z = zero_pair((ts.z >> (8 * (j * GPT / 4))) & 255u);
                     const half8_t q = unpack_word(w[j], magic, z);
-const int at = (u * 16 + j * 4 + quad) * RP + arow;
+                    const int at = (u * 16 + j * 4 + quad) * RP + arow;
                     sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[at], q, sum, 0, 0, 0);
                     if constexpr (kLow) low = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[part + at], q, low, 0, 0, 0);
                     else if constexpr (P == 2)
@@ -621,9 +621,9 @@ hipError_t few_launch(const Layer &l, const LayerCall &call, int RP, hipStream_t
     const int longest = (l.kb + KS - 1) / KS;
     const size_t per = (size_t)KS * RP * (256 * kParts<XT> + 4);
     const int kc = std::min<int>(longest, std::max<int>(D, (int)(40960 / per) / D * D));
-    // (h lies behind x, and with KS > 1 behind what the wavefronts join)
-    const size_t own = (per * kc + 15) / 16 * 16, join = KS > 1 ? (KS - 1) * 64 * sizeof(float4_t) : 0;
-    const size_t lds = AD ? own + (size_t)c.ad.a.rb * h_block_bytes(c.ad.a.dtype) + join : std::max<size_t>(per * kc, join);
+    // (x and behind it h; what the wavefronts join takes their place once both are done with)
+    const size_t h = AD ? (size_t)c.ad.a.rb * h_block_bytes(c.ad.a.dtype) : 0;
+    const size_t lds = std::max<size_t>((per * kc + 15) / 16 * 16 + h, KS > 1 ? (KS - 1) * 64 * sizeof(float4_t) : 0);
     const dim3 g(KS > 1 ? l.nt : (l.nt + kLayerWaves - 1) / kLayerWaves, (c.M + kRowsM - 1) / kRowsM);
     hipLaunchKernelGGL((k_layer_few<XT, WS, GPT, KS, SPL, AD>), g, dim3(kLayerThreads), lds, s, l, c, RP, kc);
     return hipGetLastError();
