@@ -6,6 +6,7 @@ import torch
 
 import more_digits as digits
 import wfst_beam_search_amd as wb
+import test_gpu_adapters as adapters
 from test_gpu_token_scores import _check as check_scores
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,38 @@ def test_emptying_a_slot_ignores_the_matrices():
     assert lib.wfst_adapters_load(ad.handle, 1, 1, 2, 32, 3, 4, 1.0, None) == -1
     assert lib.wfst_adapters_load(ad.handle, 1, 0, 2, -5, 3, 0, 1.0, None) == 0
     assert (layer.logits(h, adapters=ad, ids=[1, 1, 1]) == 0).all()
+
+
+@pytest.mark.parametrize("V,x", [(600011, "f32"), ((1 << 20) + 9, "bf16"), (524289, "f16")])
+def test_many_tokens_of_rows_whose_pieces_take_several_runs(V, x):
+    g = torch.Generator(device="cuda").manual_seed(V)
+    t = (torch.randn(3, V, generator=g, device="cuda") * 3).to(DT[x])
+    t[1, ::2] = -INF
+    for C in (65, 200, 256):
+        tok = torch.randint(-1, V + 1, (3, C), generator=g, device="cuda", dtype=torch.int32)
+        tok[:, 64] = t.float().argmax(-1).int()
+        for n in (0, 40):
+            check_scores(wb.token_scores(t, tok, top_n=n), t, tok, n)
+
+
+@pytest.mark.parametrize("N", [333, 5000, 17000])
+@pytest.mark.parametrize("x,a", [("f16", "f16"), ("bf16", "f32"), ("f32", "bf16")])
+def test_ids_of_each_frame_past_512_rows(N, x, a):
+    """ids [B, T] of a padded batch, other slots beside each other, runs, repeats, none."""
+    B, T, K = 6, 151, 260
+    layer, arrays = adapters._layer(N, K, N)
+    ranks = [40, 3, 0, 16, 17, 1, 33, 48, 8]
+    ad = wb.Adapters(layer, len(ranks), 48, dtype=a)
+    held = adapters._fill(ad, layer, N, ranks, a)
+    rng = np.random.default_rng(N)
+    h = torch.from_numpy(rng.normal(size=(B, T, K)).astype(np.float32)).to(DT[x]).cuda()
+    ids = rng.integers(-1, len(ranks), (B, T)).astype(np.int32)
+    ids[1] = np.arange(T) // 20 % len(ranks)
+    ids[2, :40] = 7
+    lens = np.array([T, T - 3, 100, T, 7, T], np.int32)
+    L = torch.from_numpy(lens).cuda()
+    act = torch.arange(T, device="cuda")[None] < L[:, None]
+    h[~act] = float("nan")
+    y = layer.logits(h, lengths=L, adapters=ad, ids=torch.from_numpy(ids).cuda())
+    adapters._check(y[act], h[act], arrays, ids[act.cpu().numpy()], held)
+    assert torch.equal(layer.logits(h, lengths=lens, adapters=ad, ids=ids)[act], y[act])
