@@ -17,9 +17,10 @@ namespace {
 // of 8 bits; with up in binary16 as hi + lo / 2^11, two binary16 values scaled by a
 // power of two per row and 16 ranks (off by at most 2^-23 of itself or 2^-50 of the
 // largest of those 16). 16000 rows x 5000 x 1024 of binary16, one slot of rank 16, 32, 128, us
-// for the whole call: 406, 420, 562, without a slot 363; 64 rows x 32003 x 2050 over 64 slots
-// of rank 16, 32: 72, 106 in binary32 (up alone 131, 262 MB: 4.6, 4.2 TB/s of the time that the
-// layer does not take), 69, 83 in bfloat16; without a slot 48.
+// for the whole call: 399, 415, 554, without a slot 357, the layer alone 318; 64 rows x 32003 x
+// 2050 of binary32 over 64 slots of rank 16, 32: 72, 107 in binary32 (up is 131, 262 MB, of which
+// repeated calls find a part in the last cache), 65, 79 in bfloat16; without a slot 48, the layer
+// alone 45.
 
 constexpr int kRowsTile = 16;
 

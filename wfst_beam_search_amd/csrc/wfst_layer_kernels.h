@@ -155,7 +155,11 @@ __device__ __forceinline__ void store_y(const LayerCall &c, int64_t m, int n, fl
 // takes one run of 8 features a thread) leaves registers for 4 wavefronts a SIMD (118
 // of bfloat16): one row x 131072 x 4096 takes 59 us with 3 tiles ahead (62, 61, 71
 // with 4, 2, 6), where the general staging's (174) leave 2 and it takes 74; 278 MB at
-// 4.7 TB/s, 92 % of what a large copy moves on this card.
+// 4.7 TB/s, 92 % of what a large copy moves on this card. With adapters the compiler is held
+// to those 4 wavefronts (AD): 16-bit rows fit, binary32 rows, which take 136 to 148 registers
+// without adapters, spill 15 to 26 there. One such row x 131072 x 4096 with an adapter of rank
+// 16 so / unbound, us: groups of 128 93 / 81 (16-bit scales), 86 / 79 (binary32 ones), of 64
+// 92 / 88, 94 / 88, of 32 103 / 98, 105 / 100; without an adapter 77, 68, 79, 78, 88, 87.
 template <int KS, int SPL> constexpr int kTilesAhead = KS == 1 ? (SPL == 1 ? 3 : 4) : 2;
 
 template <typename XT, int WS, int GPT, int KS, int SPL, bool AD>
@@ -581,7 +585,9 @@ __global__ __launch_bounds__(512, AD && !kScaled<XT> && GPT == 1 ? 4 : 1) void k
 // 16 and more with the same slot, then each with another one: 256 rows 27 / 24, 42 / 93; 512 41
 // / 36, 69 / 118; 1024 60 / 47, 103 / 144; 4096 171 / 120, 317 / 317 (rank 64: 512 64 / 43, 180 /
 // 258; 1024 107 / 57, 278 / 328). The rule goes by the number of rows alone, so that a row's
-// result does not depend on how its id is given; batches of single rows past 512 lose by it.
+// result does not depend on how its id is given. It is a border between the two kinds, not the
+// better side of each: up to 512 rows in runs lose by it what tiles would save (rank 64: a third),
+// single rows past it what row by row would (1024: 40 %; at 4096 nothing).
 bool shrink_tiles(const LayerCall &c) { return c.M > 512; }
 
 template <typename XT, typename AT>

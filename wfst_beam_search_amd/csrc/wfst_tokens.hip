@@ -750,8 +750,13 @@ __global__ __launch_bounds__(kTokenThreads) void k_token_join(TokenCall c, int32
 // labels on 1 / 2 wavefronts 23 / 30, 32 / 41, 41 / 48, 129 / 74; 5000 on 2 / 4 46 / 55, 60 /
 // 79, 72 / 92, 147 / 117 (binary32 68 / 81, 83 / 107, 97 / 120, 155 / 148), 3000 82 / 129 with
 // 64: many alternatives take more wavefronts where a thread holds many labels. Fewer rows
-// than fill the card take about as long either way. Pieces of 8192 labels, or of 2048 and
-// more of them: one row of 131072 18 / 19 us, 64 rows 21 / 34.
+// than fill the card take about as long either way. Pieces of 8192 labels, or of 2048 and more of
+// them, us, without tokens and alternatives, with one token and 20, with 16 and 64, binary32:
+// 131072 labels, 1 row 13 / 14, 17 / 19, 30 / 34; 16 rows 13 / 13, 18 / 22, 32 / 38; 64 rows 13 /
+// 15, 21 / 34, 41 / 64; 256 rows 27 / 36, 46 / 83, 105 / 164. 32003 labels, 1 row 12 / 12, 16 / 15, 27
+// / 23; 48 rows 13 / 13, 17 / 17, 28 / 26; 256 rows 13 / 15, 21 / 30, 38 / 54. 16384 labels, 1 to 64
+// rows 13 / 14, 16 / 17, 26 to 28 / 21 to 22. So short pieces pay for a few rows with many given
+// tokens alone (up to 7 us), and the rule does not look at either.
 struct TokenShape { int waves, nv, pieces, subs; };
 
 TokenShape token_shape(int32_t V, int32_t top_n, int32_t x_dtype)
@@ -771,7 +776,11 @@ TokenShape token_shape(int32_t V, int32_t top_n, int32_t x_dtype)
 }
 
 // u64 of a row's list in LDS: the labels that may reach the bound, 8 zeros, and twice
-// the n best so far.
+// the n best so far. Room for the worst case (all of bound_cap(n) threads' labels), where about
+// n are listed. It takes workgroups off a CU that the registers leave room for in three cases: 3
+// instead of 4 with 31 or 32 alternatives of the longest rows of one wavefront (41 to 43 KiB), 5
+// instead of 7 with 64 of 1000 16-bit labels (32 KiB), 7 instead of 8 with 64 of two wavefronts'
+// rows (23 KiB).
 int token_list(const TokenCall &c, int nv, int vec, bool cut)
 {
     return c.top_n ? (std::min(bound_cap(c.top_n) * nv * vec, c.V) + 8 + (cut ? 2 * c.top_n : 0) + 1) / 2 * 2 : 0;

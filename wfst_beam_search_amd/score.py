@@ -10,7 +10,9 @@ tensor that needs one (backward, or a forward-mode dual) is refused.
 Every call is asynchronous on ``stream`` (a ``torch.cuda.Stream`` or a raw
 handle; default: the current stream of the operands' device; new tensors then
 belong to that stream) and may be captured into a HIP graph when its ``lengths``
-is a device tensor. Tensors may have any
+and ``ids`` are device tensors. Operands that belong to another stream than the
+call's have to be kept until that one has passed it (memory that is freed before goes
+to its own stream's next tensor). Tensors may have any
 leading dimensions whose rows lie a constant distance apart. ``lengths`` (int32
 [B], for tensors [B, T, ...]; a device tensor, or host values that are copied
 first) marks the rows t >= lengths[b] as empty: they are not read, and in ``out``
@@ -403,7 +405,8 @@ class Adapters:
 
     def load(self, slot: int, down, up, scale: float = 1.0, stream=None):
         """Fill ``slot`` with a copy of ``down`` [r, K] and ``up`` [N, r]. Ordered on ``stream`` like
-        every call; the other slots may be in use meanwhile."""
+        every call, and the matrices are kept as its operands are; the other slots may be in use
+        meanwhile."""
         if self.handle is None:
             raise ValueError("the adapters were released")
         for t, name in ((down, "down"), (up, "up")):
@@ -414,7 +417,7 @@ class Adapters:
         if r < 1 or down.shape[1] != self.in_features or tuple(up.shape) != (self.out_features, r):
             raise ValueError(f"down must be [r, {self.in_features}] and up [{self.out_features}, r]")
         dstep, ustep = _rows(down, "down")[1], _rows(up, "up")[1]
-        raw, other = _stream(stream, self.device)
+        raw, _ = _stream(stream, self.device)
         _check(load_library().wfst_adapters_load(self.handle, _int32(slot, "slot"), r, down.data_ptr(), dstep,
                                                  up.data_ptr(), ustep, float(scale), raw))
 
